@@ -404,6 +404,207 @@ int moe_layer_forward_static(const MoeLayerDesc *desc, const float *Wr, const fl
  */
 int moe_layer_static_status(cudaStream_t stream, int *status_out);
 
+/* ------------------------------------------------------------------------
+ * The attention half of a decode step.  The pages describe the engine's own
+ * attention only in words; the calls below are general operators on a paged
+ * key-value cache, to run next to the MoE layer:
+ *   moe_kv_plan      pages, positions and cache slots of a batch's new tokens
+ *   moe_rope_append  rotary positions, keys and values into the cache
+ *   moe_attn_decode  attention of one new token per request over the cache
+ *   moe_block_norm   gated residual update with the norms around it
+ * All four follow the conventions at the top of this file.  Strides are in
+ * elements.  Infinities and NaN are allowed where nothing is read from (cache
+ * slots beyond a request's length, table entries beyond its pages).
+ * ------------------------------------------------------------------------ */
+
+/* Element types. */
+#define MOE_F32 0
+#define MOE_F16 1
+#define MOE_BF16 2
+#define MOE_E4M3 3 /* FP8 E4M3, "fn" variant; a stored code c stands for c * scale */
+
+/* Flags in info[2] of moe_kv_plan. */
+#define MOE_PLAN_NO_PAGES 1  /* the free list ran out */
+#define MOE_PLAN_ROW_FULL 2  /* a request needs more pages than a table row holds */
+#define MOE_PLAN_NO_ROOM 4   /* more new tokens than max_new_tokens */
+#define MOE_PLAN_NEGATIVE 8  /* a negative length (taken as 0) or list head */
+
+/* Largest batch of moe_kv_plan and moe_attn_create. */
+#define MOE_MAX_REQUESTS 8192
+
+/*
+ * Page allocation, positions and cache slots of the tokens that a batch of
+ * requests brings, computed on the GPU from the lengths.
+ *   past_len, new_len [n_requests] int32: tokens in the cache, tokens to come
+ *   free_pages [n_free] int32: page ids to hand out, from entry *free_head on
+ *   free_head  [1] int32
+ *   block_table [n_requests] rows of max_pages int32, table_stride apart:
+ *     entry j of a row is the page of tokens [j * page_size, (j+1) *
+ *     page_size).  The entries of the pages held for past_len are read, those
+ *     of the new pages written, in request order; all others stay as they are.
+ *   q_start   [n_requests + 1] int32 out: first new token of each request
+ *   seq_len   [n_requests] int32 out: past_len + new_len
+ *   positions [max_new_tokens] int32 out: each new token's position in its
+ *     request (0 beyond the last)
+ *   slots     [max_new_tokens] int64 out: page * page_size + offset, or -1:
+ *     beyond the last token, or where no page could be had
+ *   info      [4] int32 out: new tokens, free_head after the call, MOE_PLAN_*
+ *     flags (0: all well), largest seq_len
+ * A request that gets no page has -1 in its table row from there on, and the
+ * list head stops at n_free.  Nothing but the outputs is changed: a second
+ * call on the same inputs gives the same outputs (to go on, copy info[1] to
+ * *free_head).  No output may overlap an input (block_table is both).  The
+ * lengths' sums stay below 2^31.
+ * 0 <= n_requests <= MOE_MAX_REQUESTS, 1 <= page_size <= 65536.
+ * Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+int moe_kv_plan(const int32_t *past_len, const int32_t *new_len, int n_requests, const int32_t *free_pages,
+                int n_free, const int32_t *free_head, int page_size, int32_t *block_table, int64_t table_stride,
+                int max_pages, int max_new_tokens, int32_t *q_start, int32_t *seq_len, int32_t *positions,
+                int64_t *slots, int32_t *info, cudaStream_t stream);
+
+/* Scalings of the rotary frequencies for long contexts (MoeRopeDesc). */
+#define MOE_ROPE_NONE 0
+#define MOE_ROPE_LINEAR 1 /* every frequency divided by factor */
+#define MOE_ROPE_NTK 2    /* base * factor^(rot_dim / (rot_dim - 2)) */
+#define MOE_ROPE_PARTS 3  /* by parts: pairs that turn more than beta_fast times
+                           * in original_len positions keep their frequency, those
+                           * below beta_slow turns are divided by factor, linear
+                           * between; amplitude 0.1 ln(factor) + 1 (YaRN, Peng et
+                           * al. 2023) */
+
+typedef struct {
+    int rot_dim;        /* rotated dimensions of a head; even, 2..512 */
+    double base;        /* frequency of pair i: base^(-2 i / rot_dim); > 0 */
+    int scaling;        /* MOE_ROPE_* */
+    double factor;      /* >= 1 (LINEAR, NTK, PARTS) */
+    int original_len;   /* context length before scaling (PARTS), >= 1 */
+    double beta_fast, beta_slow; /* PARTS: turns, beta_fast > beta_slow */
+} MoeRopeDesc;
+
+/*
+ * Host: the turns per position of each pair, theta_i / (2 pi), as fractions
+ * of 2^64 (whole turns drop out), and the factor on cos and sin.  The caller
+ * copies turns_host to the device once and passes it to moe_rope_append.
+ *   turns_host [rot_dim / 2] uint64 out;  amplitude_host [1] float out
+ * Errors: INVALID_ARG, SHAPE.
+ */
+int moe_rope_turns(const MoeRopeDesc *desc, uint64_t *turns_host, float *amplitude_host);
+
+/* Arguments of moe_rope_append (host struct; pointers inside are device
+ * pointers).  A row of a head is contiguous; token and head strides are free. */
+typedef struct {
+    int n_tokens, n_heads, n_kv_heads;
+    int head_dim;                /* of q and k; <= 512 */
+    int v_dim;                   /* of v; 0: no v (v, v_cache unused) */
+    int rot_dim, rot_offset;     /* dimensions [rot_offset, rot_offset + rot_dim) turn */
+    int interleaved;             /* pairs (2i, 2i+1); else (i, i + rot_dim / 2) */
+    int act_type, cache_type;    /* MOE_F32 / F16 / BF16; MOE_F16 / BF16 / E4M3 */
+    int page_size;
+    const uint64_t *turns;       /* [rot_dim / 2] of moe_rope_turns, on the device */
+    float amplitude;
+    float k_scale, v_scale;      /* > 0; E4M3 caches hold x / scale, rounded to nearest, saturated */
+    const int32_t *positions;    /* [n_tokens] */
+    const int64_t *slots;        /* [n_tokens]; < 0 or >= n_pages * page_size: not cached */
+    int64_t n_pages;
+    const void *q, *k, *v;       /* [n_tokens, heads, dim] */
+    void *q_out;                 /* [n_tokens, n_heads, head_dim]; may be q */
+    void *k_cache, *v_cache;     /* slot s: page s / page_size, token s % page_size */
+    int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+    int64_t qo_stride_t, qo_stride_h;
+    int64_t kc_stride_page, kc_stride_tok, kc_stride_head;
+    int64_t vc_stride_page, vc_stride_tok, vc_stride_head;
+} MoeRopeArgs;
+
+/*
+ * Rotary positions on q and k, and k and v into the paged cache.
+ *   (a, b) -> amplitude * (a cos - b sin, a sin + b cos), the angle position *
+ *   theta_i reduced to a part of a turn in 64-bit integers (no error but that
+ *   of theta_i, 2^-53 of it, times the position), the rest in 32 bits, one
+ *   rounding to the output type.
+ * Distinct tokens have distinct slots.  q, k, v may be views of one buffer.
+ * Any alignment; fastest when every row starts on 16 bytes.
+ * Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+int moe_rope_append(const MoeRopeArgs *args, cudaStream_t stream);
+
+/* Sizes of an attention handle. */
+typedef struct {
+    int max_requests;        /* 1..MOE_MAX_REQUESTS */
+    int n_heads, n_kv_heads; /* n_heads a multiple of n_kv_heads; query head h
+                              * reads key head h / (n_heads / n_kv_heads) */
+    int k_dim, v_dim;        /* multiples of 8 (of 16 for E4M3 caches), 8..256 */
+} MoeAttnDesc;
+
+/*
+ * Create / destroy an attention handle: the workspace that a forward splits
+ * long requests over and joins them in.  It owns that device memory (about 5
+ * MiB at 128 dimensions, and 4 bytes for each request and group of 8 query
+ * heads) and serves one stream at a time, on the device current at create.
+ * Destroying NULL is accepted.  Errors: INVALID_ARG, SHAPE, NOMEM, CUDA.
+ */
+int moe_attn_create(const MoeAttnDesc *desc, void **handle_out);
+int moe_attn_destroy(void *handle);
+
+/* Arguments of moe_attn_decode (host struct; pointers are device pointers). */
+typedef struct {
+    int n_requests;
+    int act_type, cache_type;    /* q and out: MOE_F32 / F16 / BF16; cache: MOE_F16 / BF16 / E4M3 */
+    int page_size;               /* 1..65536 */
+    int max_pages;               /* entries of a table row */
+    int window;                  /* > 0: only the last `window` tokens are seen; 0: all */
+    float scale;                 /* on q . k */
+    float k_scale, v_scale;      /* on E4M3 codes */
+    const int32_t *seq_len;      /* [n_requests]; longer than the table row: cut to it */
+    const int32_t *block_table;  /* rows table_stride apart */
+    int64_t table_stride;
+    int64_t n_pages;             /* pages of the caches; tokens on other page ids are not seen */
+    const void *q;               /* [n_requests, n_heads, k_dim] */
+    const void *k_cache, *v_cache; /* 16-byte aligned; strides multiples of 16 bytes */
+    void *out;                   /* [n_requests, n_heads, v_dim] */
+    float *lse;                  /* [n_requests, n_heads] contiguous, or NULL */
+    int64_t q_stride_b, q_stride_h, out_stride_b, out_stride_h;
+    int64_t kc_stride_page, kc_stride_tok, kc_stride_head;
+    int64_t vc_stride_page, vc_stride_tok, vc_stride_head;
+} MoeAttnArgs;
+
+/*
+ * Attention of one new token per request over the paged cache.
+ *   s_j = scale * k_scale * (q . k_j) over the request's tokens j in
+ *   [max(0, seq_len - window), seq_len);  out = v_scale * sum softmax(s)_j v_j;
+ *   lse = ln sum exp(s_j).
+ * A request that sees no token (seq_len <= 0) gets out = 0 and lse = -inf.
+ * Logits, softmax statistics and sums are held in 32 bits.  The result does
+ * not depend on which block finishes first.  May be captured in a CUDA graph.
+ * Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+int moe_attn_decode(void *handle, const MoeAttnArgs *args, cudaStream_t stream);
+
+/* Arguments of moe_block_norm (host struct; pointers are device pointers). */
+typedef struct {
+    int n_tokens, dim;         /* dim 1..16384 */
+    int act_type;              /* of x, y, gate, out, normed: MOE_F32 / F16 / BF16 */
+    int gate_sigmoid;          /* 1: the gate enters as sigmoid(gate); 0: as it is */
+    float alpha, beta, eps;    /* eps >= 0 */
+    const void *x, *y;         /* residual stream and block output; y NULL: r = alpha x */
+    const float *w_post, *w_pre; /* [dim]; w_post NULL: no norm after the block */
+    const void *gate;          /* or NULL; element (t, d) at t * gate_stride_t + d * gate_stride_d */
+    void *out, *normed;        /* out may be x; normed NULL: no norm before the next block */
+    int64_t x_stride, y_stride, out_stride, normed_stride; /* between tokens */
+    int64_t gate_stride_t, gate_stride_d;                  /* gate_stride_d 0 or 1 */
+} MoeNormArgs;
+
+/*
+ * The join between two blocks of a layer in one pass:
+ *   u = y * rsqrt(mean(y^2) + eps) * w_post     (w_post NULL: u = y)
+ *   out = r = alpha * x + beta * act(gate) * u
+ *   normed = r * rsqrt(mean(r^2) + eps) * w_pre (w_pre NULL: weight 1)
+ * in 32 bits, each output rounded once (the second norm takes the unrounded
+ * r).  Rows are contiguous; out may alias x, normed may alias y.
+ * Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+int moe_block_norm(const MoeNormArgs *args, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

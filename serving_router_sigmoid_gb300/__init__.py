@@ -334,3 +334,7 @@ def static_status(stream=None) -> int:
     if rc not in (MOE_OK, MOE_ERR_DEVICE):
         _check(rc)
     return int(v.value)
+
+
+from ._paged import (MOE_PLAN_NEGATIVE, MOE_PLAN_NO_PAGES, MOE_PLAN_NO_ROOM, MOE_PLAN_ROW_FULL,  # noqa: E402,F401
+                     KvPlan, PagedAttention, Rope, block_norm)

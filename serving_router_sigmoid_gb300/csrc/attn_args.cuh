@@ -1,0 +1,150 @@
+// attn_args.cuh -- argument checks, launchers and element conversions shared
+// by the paged-cache operators (plan, rotary append, attention, block norm).
+// Internal.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+// Unsigned division by a host-known divisor as a multiplication: for n < 2^31
+// and 1 <= d < 2^31, n / d = (n * mul) >> (32 + shift) with
+// shift = ceil(log2 d) - 1 and mul = ceil(2^(32 + shift) / d) (Granlund and
+// Montgomery 1994); d = 1 is flagged by mul = 0.
+struct FastDiv {
+    uint32_t mul, shift, d;
+    __host__ __device__ FastDiv() : mul(0), shift(0), d(1) {}
+    explicit FastDiv(uint32_t div) : mul(0), shift(0), d(div) {
+        if (div <= 1) return;
+        uint32_t l = 0;
+        while ((1ull << l) < div) ++l;
+        shift = l - 1;
+        mul = (uint32_t)(((1ull << (32 + shift)) + div - 1) / div);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return mul ? __umulhi(n, mul) >> shift : n; }
+};
+
+inline size_t dtype_bytes(int t) { return t == MOE_F32 ? 4 : t == MOE_E4M3 ? 1 : 2; }
+
+// Element types as C++ types.
+template <int DT> struct Elem;
+template <> struct Elem<MOE_F32> { using type = float; };
+template <> struct Elem<MOE_F16> { using type = __half; };
+template <> struct Elem<MOE_BF16> { using type = __nv_bfloat16; };
+template <> struct Elem<MOE_E4M3> { using type = uint8_t; };
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f32(float v, float &o) { o = v; }
+__device__ __forceinline__ void from_f32(float v, __half &o) { o = __float2half_rn(v); }
+__device__ __forceinline__ void from_f32(float v, __nv_bfloat16 &o) { o = __float2bfloat16_rn(v); }
+
+// Two e4m3 codes of the low 16 bits -> two f16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("{ .reg .b16 c; cvt.u16.u32 c, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(r) : "r"(codes));
+    return r;
+}
+// lo, hi -> two e4m3 codes (nearest, ties to even, saturating), lo in the low byte.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+    uint32_t r;
+    asm("{ .reg .b16 c; cvt.rn.satfinite.e4m3x2.f32 c, %2, %1; cvt.u32.u16 %0, c; }" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+// N consecutive elements <-> fp32 registers, in vector accesses of up to 16
+// bytes (the caller guarantees the alignment of N elements, at most 16 bytes).
+template <int N>
+__device__ __forceinline__ void load_vec(const float *p, float (&v)[N]) {
+    static_assert(N % 4 == 0, "");
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(p + i);
+        v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
+    }
+}
+__device__ __forceinline__ float2 half_pair(uint32_t w, __half) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+__device__ __forceinline__ float2 half_pair(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi, __half) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <int N, typename H>
+__device__ __forceinline__ void load_vec(const H *p, float (&v)[N]) {
+    static_assert(N % 8 == 0, "");
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(p + i);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = half_pair(u[j], H());
+            v[i + 2 * j] = f.x; v[i + 2 * j + 1] = f.y;
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_vec(float *p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int N, typename H>
+__device__ __forceinline__ void store_vec(H *p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+        *reinterpret_cast<uint4 *>(p + i) =
+            make_uint4(pack_pair(v[i], v[i + 1], H()), pack_pair(v[i + 2], v[i + 3], H()),
+                       pack_pair(v[i + 4], v[i + 5], H()), pack_pair(v[i + 6], v[i + 7], H()));
+}
+// e4m3 codes: 8 elements in one 8-byte store.
+__device__ __forceinline__ void store_vec(uint8_t *p, const float (&v)[8]) {
+    const uint32_t a = f32x2_to_e4m3x2(v[0], v[1]) | f32x2_to_e4m3x2(v[2], v[3]) << 16;
+    const uint32_t b = f32x2_to_e4m3x2(v[4], v[5]) | f32x2_to_e4m3x2(v[6], v[7]) << 16;
+    *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
+}
+
+// Host launchers (defined in the .cu files).
+struct KvPlanArgs {
+    const int32_t *past, *fresh;
+    int n_req;
+    const int32_t *free_pages;
+    int n_free;
+    const int32_t *free_head;
+    int page;
+    int32_t *table;
+    int64_t table_stride;
+    int max_pages, max_new;
+    int32_t *q_start, *seq_len, *positions;
+    int64_t *slots;
+    int32_t *info;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t s);
+cudaError_t launch_rope_append(const MoeRopeArgs &a, cudaStream_t s);
+cudaError_t launch_block_norm(const MoeNormArgs &a, cudaStream_t s);
+
+// What an attention handle holds; ws: partial results, counters: arrivals of
+// the blocks that share a request's head group.
+struct AttnHandle {
+    uint32_t magic;
+    int device, num_sms;
+    MoeAttnDesc d;
+    float *part;
+    int *arrived;
+};
+cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaStream_t s);
+
+}  // namespace moe

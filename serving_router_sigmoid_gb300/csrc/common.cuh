@@ -79,6 +79,10 @@ struct DebugPtrs {
     int32_t *down_acc;
 };
 
+// Sets the calling thread's error text (moe_last_error) and returns `code`.
+int fail(int code, const char *fmt, ...);
+int cuda_fail(cudaError_t ce, const char *what);
+
 // ------------------------------------------------------------------ helpers
 
 // Sentinels of the decode kernel's data-as-flag hand-overs: a logit slot or a

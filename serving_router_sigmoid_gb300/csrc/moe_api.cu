@@ -11,9 +11,9 @@
 
 #include "layer_args.cuh"
 
-namespace {
+namespace moe {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 int fail(int code, const char *fmt, ...) {
     va_list ap;
@@ -26,6 +26,13 @@ int fail(int code, const char *fmt, ...) {
 int cuda_fail(cudaError_t ce, const char *what) {
     return fail(MOE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(ce), cudaGetErrorName(ce));
 }
+
+}  // namespace moe
+
+namespace {
+
+using moe::cuda_fail;
+using moe::fail;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -326,7 +333,7 @@ extern "C" {
 
 int moe_version(void) { return (1 << 16) | 0; }
 
-const char *moe_last_error(void) { return g_err; }
+const char *moe_last_error(void) { return moe::g_err; }
 
 int moe_pack_int4(const float *w, uint8_t *q4, float *scale, int64_t O, int64_t I, cudaStream_t stream) {
     if (O < 0 || I < 0) return fail(MOE_ERR_SHAPE, "O=%lld I=%lld must be >= 0", (long long)O, (long long)I);
