@@ -63,8 +63,8 @@ def _device(device) -> int:
 def _here(dev: int, **tensors) -> None:
     """Every tensor (None: absent) on CUDA device `dev`, which has to be the current one."""
     for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name}: expected a tensor on cuda:{dev} (the library has no CPU path)")
+        if t is not None and (dev < 0 or t.get_device() != dev):
+            raise ValueError(f"{name}: expected a tensor on cuda:{max(dev, 0)} (the library has no CPU path)")
     if torch.cuda.current_device() != dev:
         raise ValueError(f"cuda:{dev} has to be the current device")
 
