@@ -145,6 +145,7 @@ struct AttnHandle {
     float *part;
     int *arrived;
 };
+cudaError_t attn_prepare(const MoeAttnDesc &d, size_t *piece_floats, int *groups);
 cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaStream_t s);
 
 }  // namespace moe

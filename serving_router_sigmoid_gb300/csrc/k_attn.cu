@@ -1,103 +1,71 @@
-// k_attn.cu -- attention of one new token per request over the paged cache
-// (moe_attn_decode): one block per query head, its warps take the tokens in
-// turn with a running maximum and sum each, joined in shared memory.
-#include "attn_args.cuh"
+// k_attn.cu -- launch of the paged-cache attention (moe_attn_decode): the
+// kernel's form by sizes and types, its attributes and its parameters.
+#include "attn_dev.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMaxHeadDim = 256;
-
-template <int CT>
-__device__ __forceinline__ float cached(const void *p, int64_t i) {
-    if constexpr (CT == MOE_E4M3) {
-        const uint32_t h = e4m3x2_to_f16x2(static_cast<const uint8_t *>(p)[i]);
-        return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
-    } else {
-        return to_f32(static_cast<const typename Elem<CT>::type *>(p)[i]);
+attn::Form form_of(const MoeAttnDesc &d, int cache_type, bool wide) {
+    const int dim = d.k_dim > d.v_dim ? d.k_dim : d.v_dim, group = d.n_heads / d.n_kv_heads;
+    switch (cache_type) {
+        case MOE_F16: return attn::pick_f16(dim, group, wide);
+        case MOE_BF16: return attn::pick_bf16(dim, group, wide);
+        default: return attn::pick_e4m3(dim, group, wide);
     }
-}
-
-__device__ __forceinline__ float act_at(const void *p, int type, int64_t i) {
-    return type == MOE_F32   ? static_cast<const float *>(p)[i]
-           : type == MOE_F16 ? __half2float(static_cast<const __half *>(p)[i])
-                             : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-}
-
-template <int CT>
-__global__ void __launch_bounds__(32 * kWarps) attn_decode_kernel(const __grid_constant__ MoeAttnArgs a,
-                                                                  const __grid_constant__ MoeAttnDesc d) {
-    __shared__ float s_o[kWarps][kMaxHeadDim];
-    __shared__ float s_m[kWarps], s_l[kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.x / d.n_heads, h = blockIdx.x - b * d.n_heads, kh = h / (d.n_heads / d.n_kv_heads);
-    const long long cap = (long long)a.max_pages * a.page_size;
-    const int len = (int)min((long long)max(a.seq_len[b], 0), cap);
-    const int from = a.window > 0 ? max(0, len - a.window) : 0;
-    float q[8], o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int e = lane + 32 * i;
-        q[i] = e < d.k_dim ? act_at(a.q, a.act_type, b * a.q_stride_b + h * a.q_stride_h + e) : 0.f;
-        o[i] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int t = from + warp; t < len; t += kWarps) {
-        const int col = t / a.page_size;
-        const int page = a.block_table[b * a.table_stride + col];
-        if (page < 0 || page >= a.n_pages) continue;
-        const int at = t - col * a.page_size;
-        const int64_t ko = page * a.kc_stride_page + at * a.kc_stride_tok + kh * a.kc_stride_head;
-        const int64_t vo = page * a.vc_stride_page + at * a.vc_stride_tok + kh * a.vc_stride_head;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = lane + 32 * i;
-            if (e < d.k_dim) s = fmaf(q[i], cached<CT>(a.k_cache, ko + e), s);
-        }
-        s = warp_sum_f(s) * (a.scale * a.k_scale);
-        const float mn = fmaxf(m, s);
-        const float f = expf(m - mn), p = expf(s - mn);
-        m = mn;
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = lane + 32 * i;
-            if (e < d.v_dim) o[i] = fmaf(p, cached<CT>(a.v_cache, vo + e), o[i] * f);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s_o[warp][lane + 32 * i] = o[i];
-    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-    __syncthreads();
-    float top = -INFINITY, total = 0.f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-    for (int w = 0; w < kWarps; ++w)
-        if (s_l[w] > 0.f) total += s_l[w] * expf(s_m[w] - top);
-    for (int e = threadIdx.x; e < d.v_dim; e += 32 * kWarps) {
-        float r = 0.f;
-        for (int w = 0; w < kWarps; ++w)
-            if (s_l[w] > 0.f) r += s_o[w][e] * expf(s_m[w] - top);
-        r = total > 0.f ? r / total * a.v_scale : 0.f;
-        const int64_t at = b * a.out_stride_b + h * a.out_stride_h + e;
-        if (a.act_type == MOE_F32) static_cast<float *>(a.out)[at] = r;
-        else if (a.act_type == MOE_F16) static_cast<__half *>(a.out)[at] = __float2half_rn(r);
-        else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(r);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)b * d.n_heads + h] = total > 0.f ? top + logf(total) : -INFINITY;
 }
 
 }  // namespace
 
+// Piece floats a block may leave, over all forms of a handle, and head groups.
+cudaError_t attn_prepare(const MoeAttnDesc &d, size_t *piece_floats, int *groups) {
+    *piece_floats = 0;
+    *groups = 0;
+    for (int ct : {MOE_F16, MOE_BF16, MOE_E4M3})
+        for (bool wide : {false, true}) {
+            const attn::Form f = form_of(d, ct, wide);
+            const cudaError_t ce = cudaFuncSetAttribute(reinterpret_cast<const void *>(f.fn),
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                        (int)f.smem(MOE_MAX_REQUESTS));
+            if (ce != cudaSuccess) return ce;
+            const int per = (d.n_heads / d.n_kv_heads + f.rows - 1) / f.rows;
+            if ((size_t)f.piece > *piece_floats) *piece_floats = f.piece;
+            if (d.n_kv_heads * per > *groups) *groups = d.n_kv_heads * per;
+        }
+    return cudaSuccess;
+}
+
 cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaStream_t s) {
-    const int grid = a.n_requests * h.d.n_heads;
-    switch (a.cache_type) {
-        case MOE_F16: attn_decode_kernel<MOE_F16><<<grid, 32 * kWarps, 0, s>>>(a, h.d); break;
-        case MOE_BF16: attn_decode_kernel<MOE_BF16><<<grid, 32 * kWarps, 0, s>>>(a, h.d); break;
-        default: attn_decode_kernel<MOE_E4M3><<<grid, 32 * kWarps, 0, s>>>(a, h.d); break;
-    }
-    return cudaGetLastError();
+    // fp32 queries, and f16 queries on bf16 keys, enter the products in several terms
+    const bool wide = a.act_type == MOE_F32 || (a.act_type == MOE_F16 && a.cache_type == MOE_BF16);
+    const attn::Form f = form_of(h.d, a.cache_type, wide);
+    const int64_t ae = (int64_t)dtype_bytes(a.act_type), ce = (int64_t)dtype_bytes(a.cache_type);
+    const auto on16 = [&](const void *p, int64_t s0, int64_t s1) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && s0 * ae % 16 == 0 && s1 * ae % 16 == 0;
+    };
+    attn::Params p;
+    p.a = a;
+    p.n_heads = h.d.n_heads;
+    p.n_kv = h.d.n_kv_heads;
+    p.group = h.d.n_heads / h.d.n_kv_heads;
+    p.n_groups = (p.group + f.rows - 1) / f.rows;
+    p.k_dim = h.d.k_dim;
+    p.v_dim = h.d.v_dim;
+    p.q16 = on16(a.q, a.q_stride_b, a.q_stride_h);
+    p.out16 = on16(a.out, a.out_stride_b, a.out_stride_h);
+    p.by16 = a.page_size % 16 == 0;
+    p.k_page = a.kc_stride_page * ce;
+    p.k_tok = a.kc_stride_tok * ce;
+    p.k_head = a.kc_stride_head * ce;
+    p.v_page = a.vc_stride_page * ce;
+    p.v_tok = a.vc_stride_tok * ce;
+    p.v_head = a.vc_stride_head * ce;
+    p.by_page = FastDiv((uint32_t)a.page_size);
+    p.part = h.part;
+    p.arrived = h.arrived;
+    p.min_steps = 2 * (f.threads / 32);  // two steps a warp
+    void *args[] = {&p};
+    return cudaLaunchKernel(reinterpret_cast<const void *>(f.fn), dim3(h.num_sms), dim3(f.threads), args,
+                            f.smem(a.n_requests), s);
 }
 
 }  // namespace moe
