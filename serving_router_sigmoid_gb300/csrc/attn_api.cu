@@ -191,7 +191,7 @@ int moe_attn_decode(void *handle, const MoeAttnArgs *p, cudaStream_t stream) {
         return fail(MOE_ERR_SHAPE, "n_requests=%d outside [0, max_requests=%d]", a.n_requests, h->d.max_requests);
     if (a.page_size < 1 || a.page_size > kMaxPage)
         return fail(MOE_ERR_SHAPE, "page_size=%d: need 1 <= page_size <= %d", a.page_size, kMaxPage);
-    if (a.max_pages < 0 || a.n_pages < 0 || a.window < 0)
+    if (a.max_pages < 0 || a.n_pages < 0 || a.n_pages > INT32_MAX || a.window < 0)
         return fail(MOE_ERR_SHAPE, "max_pages=%d n_pages=%lld window=%d must be >= 0", a.max_pages,
                     (long long)a.n_pages, a.window);
     if ((int64_t)a.max_pages * a.page_size > INT32_MAX)

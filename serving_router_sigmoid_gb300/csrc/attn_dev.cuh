@@ -47,7 +47,9 @@ struct Params {
     int k_dim, v_dim;
     int q16, out16;       // rows of q / out start on 16 bytes
     int by16;             // pages hold whole runs of 16 tokens
-    int64_t k_page, k_tok, k_head, v_page, v_tok, v_head;  // strides in bytes
+    uint32_t n_pages;
+    int64_t k_page, k_tok, k_tok8, k_head;  // strides in bytes (tok8: of 8 tokens)
+    int64_t v_page, v_tok, v_tok8, v_head;
     FastDiv by_page;
     float *part;          // [2 grid] pieces
     int *arrived;         // [requests, key heads * groups]
@@ -70,13 +72,14 @@ struct Cfg {
     static constexpr int NQ = !WIDE ? 1 : kF16 ? 2 : 3;
     static constexpr int NP = WIDE ? NQ : 2;
     static constexpr int ROWS = 8 * NT;
-    static constexpr bool QS = NQ * NT * DMAX > 128;  // query fragments in shared memory
+    static constexpr bool QS = NQ * NT * DMAX > 128;  // query fragments stay in shared memory
     // one block per SM; registers allow 12 warps of the plain form, and shared
     // memory 4 of the largest ones
     static constexpr int WARPS = DMAX <= 128 && NT == 1 && !WIDE ? 12 : WIDE && NT * DMAX == 256 ? 4 : 8;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int PIECE = ROWS * (DMAX + 2);  // floats of a piece: O, m, l
-    static constexpr size_t kQBytes = QS ? (size_t)WARPS * NQ * NT * KSTEPS * 32 * 8 : 0;
+    static constexpr int QFRAGS = NQ * NT * KSTEPS;
+    static constexpr size_t kQBytes = (size_t)WARPS * QFRAGS * 32 * 8;
     static constexpr size_t smem(int n_requests) {
         return ((size_t)(n_requests + 1) * 4 + 15) / 16 * 16 + kQBytes + (size_t)WARPS * 2 * PIECE * 4;
     }
@@ -121,6 +124,12 @@ __device__ __forceinline__ uint2 ld8(const char *p) {
     asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
     return r;
 }
+// Four e4m3 codes -> two pairs of f16 (exact).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (F16) return pack_pair(lo, hi, __half());
@@ -147,50 +156,56 @@ __device__ __forceinline__ void seen(const MoeAttnArgs &a, int b, int &from, int
     from = a.window > 0 ? max(0, len - a.window) : 0;
 }
 
-// N consecutive elements of q as fp32 (zeros beyond `left` elements).
-template <int N>
-__device__ __forceinline__ void load_q(const Params &p, int64_t at, int left, float (&v)[N]) {
+// 8 consecutive elements of q as fp32.
+__device__ __forceinline__ void load_q(const Params &p, int64_t at, float (&v)[8]) {
+    if (p.a.act_type == MOE_F32) {
+        const float *q = static_cast<const float *>(p.a.q) + at;
+        if (p.q16) {
+            load_vec(q, v);
+        } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
-    if (left <= 0) return;
-    if (p.q16) {
-        if (p.a.act_type == MOE_F32) load_vec(static_cast<const float *>(p.a.q) + at, v);
-        else if (p.a.act_type == MOE_F16) load_vec(static_cast<const __half *>(p.a.q) + at, v);
-        else load_vec(static_cast<const __nv_bfloat16 *>(p.a.q) + at, v);
+            for (int i = 0; i < 8; ++i) v[i] = q[i];
+        }
         return;
     }
+    const uint16_t *q = static_cast<const uint16_t *>(p.a.q) + at;
+    uint32_t w[4];
+    if (p.q16) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(q);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (p.a.act_type == MOE_F32) v[i] = static_cast<const float *>(p.a.q)[at + i];
-        else if (p.a.act_type == MOE_F16) v[i] = __half2float(static_cast<const __half *>(p.a.q)[at + i]);
-        else v[i] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.a.q)[at + i]);
+        for (int i = 0; i < 4; ++i) w[i] = q[2 * i] | (uint32_t)q[2 * i + 1] << 16;
+    }
+    const bool h = p.a.act_type == MOE_F16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = h ? half_pair(w[i], __half()) : half_pair(w[i], __nv_bfloat16());
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
     }
 }
 
-// N (4 or 8k) consecutive outputs.
-template <int N>
-__device__ __forceinline__ void store_out(const Params &p, int64_t at, const float (&v)[N]) {
-    if (p.out16) {
-        if (p.a.act_type == MOE_F32) {
-            store_vec(static_cast<float *>(p.a.out) + at, v);
-            return;
-        }
-        if constexpr (N % 8 == 0) {
-            if (p.a.act_type == MOE_F16) store_vec(static_cast<__half *>(p.a.out) + at, v);
-            else store_vec(static_cast<__nv_bfloat16 *>(p.a.out) + at, v);
+// 4 consecutive outputs.
+__device__ __forceinline__ void store_out(const Params &p, int64_t at, const float (&v)[4]) {
+    if (p.a.act_type == MOE_F32) {
+        float *o = static_cast<float *>(p.a.out) + at;
+        if (p.out16) {
+            store_vec(o, v);
         } else {
-            uint2 w;
-            w.x = p.a.act_type == MOE_F16 ? pack2<true>(v[0], v[1]) : pack2<false>(v[0], v[1]);
-            w.y = p.a.act_type == MOE_F16 ? pack2<true>(v[2], v[3]) : pack2<false>(v[2], v[3]);
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.out) + at) = w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = v[i];
         }
         return;
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (p.a.act_type == MOE_F32) static_cast<float *>(p.a.out)[at + i] = v[i];
-        else if (p.a.act_type == MOE_F16) static_cast<__half *>(p.a.out)[at + i] = __float2half_rn(v[i]);
-        else static_cast<__nv_bfloat16 *>(p.a.out)[at + i] = __float2bfloat16_rn(v[i]);
+    uint16_t *o = static_cast<uint16_t *>(p.a.out) + at;
+    const bool h = p.a.act_type == MOE_F16;
+    const uint32_t x = h ? pack2<true>(v[0], v[1]) : pack2<false>(v[0], v[1]);
+    const uint32_t y = h ? pack2<true>(v[2], v[3]) : pack2<false>(v[2], v[3]);
+    if (p.out16) {
+        *reinterpret_cast<uint2 *>(o) = make_uint2(x, y);
+    } else {
+        o[0] = (uint16_t)x; o[1] = (uint16_t)(x >> 16); o[2] = (uint16_t)y; o[3] = (uint16_t)(y >> 16);
     }
 }
 
@@ -201,48 +216,47 @@ struct Slot {
 };
 
 // Joins n pieces (O, m, l) of one segment, the i-th at piece(i), into the
-// output, or into a piece `to` for the blocks' join.
-template <bool GLOBAL, int ROWS, int DMAX, int THREADS, typename Piece>
-__device__ __forceinline__ void join_pieces(const Params &p, Piece piece, int n, int b, int hg, float off, float *to) {
-    const MoeAttnArgs &a = p.a;
+// output, or into a piece `to` for the blocks' join; threads tid of nthr.
+// (Rolled loops: this code runs once a segment, its size counts more.)
+template <int ROWS, int DMAX, typename Piece>
+__device__ __forceinline__ void join_pieces(const Params &p, Piece piece, int n, int b, int hg, float *to, int tid,
+                                            int nthr) {
     const int kvh = hg / p.n_groups, h0 = kvh * p.group + (hg - kvh * p.n_groups) * ROWS;
     const int heads = min(ROWS, (kvh + 1) * p.group - h0);
-    auto ld1 = [](const float *q) { return GLOBAL ? __ldcg(q) : *q; };
-    auto ld4 = [](const float *q) {
-        return GLOBAL ? __ldcg(reinterpret_cast<const float4 *>(q)) : *reinterpret_cast<const float4 *>(q);
-    };
-    for (int e = threadIdx.x; e < ROWS * (DMAX / 4); e += THREADS) {
+#pragma unroll 1
+    for (int e = tid; e < ROWS * (DMAX / 4); e += nthr) {
         const int row = e / (DMAX / 4), d = 4 * (e - row * (DMAX / 4));
         if (row >= heads || d >= p.v_dim) continue;
         float top = kFloor;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) top = fmaxf(top, ld1(piece(i) + ROWS * DMAX + row));
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) top = fmaxf(top, piece(i)[ROWS * DMAX + row]);
         float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < n; ++i) {
             const float *q = piece(i);
-            const float f = exp2_fast(ld1(q + ROWS * DMAX + row) - top);
-            sum = fmaf(ld1(q + ROWS * (DMAX + 1) + row), f, sum);
-            const float4 v = ld4(q + row * DMAX + d);
+            const float f = exp2_fast(q[ROWS * DMAX + row] - top);
+            sum = fmaf(q[ROWS * (DMAX + 1) + row], f, sum);
+            const float4 v = *reinterpret_cast<const float4 *>(q + row * DMAX + d);
             x[0] = fmaf(v.x, f, x[0]);
             x[1] = fmaf(v.y, f, x[1]);
             x[2] = fmaf(v.z, f, x[2]);
             x[3] = fmaf(v.w, f, x[3]);
         }
         if (to) {
-            *reinterpret_cast<float4 *>(to + row * DMAX + d) = make_float4(x[0], x[1], x[2], x[3]);
+            store_vec(to + row * DMAX + d, x);
             if (d == 0) {
                 to[ROWS * DMAX + row] = top;
                 to[ROWS * (DMAX + 1) + row] = sum;
             }
         } else {
-            const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+            const bool none = sum == 0.f;  // no token seen (a NaN goes through)
+            const float inv = none ? 0.f : p.a.v_scale / sum;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = sum == 0.f ? 0.f : x[j] * inv;
-            store_out(p, b * a.out_stride_b + (h0 + row) * a.out_stride_h + d, x);
-            if (d == 0 && a.lse)
-                a.lse[(int64_t)b * p.n_heads + h0 + row] =
-                    sum == 0.f ? -INFINITY : (top - off + log2f(sum)) * 0.6931471805599453f;
+            for (int j = 0; j < 4; ++j) x[j] = none ? 0.f : x[j] * inv;
+            store_out(p, b * p.a.out_stride_b + (h0 + row) * p.a.out_stride_h + d, x);
+            if (d == 0 && p.a.lse)
+                p.a.lse[(int64_t)b * p.n_heads + h0 + row] =
+                    none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
         }
     }
 }
@@ -253,15 +267,15 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
     using C = Cfg<CT, DMAX, NT, WIDE>;
     constexpr bool F16 = C::kF16;
     extern __shared__ __align__(16) char smem[];
-    __shared__ Slot slots[C::WARPS * 2];
+    __shared__ Slot slots[C::WARPS * 2], s_open[2];
     __shared__ int wsum[C::WARPS];
-    __shared__ int s_join[2];
+    __shared__ int s_join[2];  // blocks before the last of a shared segment to join, or -1
     const MoeAttnArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int n_req = a.n_requests, HG = p.n_kv * p.n_groups;
     int *prefix = reinterpret_cast<int *>(smem);
     char *after = smem + ((size_t)(n_req + 1) * 4 + 15) / 16 * 16;
-    uint2 *qsm = reinterpret_cast<uint2 *>(after) + (size_t)warp * (C::QS ? C::NQ * NT * C::KSTEPS * 32 : 0);
+    uint2 *qsm = reinterpret_cast<uint2 *>(after) + warp * C::QFRAGS * 32;
     float *pieces = reinterpret_cast<float *>(after + C::kQBytes);
 
     // prefix sum of the requests' steps
@@ -291,16 +305,17 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
             all += s;
         }
         if (b < n_req) prefix[b] = total + below + x - n;
-        // requests that see nothing: zeros, by the blocks in turn
         total += all;
     }
     if (tid == 0) prefix[n_req] = total;
     if (lane < 2) slots[warp * 2 + lane].b = -1;
     if (tid < 2) s_join[tid] = -1;
     __syncthreads();
+    // requests that see nothing, by the blocks in turn
     for (int b = blockIdx.x; b < n_req; b += gridDim.x) {
         if (prefix[b + 1] != prefix[b]) continue;
         const float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
         for (int i = tid; i < p.n_heads * (p.v_dim / 4); i += C::THREADS) {
             const int h = i / (p.v_dim / 4), d = 4 * (i - h * (p.v_dim / 4));
             store_out(p, b * a.out_stride_b + h * a.out_stride_h + d, z);
@@ -311,19 +326,25 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
 
     // this block's and this warp's run of steps
     const long long U = (long long)total * HG;
-    long long nblk = (U + p.min_steps - 1) / p.min_steps;
-    if (nblk > gridDim.x) nblk = gridDim.x;
-    if ((long long)blockIdx.x >= nblk) return;
-    const long long lo = blockIdx.x * U / nblk, hi = (blockIdx.x + 1) * U / nblk;
-    const long long wb = lo + warp * (hi - lo) / C::WARPS, we = lo + (warp + 1) * (hi - lo) / C::WARPS;
+    long long per = (U + gridDim.x - 1) / gridDim.x;
+    if (per < p.min_steps) per = p.min_steps;
+    const long long lo = blockIdx.x * per, hi = min(lo + per, U);
+    if (lo >= U) return;
+    const long long per_w = (hi - lo + C::WARPS - 1) / C::WARPS;
+    const long long wb = min(lo + warp * per_w, hi), we = min(wb + per_w, hi);
 
+    int b = 0, hg = 0, steps = 1;
+    long long sb = 0;  // first step of the segment (b, hg)
+    if (wb < we) {
+        b = last_le(prefix, n_req, (int)(wb / HG));
+        steps = prefix[b + 1] - prefix[b];
+        sb = (long long)prefix[b] * HG;
+        hg = (int)((wb - sb) / steps);
+        sb += (long long)hg * steps;
+    }
     for (long long u = wb; u < we;) {
-        const int b = last_le(prefix, n_req, (int)(u / HG));
-        const int steps = prefix[b + 1] - prefix[b];
-        const long long base = (long long)prefix[b] * HG;
-        const int hg = (int)((u - base) / steps);
-        const long long sb = base + (long long)hg * steps, se = sb + steps;
-        const int first = (int)(u - sb), last = (int)((se < we ? se : we) - sb);
+        const long long se = sb + steps;
+        const int first = (int)(u - sb), last = (int)(min(se, we) - sb);
         const int kvh = hg / p.n_groups, h0 = kvh * p.group + (hg - kvh * p.n_groups) * C::ROWS;
         const int heads = min(C::ROWS, (kvh + 1) * p.group - h0);
         int from, len;
@@ -340,90 +361,31 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
             nxt = wcol + 32 + lane < ncol ? __ldg(bt + wcol + 32 + lane) : -1;
         }
 
-        // query fragments; fac: what turns an accumulator into a logit in units of log 2
-        uint32_t qf[C::QS ? 1 : C::NQ * NT * C::KSTEPS][2];
-        float fac[NT][2];
+        const char *kb = static_cast<const char *>(a.k_cache) + kvh * p.k_head + g * p.k_tok + c * 16;
+        const char *vb = static_cast<const char *>(a.v_cache) + kvh * p.v_head + 2 * c * p.v_tok + g * C::VB;
+        uint4 kr[C::R][2][C::KCH];
+        uint32_t vr[C::R][4][C::VCH][C::VB / 4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            constexpr int EC = 16 / C::ES;
-            const bool on = nt * 8 + g < heads;
-            const int64_t at = b * a.q_stride_b + (int64_t)(h0 + nt * 8 + g) * a.q_stride_h;
-            float pw = 1.f;
-            float v[C::KCH][EC];
-            float top = 0.f;
+        for (int r = 0; r < C::R; ++r) {
 #pragma unroll
-            for (int i = 0; i < C::KCH; ++i) {
-                const int d = (4 * i + c) * EC;
-                load_q(p, at + d, on ? p.k_dim - d : 0, v[i]);
-                if (F16) {
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int e = 0; e < EC; ++e) top = fmaxf(top, fabsf(v[i][e]));
-                }
-            }
-            if (F16) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                int ex = (int)(__float_as_uint(top) >> 23) - 127;
-                ex = top > 0.f ? max(-126, min(126, ex)) : 0;
-                pw = __uint_as_float((uint32_t)(ex + 127) << 23);
-                const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+                for (int i = 0; i < C::KCH; ++i) kr[r][h][i] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int i = 0; i < C::KCH; ++i)
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int e = 0; e < EC; ++e) v[i][e] *= inv;
-            }
+                for (int i = 0; i < C::VCH; ++i)
 #pragma unroll
-            for (int i = 0; i < C::KCH; ++i)
-#pragma unroll
-                for (int w = 0; w < EC / 2; ++w) {
-                    float x = v[i][2 * w], y = v[i][2 * w + 1];
-#pragma unroll
-                    for (int q = 0; q < C::NQ; ++q) {
-                        const uint32_t pk = pack2<F16>(x, y);
-                        const int f = (q * NT + nt) * C::KSTEPS + i * (EC / 4) + w / 2;
-                        if constexpr (C::QS) (w & 1 ? qsm[f * 32 + lane].y : qsm[f * 32 + lane].x) = pk;
-                        else qf[f][w & 1] = pk;
-                        const float2 r = unpack2<F16>(pk);
-                        x -= r.x;
-                        y -= r.y;
-                    }
-                }
-            const float f0 = a.scale * a.k_scale * 1.4426950408889634f;
-            fac[nt][0] = f0 * __shfl_sync(0xffffffffu, pw, (2 * c) * 4);
-            fac[nt][1] = f0 * __shfl_sync(0xffffffffu, pw, (2 * c + 1) * 4);
-        }
-        __syncwarp();
-
-        float o[NT][C::VW][4], m[NT][2], l[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int w = 0; w < C::VW; ++w)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[nt][w][i] = 0.f;
-            m[nt][0] = m[nt][1] = kFloor;
-            l[nt][0] = l[nt][1] = 0.f;
+                    for (int j = 0; j < C::VB / 4; ++j) vr[r][k][i][j] = 0u;
         }
 
-        const char *kb = static_cast<const char *>(a.k_cache) + kvh * p.k_head + c * 16;
-        const char *vb = static_cast<const char *>(a.v_cache) + kvh * p.v_head + g * C::VB;
-        int page[C::R], at[C::R];  // of the tile whose keys were requested last (pages of whole tiles)
-        auto find = [&](int t) {
-#pragma unroll
-            for (int r = 0; r < C::R; ++r) {
-                const int tok = t + 16 * r;
-                const int col = (int)p.by_page.div(tok);
-                if (col - wcol >= 32) {
-                    wcol += 32;
-                    cur = nxt;
-                    nxt = wcol + 32 + lane < ncol ? __ldg(bt + wcol + 32 + lane) : -1;
-                }
-                page[r] = __shfl_sync(0xffffffffu, cur, (col - wcol) & 31);
-                at[r] = tok - col * a.page_size;
-            }
-        };
-        // Byte offset of token t + row in a cache, or -1 where there is nothing to see.
-        auto row_at = [&](int t, int r, int row, int64_t sp, int64_t st) -> int64_t {
+        // A step is `plain` when all its tokens are seen and lie on whole
+        // pages: its rows are then at fixed distances from one address a tile.
+        // (Pieces beyond the head's size stay the zeros they are.)
+        int page[C::R], at[C::R];
+        bool plain = false;
+        uint32_t k_on = 0;  // else: bit 2 r + half, that key row is seen
+        auto row_at = [&](int t, int r, int row, int64_t sp, int64_t st) -> int64_t {  // from row 0; -1: not seen
             const int tok = t + 16 * r + row;
             if (tok < from || tok >= len) return -1;
             int pg, in;
@@ -435,53 +397,170 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                 pg = __ldg(bt + col);
                 in = tok - col * a.page_size;
             }
-            if ((unsigned)pg >= (unsigned long long)a.n_pages) return -1;
-            return pg * sp + in * st;
+            return (uint32_t)pg < p.n_pages ? pg * sp + in * st : -1;
         };
-        uint4 kr[C::R][2][C::KCH];
-        uint32_t k_on = 0;  // bit 2 r + half: that row is seen
-        auto load_keys = [&](int t) {
-            if (p.by16) find(t);
-            k_on = 0;
+        auto request_keys = [&](int t) {
+            plain = p.by16 && t >= from && t + C::TT <= len;
+            if (p.by16) {
 #pragma unroll
-            for (int r = 0; r < C::R; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t off = row_at(t, r, g + 8 * h, p.k_page, p.k_tok);
-                    if (off >= 0) k_on |= 1u << (2 * r + h);
-#pragma unroll
-                    for (int i = 0; i < C::KCH; ++i) {
-                        kr[r][h][i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (off >= 0 && (4 * i + c) * (16 / C::ES) < p.k_dim) kr[r][h][i] = ld16(kb + off + i * 64);
+                for (int r = 0; r < C::R; ++r) {
+                    const int tok = t + 16 * r, col = (int)p.by_page.div(tok);
+                    if (col - wcol >= 32) {
+                        wcol += 32;
+                        cur = nxt;
+                        nxt = wcol + 32 + lane < ncol ? __ldg(bt + wcol + 32 + lane) : -1;
                     }
+                    page[r] = __shfl_sync(0xffffffffu, cur, (col - wcol) & 31);
+                    at[r] = tok - col * a.page_size;
+                    plain = plain && (uint32_t)page[r] < p.n_pages;
                 }
+            }
+            if (plain) {
+#pragma unroll
+                for (int r = 0; r < C::R; ++r) {
+                    const char *k = kb + page[r] * p.k_page + at[r] * p.k_tok;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < C::KCH; ++i)
+                            if ((4 * i + c) * (16 / C::ES) < p.k_dim) kr[r][h][i] = ld16(k + h * p.k_tok8 + i * 64);
+                }
+            } else {
+                k_on = 0;
+#pragma unroll
+                for (int r = 0; r < C::R; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int64_t off = row_at(t, r, g + 8 * h, p.k_page, p.k_tok);
+                        if (off >= 0) k_on |= 1u << (2 * r + h);
+#pragma unroll
+                        for (int i = 0; i < C::KCH; ++i) {
+                            kr[r][h][i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (off >= 0 && (4 * i + c) * (16 / C::ES) < p.k_dim)
+                                kr[r][h][i] = ld16(kb + (off - g * p.k_tok) + i * 64);
+                        }
+                    }
+            }
+        };
+        auto ldv = [&](uint32_t(&w)[C::VB / 4], const char *q) {
+            if constexpr (C::VB == 16) {
+                const uint4 x = ld16(q);
+                w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+            } else {
+                const uint2 x = ld8(q);
+                w[0] = x.x; w[1] = x.y;
+            }
+        };
+        auto request_values = [&](int t) {
+            if (plain) {
+#pragma unroll
+                for (int r = 0; r < C::R; ++r) {
+                    const char *v = vb + page[r] * p.v_page + at[r] * p.v_tok;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < C::VCH; ++i)
+                            if ((8 * i + g) * C::VE < p.v_dim)
+                                ldv(vr[r][k][i], v + (k & 1) * p.v_tok + (k >> 1) * p.v_tok8 + i * (8 * C::VB));
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < C::R; ++r)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int64_t off = row_at(t, r, 2 * c + (k & 1) + 8 * (k >> 1), p.v_page, p.v_tok);
+#pragma unroll
+                        for (int i = 0; i < C::VCH; ++i) {
+#pragma unroll
+                            for (int j = 0; j < C::VB / 4; ++j) vr[r][k][i][j] = 0u;
+                            if (off >= 0 && (8 * i + g) * C::VE < p.v_dim)
+                                ldv(vr[r][k][i], vb + (off - 2 * c * p.v_tok) + i * (8 * C::VB));
+                        }
+                    }
+            }
         };
 
-        load_keys(tok0 + first * C::TT);
+        request_keys(tok0 + first * C::TT);
+
+        // Query fragments, through this warp's shared memory.  fac: what turns
+        // an accumulator into a logit in units of log 2.
+        uint32_t qf[C::QS ? 1 : C::QFRAGS][2];
+        float fac[NT][2];
+        constexpr int EC = 16 / C::ES;
+#pragma unroll 1
+        for (int nt = 0; nt < NT; ++nt) {
+            const bool on = nt * 8 + g < heads;
+            const int64_t qat = b * a.q_stride_b + (int64_t)(h0 + nt * 8 + g) * a.q_stride_h;
+            float pw = 1.f, inv = 1.f;
+            if (F16) {
+                float top = 0.f;
+#pragma unroll 1
+                for (int i = 0; i < C::KCH * (EC / 8); ++i) {
+                    const int d = (4 * (i / (EC / 8)) + c) * EC + 8 * (i % (EC / 8));
+                    float v[8];
+                    if (!on || d >= p.k_dim) continue;
+                    load_q(p, qat + d, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                int ex = (int)(__float_as_uint(top) >> 23) - 127;
+                ex = top > 0.f ? max(-126, min(126, ex)) : 0;
+                pw = __uint_as_float((uint32_t)(127 + ex) << 23);
+                inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+            }
+#pragma unroll 1
+            for (int i = 0; i < C::KCH * (EC / 8); ++i) {
+                const int d = (4 * (i / (EC / 8)) + c) * EC + 8 * (i % (EC / 8));
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (on && d < p.k_dim) load_q(p, qat + d, v);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = v[4 * w + e] * inv;
+#pragma unroll
+                    for (int q = 0; q < C::NQ; ++q) {
+                        const uint2 pk = make_uint2(pack2<F16>(x[0], x[1]), pack2<F16>(x[2], x[3]));
+                        qsm[((q * NT + nt) * C::KSTEPS + 2 * i + w) * 32 + lane] = pk;
+                        const float2 r0 = unpack2<F16>(pk.x), r1 = unpack2<F16>(pk.y);
+                        x[0] -= r0.x; x[1] -= r0.y; x[2] -= r1.x; x[3] -= r1.y;
+                    }
+                }
+            }
+            const float f0 = a.scale * a.k_scale * 1.4426950408889634f;
+            const float f1 = f0 * __shfl_sync(0xffffffffu, pw, (2 * c) * 4);
+            const float f2 = f0 * __shfl_sync(0xffffffffu, pw, (2 * c + 1) * 4);
+            if (NT == 1 || nt == 0) fac[0][0] = f1, fac[0][1] = f2;
+            else fac[NT - 1][0] = f1, fac[NT - 1][1] = f2;
+        }
+        __syncwarp();
+        if constexpr (!C::QS) {
+#pragma unroll
+            for (int f = 0; f < C::QFRAGS; ++f) {
+                const uint2 w = qsm[f * 32 + lane];
+                qf[f][0] = w.x;
+                qf[f][1] = w.y;
+            }
+        }
+
+        // mo: the running maximum less kOff, so that weights come out times 2^kOff
+        float o[NT][C::VW][4], mo[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int w = 0; w < C::VW; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nt][w][i] = 0.f;
+            mo[nt][0] = mo[nt][1] = kFloor;
+            l[nt][0] = l[nt][1] = 0.f;
+        }
+
 #pragma unroll 1
         for (int step = first; step < last; ++step) {
             const int t = tok0 + step * C::TT;
-            // request this step's values
-            uint32_t vr[C::R][4][C::VCH][C::VB / 4];
-#pragma unroll
-            for (int r = 0; r < C::R; ++r)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int64_t off = row_at(t, r, 2 * c + (k & 1) + 8 * (k >> 1), p.v_page, p.v_tok);
-#pragma unroll
-                    for (int i = 0; i < C::VCH; ++i) {
-                        const bool on = off >= 0 && (8 * i + g) * C::VE < p.v_dim;
-                        if constexpr (C::VB == 16) {
-                            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                            if (on) x = ld16(vb + off + i * 128);
-                            vr[r][k][i][0] = x.x; vr[r][k][i][1] = x.y; vr[r][k][i][2] = x.z; vr[r][k][i][3] = x.w;
-                        } else {
-                            uint2 x = make_uint2(0u, 0u);
-                            if (on) x = ld8(vb + off + i * 64);
-                            vr[r][k][i][0] = x.x; vr[r][k][i][1] = x.y;
-                        }
-                    }
-                }
+            request_values(t);
             // S^T = K q^T
             float s[C::R][NT][4];
 #pragma unroll
@@ -497,12 +576,8 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         const uint32_t w[4] = {kr[r][h][i].x, kr[r][h][i].y, kr[r][h][i].z, kr[r][h][i].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            if constexpr (C::ES == 1) {
-                                x[h][2 * j] = e4m3x2_to_f16x2(w[j] & 0xFFFFu);
-                                x[h][2 * j + 1] = e4m3x2_to_f16x2(w[j] >> 16);
-                            } else {
-                                x[h][j] = w[j];
-                            }
+                            if constexpr (C::ES == 1) e4m3x4_to_f16x4(w[j], x[h][2 * j], x[h][2 * j + 1]);
+                            else x[h][j] = w[j];
                         }
                     }
 #pragma unroll
@@ -520,34 +595,44 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                             }
                 }
             }
+            const bool masked = !plain;
             const uint32_t on = k_on;
-            if (step + 1 < last) load_keys(t + C::TT);
+            if (step + 1 < last) request_keys(t + C::TT);
 
             // softmax weights against the running maximum
-            bool move = false;
 #pragma unroll
             for (int r = 0; r < C::R; ++r)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float x = s[r][nt][i] * fac[nt][i & 1];
-                        s[r][nt][i] = on >> (2 * r + (i >> 1)) & 1u ? x : -INFINITY;
-                        move |= s[r][nt][i] > m[nt][i & 1] + kLazy;
+                        s[r][nt][i] *= fac[nt][i & 1];
+                        if (masked && !(on >> (2 * r + (i >> 1)) & 1u)) s[r][nt][i] = -INFINITY;
                     }
+            float top[NT][2];
+            bool move = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    top[nt][k] = fmaxf(s[0][nt][k], s[0][nt][k + 2]);
+#pragma unroll
+                    for (int r = 1; r < C::R; ++r)
+                        top[nt][k] = fmaxf(top[nt][k], fmaxf(s[r][nt][k], s[r][nt][k + 2]));
+                    move |= top[nt][k] > mo[nt][k] + (kLazy + C::kOff);
+                }
             if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float x = m[nt][k];
-#pragma unroll
-                        for (int r = 0; r < C::R; ++r) x = fmaxf(x, fmaxf(s[r][nt][k], s[r][nt][k + 2]));
+                        float x = top[nt][k];
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        const float f = exp2_fast(m[nt][k] - x);
-                        m[nt][k] = x;
+                        x = fmaxf(x - C::kOff, mo[nt][k]);
+                        const float f = exp2_fast(mo[nt][k] - x);
+                        mo[nt][k] = x;
                         l[nt][k] *= f;
 #pragma unroll
                         for (int w = 0; w < C::VW; ++w) {
@@ -562,7 +647,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[r][nt][i] = exp2_fast(s[r][nt][i] - m[nt][i & 1] + C::kOff);
+                    for (int i = 0; i < 4; ++i) s[r][nt][i] = exp2_fast(s[r][nt][i] - mo[nt][i & 1]);
                     l[nt][0] += s[r][nt][0] + s[r][nt][2];
                     l[nt][1] += s[r][nt][1] + s[r][nt][3];
 #pragma unroll
@@ -584,137 +669,170 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < C::VCH; ++i)
 #pragma unroll
-                    for (int j = 0; j < C::VE / 2; ++j) {
-                        uint32_t w[4];
+                    for (int j = 0; j < C::VB / 4; ++j) {
+                        constexpr int PER = C::ES == 1 ? 2 : 1;  // pairs of dimensions a word
+                        uint32_t w[4][PER];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            if constexpr (C::ES == 1)
-                                w[k] = e4m3x2_to_f16x2(j & 1 ? vr[r][k][i][j >> 1] >> 16
-                                                             : vr[r][k][i][j >> 1] & 0xFFFFu);
-                            else
-                                w[k] = vr[r][k][i][j];
+                            if constexpr (C::ES == 1) e4m3x4_to_f16x4(vr[r][k][i][j], w[k][0], w[k][1]);
+                            else w[k][0] = vr[r][k][i][j];
                         }
-                        const uint32_t a0 = __byte_perm(w[0], w[1], 0x5410), a1 = __byte_perm(w[0], w[1], 0x7632);
-                        const uint32_t a2 = __byte_perm(w[2], w[3], 0x5410), a3 = __byte_perm(w[2], w[3], 0x7632);
 #pragma unroll
-                        for (int q = 0; q < C::NP; ++q)
+                        for (int e = 0; e < PER; ++e) {
+                            const uint32_t a0 = __byte_perm(w[0][e], w[1][e], 0x5410);
+                            const uint32_t a1 = __byte_perm(w[0][e], w[1][e], 0x7632);
+                            const uint32_t a2 = __byte_perm(w[2][e], w[3][e], 0x5410);
+                            const uint32_t a3 = __byte_perm(w[2][e], w[3][e], 0x7632);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma<F16>(o[nt][i * (C::VE / 2) + j], a0, a1, a2, a3, pb[r][nt][q][0], pb[r][nt][q][1]);
+                            for (int q = 0; q < C::NP; ++q)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma<F16>(o[nt][i * (C::VE / 2) + j * PER + e], a0, a1, a2, a3, pb[r][nt][q][0],
+                                             pb[r][nt][q][1]);
+                        }
                     }
         }
 
-        // the segment's end, or the run's
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 4);
-                l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 8);
-                l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 16);
-            }
+        // the segment's end, or the run's: the piece to shared memory, and, if
+        // it is the whole segment, on to the output
         const bool whole = sb >= wb && se <= we;
         float *pc = pieces + (warp * 2 + (sb < wb ? 0 : 1)) * C::PIECE;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int row = nt * 8 + 2 * c + k, h = h0 + row;
-                const bool none = l[nt][k] == 0.f;  // no token seen (NaN goes through)
-                const float inv = none ? 0.f : a.v_scale / l[nt][k];
-                if (whole && row >= heads) continue;
+                const int row = nt * 8 + 2 * c + k;
+                float sum = l[nt][k];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
 #pragma unroll
                 for (int i = 0; i < C::VCH; ++i) {
-                    const int d = (8 * i + g) * C::VE;
-                    if (d >= p.v_dim) continue;
                     float x[C::VE];
 #pragma unroll
                     for (int j = 0; j < C::VE / 2; ++j) {
                         x[2 * j] = o[nt][i * (C::VE / 2) + j][k];
                         x[2 * j + 1] = o[nt][i * (C::VE / 2) + j][k + 2];
                     }
-                    if (whole) {
-#pragma unroll
-                        for (int j = 0; j < C::VE; ++j) x[j] = none ? 0.f : x[j] * inv;
-                        store_out(p, b * a.out_stride_b + h * a.out_stride_h + d, x);
-                    } else {
-                        store_vec(pc + row * DMAX + d, x);
-                    }
+                    store_vec(pc + row * DMAX + (8 * i + g) * C::VE, x);
                 }
                 if (g == 0) {
-                    if (!whole) {
-                        pc[C::ROWS * DMAX + row] = m[nt][k];
-                        pc[C::ROWS * (DMAX + 1) + row] = l[nt][k];
-                    } else if (a.lse) {
-                        a.lse[(int64_t)b * p.n_heads + h] =
-                            none ? -INFINITY : (m[nt][k] - C::kOff + log2f(l[nt][k])) * 0.6931471805599453f;
-                    }
+                    pc[C::ROWS * DMAX + row] = mo[nt][k];
+                    pc[C::ROWS * (DMAX + 1) + row] = sum;
                 }
             }
-        if (!whole && lane == 0) slots[warp * 2 + (sb < wb ? 0 : 1)] = Slot{sb, se, b, hg};
-        u = sb + last;
         __syncwarp();
+        if (whole)
+            join_pieces<C::ROWS, DMAX>(p, [&](int) { return pc; }, 1, b, hg, nullptr, lane, 32);
+        else if (lane == 0)
+            slots[warp * 2 + (sb < wb ? 0 : 1)] = Slot{sb, se, b, hg};
+        __syncwarp();
+        u = min(se, we);
+        sb = se;
+        if (++hg == HG && u < we) {
+            hg = 0;
+            do ++b; while (prefix[b + 1] == prefix[b]);
+            steps = prefix[b + 1] - prefix[b];
+        }
     }
     __syncthreads();
 
     // the warps' pieces of each segment, in order
-    bool open = false;
+    int n_open = 0;
+#pragma unroll 1
     for (int i = 0; i < 2 * C::WARPS;) {
         if (slots[i].b < 0) {
             ++i;
             continue;
         }
         const Slot sl = slots[i];
-        int idx[2 * C::WARPS];
+        // a warp leaves at most one piece of a segment: in its second place if
+        // the segment starts there, in the first otherwise
+        const int i0 = i;
         int n = 0;
         for (; i < 2 * C::WARPS; ++i) {
             if (slots[i].b < 0) continue;
             if (slots[i].begin != sl.begin) break;
-            idx[n++] = i;
+            ++n;
         }
         const bool inside = sl.begin >= lo && sl.end <= hi;
         float *to = inside ? nullptr : p.part + (size_t)(2 * blockIdx.x + (sl.begin < lo ? 0 : 1)) * C::PIECE;
-        open |= !inside;
-        join_pieces<false, C::ROWS, DMAX, C::THREADS>(
-            p, [&](int k) { return pieces + idx[k] * C::PIECE; }, n, sl.b, sl.hg, C::kOff, to);
+        if (!inside) {
+            if (tid == 0) s_open[n_open] = sl;
+            ++n_open;
+        }
+        join_pieces<C::ROWS, DMAX>(
+            p, [&](int k) { return pieces + (k == 0 ? i0 : (i0 & ~1) + 2 * k) * C::PIECE; }, n, sl.b, sl.hg, to, tid,
+            C::THREADS);
     }
-    if (!open) return;
+    if (n_open == 0) return;
 
-    // segments shared with other blocks: the last block to arrive joins them
+    // Segments shared with other blocks: the last block to arrive joins them.
     __threadfence();
     __syncthreads();
-    __shared__ Slot s_open[2];
-    if (tid == 0) {
-        int k = 0;
-        for (int i = 0; i < 2 * C::WARPS; ++i) {
-            const Slot &sl = slots[i];
-            if (sl.b < 0 || (sl.begin >= lo && sl.end <= hi)) continue;
-            if (k > 0 && s_open[k - 1].begin == sl.begin) continue;
-            s_open[k] = sl;
-            // blocks sharing it: those whose run holds its first and its last step
-            const int c0 = (int)(((sl.begin + 1) * nblk - 1) / U), c1 = (int)((sl.end * nblk - 1) / U);
-            int *cnt = p.arrived + sl.b * HG + sl.hg;
-            if (atomicAdd(cnt, 1) == c1 - c0) {
-                *cnt = 0;  // for the next launch
-                s_join[k] = c0;
-            }
-            ++k;
+    if (tid < n_open) {
+        const Slot &sl = s_open[tid];
+        const int n = (int)((sl.end - 1) / per - sl.begin / per);
+        int *cnt = p.arrived + sl.b * HG + sl.hg;
+        if (atomicAdd(cnt, 1) == n) {
+            *cnt = 0;  // for the next launch
+            s_join[tid] = n;
         }
         __threadfence();
     }
     __syncthreads();
-    for (int k = 0; k < 2; ++k) {
-        const int c0 = s_join[k];
-        if (c0 < 0) continue;
+    for (int k = 0; k < n_open; ++k) {
+        const int n = s_join[k] + 1;
+        if (n == 0) continue;
+        // A block's piece of a segment lies in its second place if the segment
+        // starts there, in the first otherwise.  Maxima and sums come first, in
+        // one round trip, as weights into shared memory (the warps' pieces have
+        // been read); then the sums of O, eight pieces in flight.
         const Slot sl = s_open[k];
-        const int n = (int)((sl.end * nblk - 1) / U) - c0 + 1;
-        join_pieces<true, C::ROWS, DMAX, C::THREADS>(
-            p,
-            [&](int i) {
-                const long long blo = (long long)(c0 + i) * U / nblk;
-                return p.part + (size_t)(2 * (c0 + i) + (sl.begin < blo ? 0 : 1)) * C::PIECE;
-            },
-            n, sl.b, sl.hg, C::kOff, nullptr);
+        const int c0 = (int)(sl.begin / per);
+        auto piece = [&](int i) { return p.part + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * C::PIECE; };
+        float *wm = pieces, *ws = pieces + n * C::ROWS;
+        for (int e = tid; e < n * C::ROWS; e += C::THREADS) {
+            const float *q = piece(e / C::ROWS) + C::ROWS * DMAX + e % C::ROWS;
+            wm[e] = __ldcg(q);
+            ws[e] = __ldcg(q + C::ROWS);
+        }
+        __syncthreads();
+        const int kvh = sl.hg / p.n_groups, h0 = kvh * p.group + (sl.hg - kvh * p.n_groups) * C::ROWS;
+        const int heads = min(C::ROWS, (kvh + 1) * p.group - h0);
+#pragma unroll 1
+        for (int e = tid; e < heads * (DMAX / 4); e += C::THREADS) {
+            const int row = e / (DMAX / 4), d = 4 * (e - row * (DMAX / 4));
+            if (d >= p.v_dim) continue;
+            float top = kFloor, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < n; ++i) top = fmaxf(top, wm[i * C::ROWS + row]);
+#pragma unroll 1
+            for (int i0 = 0; i0 < n; i0 += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i0 + i < n) v[i] = __ldcg(reinterpret_cast<const float4 *>(piece(i0 + i) + row * DMAX + d));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (i0 + i >= n) break;
+                    const float f = exp2_fast(wm[(i0 + i) * C::ROWS + row] - top);
+                    sum = fmaf(ws[(i0 + i) * C::ROWS + row], f, sum);
+                    x[0] = fmaf(v[i].x, f, x[0]);
+                    x[1] = fmaf(v[i].y, f, x[1]);
+                    x[2] = fmaf(v[i].z, f, x[2]);
+                    x[3] = fmaf(v[i].w, f, x[3]);
+                }
+            }
+            const bool none = sum == 0.f;
+            const float inv = none ? 0.f : a.v_scale / sum;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = none ? 0.f : x[j] * inv;
+            store_out(p, sl.b * a.out_stride_b + (h0 + row) * a.out_stride_h + d, x);
+            if (d == 0 && a.lse)
+                a.lse[(int64_t)sl.b * p.n_heads + h0 + row] =
+                    none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        }
+        __syncthreads();
     }
 }
 

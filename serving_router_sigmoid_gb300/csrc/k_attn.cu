@@ -56,8 +56,11 @@ cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaSt
     p.k_page = a.kc_stride_page * ce;
     p.k_tok = a.kc_stride_tok * ce;
     p.k_head = a.kc_stride_head * ce;
+    p.k_tok8 = 8 * p.k_tok;
+    p.n_pages = (uint32_t)a.n_pages;
     p.v_page = a.vc_stride_page * ce;
     p.v_tok = a.vc_stride_tok * ce;
+    p.v_tok8 = 8 * p.v_tok;
     p.v_head = a.vc_stride_head * ce;
     p.by_page = FastDiv((uint32_t)a.page_size);
     p.part = h.part;
