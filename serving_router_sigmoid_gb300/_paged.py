@@ -60,12 +60,15 @@ def _device(device) -> int:
     return torch.cuda.current_device() if d.index is None else d.index
 
 
-def _here(dev: int, **tensors) -> None:
+def _here(dev: int, *tensors) -> None:
     """Every tensor (None: absent) on CUDA device `dev`, which has to be the current one."""
-    for name, t in tensors.items():
-        if t is not None and (dev < 0 or t.get_device() != dev):
-            raise ValueError(f"{name}: expected a tensor on cuda:{max(dev, 0)} (the library has no CPU path)")
-    if torch.cuda.current_device() != dev:
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected every tensor on cuda:{max(dev, 0)}, got one on {t.device} "
+                             "(the library has no CPU path)")
+    if dev < 0:
+        raise ValueError("expected CUDA tensors (the library has no CPU path)")
+    if torch._C._cuda_getDevice() != dev:
         raise ValueError(f"cuda:{dev} has to be the current device")
 
 
@@ -75,9 +78,11 @@ def _raw(stream, dev: int) -> int:
     return _stream(stream).value or 0
 
 
-def _empty(shape, dtype, dev: int, stream):
-    """A new tensor that belongs to the stream the call runs on."""
+def _empty(shape, like, dtype, dev: int, stream):
+    """A new contiguous tensor that belongs to the stream the call runs on."""
     if stream is None:
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like)  # the cheapest way
         return torch.empty(shape, dtype=dtype, device=dev)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
     with torch.cuda.stream(s):
@@ -99,15 +104,13 @@ def _table(t, rows):
 def _caches(k_cache, v_cache, heads, k_dim, v_dim):
     """MOE_* type of a pair of caches [pages, page_size, heads, dim] (any strides, contiguous rows)."""
     kind = _CACHE.get(k_cache.dtype)
-    if kind is None:
-        raise ValueError(f"k_cache: expected float16, bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
-    for name, c, dim in (("k_cache", k_cache, k_dim), ("v_cache", v_cache, v_dim)):
-        if c is None:
-            continue
-        if c.dtype is not k_cache.dtype or c.dim() != 4 or c.shape[:2] != k_cache.shape[:2] or \
-                c.shape[2:] != (heads, dim) or c.stride(3) != 1:
-            raise ValueError(f"{name}: expected {k_cache.dtype} [pages, page_size, {heads}, {dim}] with contiguous "
-                             f"rows, got {c.dtype} {tuple(c.shape)}")
+    ks = k_cache.shape
+    if kind is None or len(ks) != 4 or ks[2] != heads or ks[3] != k_dim or k_cache.stride(3) != 1 or (
+            v_cache is not None and (v_cache.dtype is not k_cache.dtype or v_cache.stride(-1) != 1 or
+                                     v_cache.shape != (ks[0], ks[1], heads, v_dim))):
+        raise ValueError(f"expected caches [pages, page_size, {heads}, {k_dim}] and [.., .., {heads}, {v_dim}] of one "
+                         f"type (float16, bfloat16 or float8_e4m3fn) with contiguous rows, got "
+                         f"{[None if c is None else (c.dtype, tuple(c.shape)) for c in (k_cache, v_cache)]}")
     return kind
 
 
@@ -136,8 +139,7 @@ class KvPlan:
         n, dev = past_len.shape[0], self._dev
         if n > self.max_requests:
             raise ValueError(f"{n} requests: the plan holds {self.max_requests}")
-        _here(dev, past_len=past_len, new_len=new_len, free_pages=free_pages, free_head=free_head,
-              block_table=block_table)
+        _here(dev, past_len, new_len, free_pages, free_head, block_table)
         _ints("past_len", past_len, (n,))
         _ints("new_len", new_len, (n,))
         _ints("free_pages", free_pages, (free_pages.numel(),))
@@ -183,19 +185,19 @@ class Rope:
         (int64 [>= n]; < 0: not cached), positions int32 [>= n].  Token and
         head strides are free.  E4M3 caches hold x / scale."""
         dev = self._dev
-        _here(dev, q=q, k=k, v=v, positions=positions, slots=slots, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
+        _here(dev, q, k, v, positions, slots, k_cache, v_cache, q_out)
         n, heads, dim = q.shape
         kv_heads = k.shape[1]
         act, v_dim = _ACT.get(q.dtype), 0 if v is None else v.shape[2]
         if act is None:
             raise ValueError(f"q: expected float32, float16 or bfloat16, got {q.dtype}")
         if q_out is None:
-            q_out = _empty((n, heads, dim), q.dtype, dev, stream)
-        for name, t, shape in (("q", q, (n, heads, dim)), ("k", k, (n, kv_heads, dim)), ("v", v, (n, kv_heads, v_dim)),
-                               ("q_out", q_out, (n, heads, dim))):
-            if t is not None and (t.dtype is not q.dtype or t.shape != shape or t.stride(2) != 1):
-                raise ValueError(f"{name}: expected {q.dtype} {shape} with contiguous rows, got {t.dtype} "
-                                 f"{tuple(t.shape)}")
+            q_out = _empty((n, heads, dim), q, q.dtype, dev, stream)
+        if k.dtype is not q.dtype or k.shape != (n, kv_heads, dim) or q.stride(2) != 1 or k.stride(2) != 1 or \
+                (v is not None and (v.dtype is not q.dtype or v.shape != (n, kv_heads, v_dim) or v.stride(2) != 1)) or \
+                q_out.dtype is not q.dtype or q_out.shape != q.shape or q_out.stride(2) != 1:
+            raise ValueError(f"expected q, q_out {(n, heads, dim)}, k {(n, kv_heads, dim)} and v of {q.dtype} with "
+                             f"contiguous rows, got {[None if t is None else (t.dtype, tuple(t.shape)) for t in (q, q_out, k, v)]}")
         if positions.dtype is not torch.int32 or slots.dtype is not torch.int64 or positions.dim() != 1 or \
                 slots.dim() != 1 or positions.shape[0] < n or slots.shape[0] < n or \
                 not positions.is_contiguous() or not slots.is_contiguous():
@@ -251,7 +253,7 @@ class PagedAttention:
         Returns (out [n, heads, v_dim], lse [n, heads] fp32); a request that
         sees no token gets 0 and -inf."""
         dev = self._dev
-        _here(dev, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_len=seq_len, out=out, lse=lse)
+        _here(dev, q, k_cache, v_cache, block_table, seq_len, out, lse)
         n = q.shape[0]
         act = _ACT.get(q.dtype)
         if act is None or q.shape != (n, self.n_heads, self.head_dim) or q.stride(2) != 1:
@@ -263,11 +265,11 @@ class PagedAttention:
                 not seq_len.is_contiguous():
             raise ValueError(f"seq_len: expected a contiguous int32 tensor of at least {n} entries")
         if out is None:
-            out = _empty((n, self.n_heads, self.v_dim), q.dtype, dev, stream)
+            out = _empty((n, self.n_heads, self.v_dim), q if self.v_dim == self.head_dim else None, q.dtype, dev, stream)
         elif out.dtype is not q.dtype or out.shape != (n, self.n_heads, self.v_dim) or out.stride(2) != 1:
             raise ValueError(f"out: expected {q.dtype} {(n, self.n_heads, self.v_dim)} with contiguous rows")
         if lse is None:
-            lse = _empty((n, self.n_heads), torch.float32, dev, stream)
+            lse = _empty((n, self.n_heads), None, torch.float32, dev, stream)
         else:
             _ints("lse", lse, (n, self.n_heads), torch.float32)
         qs, os, ks, vs = q.stride(), out.stride(), k_cache.stride(), v_cache.stride()
@@ -291,7 +293,7 @@ def block_norm(x, y=None, w_post=None, gate=None, w_pre=None, alpha=1.0, beta=1.
     the second norm (default: when w_pre or `normed` is given; with w_pre None
     its weight is 1); without it normed is None.  out may be x, normed may be y."""
     dev = x.get_device()
-    _here(dev, x=x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, out=out, normed=normed)
+    _here(dev, x, y, w_post, gate, w_pre, out, normed)
     act = _ACT.get(x.dtype)
     if act is None or x.dim() != 2:
         raise ValueError(f"x: expected float32, float16 or bfloat16 [n, dim], got {x.dtype} {tuple(x.shape)}")
@@ -303,16 +305,17 @@ def block_norm(x, y=None, w_post=None, gate=None, w_pre=None, alpha=1.0, beta=1.
     if not norm and (w_pre is not None or normed is not None):
         raise ValueError("norm=False takes neither w_pre nor normed")
     if out is None:
-        out = _empty((n, dim), x.dtype, dev, stream)
+        out = _empty((n, dim), x, x.dtype, dev, stream)
     if normed is None and norm:
-        normed = _empty((n, dim), x.dtype, dev, stream)
-    for name, t in (("x", x), ("y", y), ("out", out), ("normed", normed)):
-        if t is not None and (t.dtype is not x.dtype or t.shape != x.shape or (dim > 1 and t.stride(1) != 1)):
-            raise ValueError(f"{name}: expected {x.dtype} {(n, dim)} with contiguous rows, got {t.dtype} "
+        normed = _empty((n, dim), x, x.dtype, dev, stream)
+    shape, dt = x.shape, x.dtype
+    for t in (x, y, out, normed):
+        if t is not None and (t.dtype is not dt or t.shape != shape or (dim > 1 and t.stride(1) != 1)):
+            raise ValueError(f"expected x, y, out and normed {dt} {(n, dim)} with contiguous rows, got {t.dtype} "
                              f"{tuple(t.shape)}")
-    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
-        if w is not None:
-            _ints(name, w, (dim,), torch.float32)
+    for w in (w_post, w_pre):
+        if w is not None and (w.dtype is not torch.float32 or w.shape != (dim,) or not w.is_contiguous()):
+            raise ValueError(f"expected w_post and w_pre float32 [{dim}], got {w.dtype} {tuple(w.shape)}")
     gt = gd = 0
     if gate is not None:
         if gate.dtype is not x.dtype or gate.dim() != 2 or gate.shape[0] not in (1, n) or gate.shape[1] not in (1, dim):

@@ -57,6 +57,17 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     return r;
 }
 
+// 16 bytes read once: past L1 (not through the read-only path, so that an output
+// may take the place of its input).
+__device__ __forceinline__ uint4 ld_once16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // N consecutive elements <-> fp32 registers, in vector accesses of up to 16
 // bytes (the caller guarantees the alignment of N elements, at most 16 bytes).
 template <int N>
@@ -64,8 +75,9 @@ __device__ __forceinline__ void load_vec(const float *p, float (&v)[N]) {
     static_assert(N % 4 == 0, "");
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-        const float4 w = *reinterpret_cast<const float4 *>(p + i);
-        v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
+        const uint4 w = ld_once16(p + i);
+        v[i] = __uint_as_float(w.x); v[i + 1] = __uint_as_float(w.y);
+        v[i + 2] = __uint_as_float(w.z); v[i + 3] = __uint_as_float(w.w);
     }
 }
 __device__ __forceinline__ float2 half_pair(uint32_t w, __half) {
@@ -87,7 +99,7 @@ __device__ __forceinline__ void load_vec(const H *p, float (&v)[N]) {
     static_assert(N % 8 == 0, "");
 #pragma unroll
     for (int i = 0; i < N; i += 8) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p + i);
+        const uint4 w = ld_once16(p + i);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -23,10 +23,17 @@ __device__ __forceinline__ float block_sum(float v, float *red, int nw) {
     return r;
 }
 
+// 1 / (1 + e^-x), within 6 ulp; for 16-bit types with the fast exponential,
+// whose error (2^-22 and 2^-23 |x|) their rounding hides.
+template <int DT>
+__device__ __forceinline__ float sigmoid(float x) {
+    return __fdividef(1.f, 1.f + (DT == MOE_F32 ? expf(-x) : __expf(-x)));
+}
+
 // V elements per access (8 or 4: aligned 16-byte pieces, 1: any alignment),
 // M accesses per thread.
-template <int DT, int V, int M>
-__global__ void __launch_bounds__(V == 8 ? 512 : 1024) block_norm_kernel(const __grid_constant__ MoeNormArgs a) {
+template <int DT, int V, int M, bool EARLY>
+__global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && M == 4 && !EARLY ? 2 : 1) block_norm_kernel(const __grid_constant__ MoeNormArgs a) {
     using A = typename Elem<DT>::type;
     __shared__ float red[2][32];
     const int nw = blockDim.x >> 5;
@@ -43,7 +50,14 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) block_norm_kernel(const _
     };
     auto ldw = [](const float *p, float(&v)[V]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = __ldg(p + j);
+        for (int j = 0; j < V; j += V == 1 ? 1 : 4) {
+            if constexpr (V == 1) {
+                v[j] = __ldg(p + j);
+            } else {
+                const float4 w = __ldg(reinterpret_cast<const float4 *>(p + j));
+                v[j] = w.x; v[j + 1] = w.y; v[j + 2] = w.z; v[j + 3] = w.w;
+            }
+        }
     };
     auto st = [](A *p, const float(&v)[V]) {
         if constexpr (V == 1) from_f32(v[0], *p);
@@ -51,53 +65,67 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) block_norm_kernel(const _
     };
 
     float r[M][V], u[M][V];
+    float wp[EARLY ? M : 1][V], wn[EARLY ? M : 1][V];
+    auto weights = [&](const float *w, float(&v)[V], int d) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = 1.f;
+        if (w && d < a.dim) ldw(w + d, v);
+    };
     float sq = 0.f;
+    const float g1 = g && a.gate_stride_d == 0 ? to_f32(*g) : 1.f;
+    {
+        float f[M][V];
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-        const int d = (m * blockDim.x + threadIdx.x) * V;
+        for (int m = 0; m < M; ++m) {
+            const int d = (m * blockDim.x + threadIdx.x) * V;
 #pragma unroll
-        for (int j = 0; j < V; ++j) r[m][j] = u[m][j] = 0.f;
-        if (d < a.dim) {
-            ld(x + d, r[m]);
-            if (y) ld(y + d, u[m]);
+            for (int j = 0; j < V; ++j) r[m][j] = u[m][j] = 0.f, f[m][j] = g1;
+            if (d < a.dim) {
+                if (y) ld(y + d, u[m]);
+                if (g && a.gate_stride_d) ld(g + d, f[m]);
+                if (EARLY) ld(x + d, r[m]);
+            }
+            if constexpr (EARLY) {
+                weights(a.w_post, wp[m], d);
+                weights(nrm ? a.w_pre : nullptr, wn[m], d);
+            }
         }
-    }
-    float post = 1.f;
-    if (y && a.w_post) {
+        // u takes gate and weight before its norm is known: what waits for the
+        // sum is one factor
 #pragma unroll
-        for (int m = 0; m < M; ++m)
+        for (int m = 0; m < M; ++m) {
+            const int d = (m * blockDim.x + threadIdx.x) * V;
 #pragma unroll
             for (int j = 0; j < V; ++j) sq = fmaf(u[m][j], u[m][j], sq);
-        post = rsqrtf(block_sum(sq, red[0], nw) / (float)a.dim + a.eps);
+            if (g && a.gate_sigmoid) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) f[m][j] = sigmoid<DT>(f[m][j]);
+            }
+            float(&w)[V] = wp[EARLY ? m : 0];
+            if constexpr (!EARLY) weights(a.w_post, w, d);
+#pragma unroll
+            for (int j = 0; j < V; ++j) u[m][j] *= f[m][j] * w[j];
+        }
     }
-    const float g1 = g && a.gate_stride_d == 0 ? to_f32(*g) : 1.f;
+    if constexpr (!EARLY) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const int d = (m * blockDim.x + threadIdx.x) * V;
+            if (d < a.dim) ld(x + d, r[m]);
+        }
+    }
+    float post = a.beta;
+    if (y && a.w_post) post *= rsqrtf(block_sum(sq, red[0], nw) / (float)a.dim + a.eps);
     sq = 0.f;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         const int d = (m * blockDim.x + threadIdx.x) * V;
         if (d >= a.dim) continue;
-        if (y) {
-            float f[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) f[j] = g1;
-            if (g && a.gate_stride_d) ld(g + d, f);
-            if (g && a.gate_sigmoid)
-#pragma unroll
-                for (int j = 0; j < V; ++j) f[j] = __fdiv_rn(1.f, 1.f + expf(-f[j]));
-            if (a.w_post) {
-                float w[V];
-                ldw(a.w_post + d, w);
-#pragma unroll
-                for (int j = 0; j < V; ++j) u[m][j] *= post * w[j];
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) r[m][j] = fmaf(a.beta * f[j], u[m][j], a.alpha * r[m][j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) r[m][j] *= a.alpha;
+        for (int j = 0; j < V; ++j) {
+            r[m][j] = fmaf(post, u[m][j], a.alpha * r[m][j]);
+            sq = fmaf(r[m][j], r[m][j], sq);
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) sq = fmaf(r[m][j], r[m][j], sq);
         st(out + d, r[m]);
     }
     if (!nrm) return;
@@ -106,56 +134,212 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) block_norm_kernel(const _
     for (int m = 0; m < M; ++m) {
         const int d = (m * blockDim.x + threadIdx.x) * V;
         if (d >= a.dim) continue;
-        float w[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) w[j] = 1.f;
-        if (a.w_pre) ldw(a.w_pre + d, w);
+        float(&w)[V] = wn[EARLY ? m : 0];
+        if constexpr (!EARLY) weights(a.w_pre, w, d);
 #pragma unroll
         for (int j = 0; j < V; ++j) r[m][j] *= pre * w[j];
         st(nrm + d, r[m]);
     }
 }
 
-template <int DT, int V>
-cudaError_t launch(const MoeNormArgs &a, cudaStream_t s) {
-    // accesses per thread: as few as 512 threads allow, then 1024 threads
-    const int acc = (a.dim + V - 1) / V;
-    int m = 1;
-    while (m < 16 && acc > m * (m < 4 ? 512 : 1024)) m *= 2;
-    int threads = ((acc + m - 1) / m + 31) / 32 * 32;
-    switch (m) {
-        case 1: block_norm_kernel<DT, V, 1><<<a.n_tokens, threads, 0, s>>>(a); break;
-        case 2: block_norm_kernel<DT, V, 2><<<a.n_tokens, threads, 0, s>>>(a); break;
-        case 4: block_norm_kernel<DT, V, 4><<<a.n_tokens, threads, 0, s>>>(a); break;
-        default:
-            if constexpr (V == 1) {
-                if (m == 8) block_norm_kernel<DT, V, 8><<<a.n_tokens, threads, 0, s>>>(a);
-                else block_norm_kernel<DT, V, 16><<<a.n_tokens, threads, 0, s>>>(a);
+__device__ __forceinline__ void copy16(void *smem, const void *gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
+                 : "memory");
+}
+
+// The same for many rows of at least 8 KB: one block per SM goes through rows
+// blockIdx, + gridDim, ...; a ring of row copies in shared memory keeps
+// `stages` - 1 rows on their way while one is computed.  A thread copies just
+// the pieces it will read, so its own wait_group is all the ring needs.  Both
+// weights stay in registers.
+constexpr int kRing = 220 * 1024;
+template <int DT, int M>
+__global__ void __launch_bounds__(512, 1)
+    block_norm_ring_kernel(const __grid_constant__ MoeNormArgs a, int stages) {
+    using A = typename Elem<DT>::type;
+    constexpr int V = DT == MOE_F32 ? 4 : 8;
+    extern __shared__ __align__(16) uint4 ring[];
+    __shared__ float red[2][32];
+    const int nw = blockDim.x >> 5, n_arr = 1 + (a.y != nullptr) + (a.gate != nullptr && a.gate_stride_d != 0);
+    auto slot = [&](int st, int arr, int m) -> uint4 & {
+        return ring[((st * n_arr + arr) * M + m) * blockDim.x + threadIdx.x];
+    };
+    auto fetch = [&](int64_t t, int st) {
+        if (t < a.n_tokens) {
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const int d = (m * blockDim.x + threadIdx.x) * V;
+                if (d >= a.dim) continue;
+                copy16(&slot(st, 0, m), static_cast<const A *>(a.x) + t * a.x_stride + d);
+                if (a.y) copy16(&slot(st, 1, m), static_cast<const A *>(a.y) + t * a.y_stride + d);
+                if (n_arr == 3) copy16(&slot(st, 2, m), static_cast<const A *>(a.gate) + t * a.gate_stride_t + d);
             }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto get = [&](int st, int arr, int m, float(&v)[V]) {
+        const uint4 w = slot(st, arr, m);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (V == 4) {
+                v[j] = __uint_as_float(u[j]);
+            } else {
+                const float2 f = half_pair(u[j], A());
+                v[2 * j] = f.x;
+                v[2 * j + 1] = f.y;
+            }
+        }
+    };
+    // three copies ahead at most: wait_group takes a constant
+    for (int i = 0; i < stages - 1; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    float wp[M][V], wn[M][V];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const int d = (m * blockDim.x + threadIdx.x) * V;
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            float4 p = make_float4(1.f, 1.f, 1.f, 1.f), n = p;
+            if (a.w_post && d < a.dim) p = __ldg(reinterpret_cast<const float4 *>(a.w_post + d + j));
+            if (a.w_pre && d < a.dim) n = __ldg(reinterpret_cast<const float4 *>(a.w_pre + d + j));
+            wp[m][j] = p.x; wp[m][j + 1] = p.y; wp[m][j + 2] = p.z; wp[m][j + 3] = p.w;
+            wn[m][j] = n.x; wn[m][j + 1] = n.y; wn[m][j + 2] = n.z; wn[m][j + 3] = n.w;
+        }
+    }
+    int st = 0;
+    for (int64_t t = blockIdx.x; t < a.n_tokens; t += gridDim.x) {
+        const float g1 = a.gate && a.gate_stride_d == 0
+                             ? to_f32(static_cast<const A *>(a.gate)[t * a.gate_stride_t]) : 1.f;
+        if (stages == 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else if (stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 2;" ::: "memory");
+        float u[M][V], r[M][V];
+        float sq = 0.f;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const int d = (m * blockDim.x + threadIdx.x) * V;
+            float f[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) u[m][j] = r[m][j] = 0.f, f[j] = g1;
+            if (d < a.dim) {
+                get(st, 0, m, r[m]);
+                if (a.y) get(st, 1, m, u[m]);
+                if (n_arr == 3) get(st, 2, m, f);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                sq = fmaf(u[m][j], u[m][j], sq);
+                if (a.gate && a.gate_sigmoid) f[j] = sigmoid<DT>(f[j]);
+                u[m][j] *= f[j] * wp[m][j];
+            }
+        }
+        // this thread's pieces are read: the next row into the slot behind
+        fetch(t + (int64_t)(stages - 1) * gridDim.x, st == 0 ? stages - 1 : st - 1);
+        st = st + 1 == stages ? 0 : st + 1;
+        float post = a.beta;
+        if (a.y && a.w_post) post *= rsqrtf(block_sum(sq, red[0], nw) / (float)a.dim + a.eps);
+        sq = 0.f;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const int d = (m * blockDim.x + threadIdx.x) * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                r[m][j] = fmaf(post, u[m][j], a.alpha * r[m][j]);
+                sq = fmaf(r[m][j], r[m][j], sq);
+            }
+            if (d < a.dim) store_vec(static_cast<A *>(a.out) + t * a.out_stride + d, r[m]);
+        }
+        if (a.normed) {
+            const float pre = rsqrtf(block_sum(sq, red[1], nw) / (float)a.dim + a.eps);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const int d = (m * blockDim.x + threadIdx.x) * V;
+#pragma unroll
+                for (int j = 0; j < V; ++j) r[m][j] *= pre * wn[m][j];
+                if (d < a.dim) store_vec(static_cast<A *>(a.normed) + t * a.normed_stride + d, r[m]);
+            }
+        }
+        if (!a.normed || !(a.y && a.w_post)) __syncthreads();  // red is written again by the next row
+    }
+}
+
+template <int DT, int M>
+cudaError_t launch_ring(const MoeNormArgs &a, int threads, int stages, size_t smem, int num_sms, cudaStream_t s) {
+    const cudaError_t ce = cudaFuncSetAttribute(block_norm_ring_kernel<DT, M>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+    if (ce != cudaSuccess) return ce;
+    block_norm_ring_kernel<DT, M><<<num_sms, threads, smem, s>>>(a, stages);
+    return cudaGetLastError();
+}
+
+// One block a row, m accesses a thread.
+template <int DT, int V, bool EARLY>
+cudaError_t launch_rows(const MoeNormArgs &a, int m, int threads, cudaStream_t s) {
+    switch (m) {
+        case 1: block_norm_kernel<DT, V, 1, EARLY><<<a.n_tokens, threads, 0, s>>>(a); break;
+        case 2: block_norm_kernel<DT, V, 2, EARLY><<<a.n_tokens, threads, 0, s>>>(a); break;
+        case 4:
+            if constexpr (!EARLY || V == 4) block_norm_kernel<DT, V, 4, EARLY><<<a.n_tokens, threads, 0, s>>>(a);
+            break;
+        case 8:
+            if constexpr (!EARLY && V <= 4) block_norm_kernel<DT, V, 8, EARLY><<<a.n_tokens, threads, 0, s>>>(a);
+            break;
+        default:
+            if constexpr (V == 1) block_norm_kernel<DT, V, 16, EARLY><<<a.n_tokens, threads, 0, s>>>(a);
     }
     return cudaGetLastError();
 }
 
+// The form of the kernel, from sizes alone.  Measured on fp32 / bf16 rows with
+// a full gate (us):
+//   weights early     1 x 6144: 4.0 against 4.3; 1216 x 4096 fp32: 17.8 against
+//                     19.8; but 304 x 6144: 9.2 against 7.5 (registers: one
+//                     block per SM), so where a thread has few pieces or there
+//                     is at most one row an SM
+//   ring of copies    2048 x 6144 fp32: 40.4 against 46.4; 1216 x 8192 bf16: 24.0
+//                     against 35.1; but 304 x 6144: 9.5 against 7.5 and rows of
+//                     4 KB 33.9 against 17.8, so from 8 rows an SM, of more than 8 KB
 template <int DT>
-cudaError_t launch_dt(const MoeNormArgs &a, cudaStream_t s) {
+cudaError_t launch_dt(const MoeNormArgs &a, int num_sms, cudaStream_t s) {
     constexpr int V = DT == MOE_F32 ? 4 : 8;
     const auto on = [](const void *p, int64_t stride) {
         return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % V == 0;
     };
+    const bool full_gate = a.gate && a.gate_stride_d != 0;
     const bool vec = a.dim % V == 0 && on(a.x, a.x_stride) && on(a.y, a.y ? a.y_stride : 0) &&
                      on(a.out, a.out_stride) && on(a.normed, a.normed ? a.normed_stride : 0) &&
-                     on(a.w_post, 0) && on(a.w_pre, 0) &&
-                     (!a.gate || a.gate_stride_d == 0 || on(a.gate, a.gate_stride_t));
-    return vec ? launch<DT, V>(a, s) : launch<DT, 1>(a, s);
+                     on(a.w_post, 0) && on(a.w_pre, 0) && (!full_gate || on(a.gate, a.gate_stride_t));
+    const int most = vec ? 512 : 1024;  // threads a block
+    const int acc = vec ? a.dim / V : a.dim;
+    if (vec && acc > 512 && a.n_tokens >= 8 * (int64_t)num_sms) {
+        const int m = (acc + 511) / 512, threads = ((acc + m - 1) / m + 31) / 32 * 32;
+        const size_t row = (size_t)16 * m * threads * (1 + (a.y != nullptr) + full_gate);
+        const int stages = (int)(kRing / row < 4 ? kRing / row : 4);
+        if (stages >= 2 && m <= 4) {
+            if (m == 2) return launch_ring<DT, 2>(a, threads, stages, row * stages, num_sms, s);
+            if (m == 3) return launch_ring<DT, 3>(a, threads, stages, row * stages, num_sms, s);
+            return launch_ring<DT, 4>(a, threads, stages, row * stages, num_sms, s);
+        }
+    }
+    int m = 1;
+    while (acc > m * most) m *= 2;
+    const int threads = ((acc + m - 1) / m + 31) / 32 * 32;
+    if (!vec) return launch_rows<DT, 1, false>(a, m, threads, s);
+    const bool early = m == 1 || (m == 2 && V == 4) || (m * V <= 16 && a.n_tokens <= num_sms);
+    return early ? launch_rows<DT, V, true>(a, m, threads, s) : launch_rows<DT, V, false>(a, m, threads, s);
 }
 
 }  // namespace
 
 cudaError_t launch_block_norm(const MoeNormArgs &a, cudaStream_t s) {
+    int dev = 0, nsm = 0;
+    cudaError_t ce = cudaGetDevice(&dev);
+    if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (ce != cudaSuccess) return ce;
     switch (a.act_type) {
-        case MOE_F32: return launch_dt<MOE_F32>(a, s);
-        case MOE_F16: return launch_dt<MOE_F16>(a, s);
-        default: return launch_dt<MOE_BF16>(a, s);
+        case MOE_F32: return launch_dt<MOE_F32>(a, nsm, s);
+        case MOE_F16: return launch_dt<MOE_F16>(a, nsm, s);
+        default: return launch_dt<MOE_BF16>(a, nsm, s);
     }
 }
 

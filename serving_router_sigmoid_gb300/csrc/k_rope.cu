@@ -25,7 +25,8 @@ struct RopeSplit {
     int tok;           // tokens a block handles
     int per_q, per_v;  // work items of a q / k head and of a v head
     int n_q, n_k, n_v; // work items of a token
-    FastDiv by_token, by_qk, by_v, by_page;
+    int head_slots, v_slots;  // heads a block takes side by side
+    FastDiv by_token, by_qk, by_v, by_heads, by_kv;
 };
 
 __device__ __forceinline__ float2 turn(float a, float b, float2 cs) {
@@ -63,90 +64,158 @@ __device__ __forceinline__ void fill_angles(const MoeRopeArgs &a, int t0, int nt
     }
 }
 
+// Eight consecutive elements as loaded.
+template <int AT>
+struct Piece {
+    using A = typename Elem<AT>::type;
+    uint4 w[AT == MOE_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const A *p) {
+        w[0] = ld_once16(p);
+        if constexpr (AT == MOE_F32) w[1] = ld_once16(p + 4);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (AT == MOE_F32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[4 * i] = __uint_as_float(w[i].x); v[4 * i + 1] = __uint_as_float(w[i].y);
+                v[4 * i + 2] = __uint_as_float(w[i].z); v[4 * i + 3] = __uint_as_float(w[i].w);
+            }
+        } else {
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = half_pair(u[i], A());
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+};
+
 // Rows whose every piece of eight elements is aligned (checked by the host).
-template <int AT, int CT>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ MoeRopeArgs a,
-                                                               const __grid_constant__ RopeSplit w) {
+// A thread keeps one piece of the head (a pair of pieces in the halves layout)
+// and goes through the block's (token, head) pairs, kBatch of them in flight.
+// The angles and the cache rows of the tokens come from shared memory.
+template <int AT, int CT, bool PAIRED>
+__global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const __grid_constant__ MoeRopeArgs a,
+                                                                  const __grid_constant__ RopeSplit w) {
     using A = typename Elem<AT>::type;
     using C = typename Elem<CT>::type;
+    constexpr int kBatch = PAIRED && AT == MOE_F32 ? 1 : 2;
     __shared__ float2 cs[kMaxTok * kMaxHalf];
-    __shared__ long long s_slot[kMaxTok];
+    __shared__ longlong2 row[kMaxTok];  // offsets of the token's rows in the caches; x < 0: not cached
     const int t0 = blockIdx.x * w.tok, nt = min(w.tok, a.n_tokens - t0);
+    const int half = a.rot_dim >> 1, n_rot = PAIRED ? a.rot_dim >> 4 : a.rot_dim >> 3;
+    const int hs = (int)w.by_qk.div(threadIdx.x), j = threadIdx.x - hs * w.per_q;  // head slot, piece
+    const int vh = (int)w.by_v.div(threadIdx.x), vj = threadIdx.x - vh * w.per_v;
+    const bool rotated = j < n_rot, two = PAIRED && rotated;
+    int d = 8 * (rotated ? j : j - n_rot);
+    if (rotated || d >= a.rot_offset) d += rotated ? a.rot_offset : a.rot_dim;
+    const int n_heads = a.n_heads + a.n_kv_heads, end = hs < w.head_slots ? nt * n_heads : 0;
+    const int v_end = vh < w.v_slots ? nt * a.n_kv_heads : 0;
+    const A *q = static_cast<const A *>(a.q) + t0 * a.q_stride_t + d;
+    const A *k = static_cast<const A *>(a.k) + t0 * a.k_stride_t + d;
+    const A *v = static_cast<const A *>(a.v) + t0 * a.v_stride_t + 8 * vj;
+    A *qo = static_cast<A *>(a.q_out) + t0 * a.qo_stride_t + d;
+
+    Piece<AT> x[kBatch], y[PAIRED ? kBatch : 1];
+    auto load = [&](int e0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int e = e0 + i * w.head_slots;
+            if (e >= end) break;
+            const int t = (int)w.by_heads.div(e), h = e - t * n_heads;
+            const A *p = h < a.n_heads ? q + t * a.q_stride_t + h * a.q_stride_h
+                                       : k + t * a.k_stride_t + (h - a.n_heads) * a.k_stride_h;
+            x[i].load(p);
+            if (two) y[PAIRED ? i : 0].load(p + half);
+        }
+    };
+    auto load_v = [&](int e0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int e = e0 + i * w.v_slots;
+            if (e >= v_end) break;
+            const int t = (int)w.by_kv.div(e), h = e - t * a.n_kv_heads;
+            x[i].load(v + t * a.v_stride_t + h * a.v_stride_h);
+        }
+    };
+    // the first rows are on their way while the angles are formed
+    load(hs);
+    if (threadIdx.x < nt) {
+        const long long slot = __ldg(a.slots + t0 + threadIdx.x);
+        longlong2 r = make_longlong2(-1, -1);
+        if (slot >= 0 && slot < (long long)a.n_pages * a.page_size) {
+            const long long page = slot / a.page_size, at = slot - page * a.page_size;
+            r.x = page * a.kc_stride_page + at * a.kc_stride_tok;
+            r.y = page * a.vc_stride_page + at * a.vc_stride_tok;
+        }
+        row[threadIdx.x] = r;
+    }
     fill_angles(a, t0, nt, cs);
-    if (threadIdx.x < nt) s_slot[threadIdx.x] = a.slots[t0 + threadIdx.x];
     __syncthreads();
-    const int half = a.rot_dim >> 1;
-    const int per_tok = w.n_q + w.n_k + w.n_v;
-    const long long n_slots = (long long)a.n_pages * a.page_size;
-    for (int i = threadIdx.x; i < nt * per_tok; i += kThreads) {
-        const int t = (int)w.by_token.div(i);
-        int j = i - t * per_tok;
-        const bool is_q = j < w.n_q;
-        const bool is_v = j >= w.n_q + w.n_k;
-        long long page = 0;
-        int at = 0;
-        if (!is_q) {
-            const long long slot = s_slot[t];
-            if (slot < 0 || slot >= n_slots) continue;
-            // slots below 2^31 by multiplication, others by a 64-bit division
-            page = slot < 0x80000000ll ? (long long)w.by_page.div((uint32_t)slot) : slot / a.page_size;
-            at = (int)(slot - page * a.page_size);
-        }
-        const int tok = t0 + t;
-        if (is_v) {
-            j -= w.n_q + w.n_k;
-            const int h = (int)w.by_v.div(j), d = 8 * (j - h * w.per_v);
-            float x[8];
-            load_vec(static_cast<const A *>(a.v) + tok * a.v_stride_t + h * a.v_stride_h + d, x);
-            CacheStore<CT>::put8(static_cast<C *>(a.v_cache) + page * a.vc_stride_page + at * a.vc_stride_tok +
-                                     h * a.vc_stride_head + d,
-                                 x, a.v_scale);
-            continue;
-        }
-        if (!is_q) j -= w.n_q;
-        const int h = (int)w.by_qk.div(j);
-        j -= h * w.per_q;
-        const A *src = is_q ? static_cast<const A *>(a.q) + tok * a.q_stride_t + h * a.q_stride_h
-                            : static_cast<const A *>(a.k) + tok * a.k_stride_t + h * a.k_stride_h;
-        A *qo = static_cast<A *>(a.q_out) + tok * a.qo_stride_t + h * a.qo_stride_h;
-        C *kc = static_cast<C *>(a.k_cache) + page * a.kc_stride_page + at * a.kc_stride_tok + h * a.kc_stride_head;
-        auto put = [&](int d, float(&x)[8]) {
-            if (is_q) store_vec(qo + d, x);
-            else CacheStore<CT>::put8(kc + d, x, a.k_scale);
-        };
-        // items: the rotated pieces first, then the pieces that pass through
-        const int n_rot = a.interleaved ? a.rot_dim >> 3 : a.rot_dim >> 4;
-        const float2 *c = cs + t * half;
-        if (j >= n_rot) {
-            int d = 8 * (j - n_rot);
-            if (d >= a.rot_offset) d += a.rot_dim;
-            float x[8];
-            load_vec(src + d, x);
-            put(d, x);
-        } else if (a.interleaved) {
-            const int d = a.rot_offset + 8 * j;
-            float x[8];
-            load_vec(src + d, x);
+#pragma unroll 1
+    for (int e0 = hs; e0 < end; e0 += kBatch * w.head_slots) {
+        Piece<AT> cx[kBatch], cy[PAIRED ? kBatch : 1];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const float2 r = turn(x[2 * p], x[2 * p + 1], c[4 * j + p]);
-                x[2 * p] = r.x;
-                x[2 * p + 1] = r.y;
-            }
-            put(d, x);
-        } else {
-            const int d = a.rot_offset + 8 * j;
-            float x[8], y[8];
-            load_vec(src + d, x);
-            load_vec(src + d + half, y);
+        for (int i = 0; i < kBatch; ++i) {
+            cx[i] = x[i];
+            if (PAIRED) cy[i] = y[i];
+        }
+        load(e0 + kBatch * w.head_slots);
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const float2 r = turn(x[p], y[p], c[8 * j + p]);
-                x[p] = r.x;
-                y[p] = r.y;
+        for (int i = 0; i < kBatch; ++i) {
+            const int e = e0 + i * w.head_slots;
+            if (e >= end) break;
+            const int t = (int)w.by_heads.div(e), h = e - t * n_heads;
+            float u[8], z[8];
+            cx[i].get(u);
+            if (two) cy[PAIRED ? i : 0].get(z);
+            if (rotated) {
+                const float2 *c = cs + t * half + (PAIRED ? 8 : 4) * j;
+                if constexpr (PAIRED) {
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        const float2 r = turn(u[m], z[m], c[m]);
+                        u[m] = r.x;
+                        z[m] = r.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const float2 r = turn(u[2 * m], u[2 * m + 1], c[m]);
+                        u[2 * m] = r.x;
+                        u[2 * m + 1] = r.y;
+                    }
+                }
             }
-            put(d, x);
-            put(d + half, y);
+            if (h < a.n_heads) {
+                A *p = qo + t * a.qo_stride_t + h * a.qo_stride_h;
+                store_vec(p, u);
+                if (two) store_vec(p + half, z);
+            } else if (row[t].x >= 0) {
+                C *p = static_cast<C *>(a.k_cache) + row[t].x + (h - a.n_heads) * a.kc_stride_head + d;
+                CacheStore<CT>::put8(p, u, a.k_scale);
+                if (two) CacheStore<CT>::put8(p + half, z, a.k_scale);
+            }
+        }
+    }
+    load_v(vh);
+#pragma unroll 1
+    for (int e0 = vh; e0 < v_end; e0 += kBatch * w.v_slots) {
+        Piece<AT> cx[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) cx[i] = x[i];
+        load_v(e0 + kBatch * w.v_slots);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int e = e0 + i * w.v_slots;
+            if (e >= v_end) break;
+            const int t = (int)w.by_kv.div(e), h = e - t * a.n_kv_heads;
+            if (row[t].x < 0) continue;
+            float u[8];
+            cx[i].get(u);
+            CacheStore<CT>::put8(static_cast<C *>(a.v_cache) + row[t].y + h * a.vc_stride_head + 8 * vj, u, a.v_scale);
         }
     }
 }
@@ -214,16 +283,27 @@ cudaError_t launch(const MoeRopeArgs &a, bool fast, int num_sms, cudaStream_t s)
     w.n_q = a.n_heads * w.per_q;
     w.n_k = a.n_kv_heads * w.per_q;
     w.n_v = a.n_kv_heads * w.per_v;
-    // enough blocks for four per SM first, then more tokens a block
-    const int64_t per = a.n_tokens / (4 * (int64_t)num_sms);
-    w.tok = per < 1 ? 1 : per > kMaxTok ? kMaxTok : (int)per;
+    // tokens a block: the fewest in a row on one of the 3 blocks an SM holds,
+    // waves * tok, and of those the most a block (16384 tokens: 6 waves of 6
+    // against 5 of 8)
+    int64_t best = INT64_MAX;
+    for (int tok = 1; tok <= kMaxTok; ++tok) {
+        const int64_t blocks = (a.n_tokens + tok - 1) / tok, row = (blocks + 3 * num_sms - 1) / (3 * num_sms) * tok;
+        if (row <= best) best = row, w.tok = tok;
+        if (blocks <= num_sms) break;
+    }
     w.by_token = FastDiv((uint32_t)(w.n_q + w.n_k + w.n_v));
     w.by_qk = FastDiv((uint32_t)w.per_q);
     w.by_v = FastDiv((uint32_t)(w.per_v > 0 ? w.per_v : 1));
-    w.by_page = FastDiv((uint32_t)a.page_size);
+    w.by_heads = FastDiv((uint32_t)(a.n_heads + a.n_kv_heads));
+    w.by_kv = FastDiv((uint32_t)(a.n_kv_heads > 0 ? a.n_kv_heads : 1));
+    w.head_slots = kThreads / w.per_q;
+    w.v_slots = w.per_v > 0 ? kThreads / w.per_v : 0;
     const int grid = (a.n_tokens + w.tok - 1) / w.tok;
-    if (fast)
-        rope_append_kernel<AT, CT><<<grid, kThreads, 0, s>>>(a, w);
+    if (fast && a.interleaved)
+        rope_append_kernel<AT, CT, false><<<grid, kThreads, 0, s>>>(a, w);
+    else if (fast)
+        rope_append_kernel<AT, CT, true><<<grid, kThreads, 0, s>>>(a, w);
     else
         rope_append_any_kernel<AT, CT><<<grid, kThreads, 0, s>>>(a, w);
     return cudaGetLastError();
