@@ -149,8 +149,8 @@ int moe_attn_create(const MoeAttnDesc *d, void **handle_out) {
         delete h;
         return cuda_fail(ce, "kernel attributes");
     }
-    // two pieces a block; one arrival counter a request and head group, zero between calls
-    const size_t part = sizeof(float) * 2 * h->num_sms * piece, cnt = sizeof(int) * (size_t)d->max_requests * groups;
+    // a block's pieces; one arrival counter a request and head group, zero between calls
+    const size_t part = sizeof(float) * h->num_sms * piece, cnt = sizeof(int) * (size_t)d->max_requests * groups;
     if ((ce = cudaMalloc(&h->part, part)) != cudaSuccess || (ce = cudaMalloc(&h->arrived, cnt)) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(h->part);
@@ -196,8 +196,8 @@ int moe_attn_decode(void *handle, const MoeAttnArgs *p, cudaStream_t stream) {
                     (long long)a.n_pages, a.window);
     if ((int64_t)a.max_pages * a.page_size > INT32_MAX)
         return fail(MOE_ERR_SHAPE, "max_pages * page_size must stay below 2^31");
-    if (a.n_requests * ((int64_t)a.max_pages * a.page_size / 16 + 2) > INT32_MAX)
-        return fail(MOE_ERR_SHAPE, "n_requests * max_pages * page_size must stay below 2^35");
+    if (!moe::attn_countable(h->d, a))
+        return fail(MOE_ERR_SHAPE, "n_requests * max_pages * page_size * key heads is beyond 2^34 token heads");
     if (a.n_requests > 1 && a.table_stride < a.max_pages)
         return fail(MOE_ERR_SHAPE, "table_stride=%lld is below max_pages=%d", (long long)a.table_stride, a.max_pages);
     if (!is_act(a.act_type) || !is_cache(a.cache_type))

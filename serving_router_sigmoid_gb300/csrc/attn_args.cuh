@@ -157,7 +157,8 @@ struct AttnHandle {
     float *part;
     int *arrived;
 };
-cudaError_t attn_prepare(const MoeAttnDesc &d, size_t *piece_floats, int *groups);
+cudaError_t attn_prepare(const MoeAttnDesc &d, size_t *block_floats, int *groups);
+bool attn_countable(const MoeAttnDesc &d, const MoeAttnArgs &a);
 cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaStream_t s);
 
 }  // namespace moe

@@ -16,22 +16,30 @@ attn::Form form_of(const MoeAttnDesc &d, int cache_type, bool wide) {
 
 }  // namespace
 
-// Piece floats a block may leave, over all forms of a handle, and head groups.
-cudaError_t attn_prepare(const MoeAttnDesc &d, size_t *piece_floats, int *groups) {
-    *piece_floats = 0;
+// Floats of the pieces of a block, over all forms of a handle, and head groups.
+cudaError_t attn_prepare(const MoeAttnDesc &d, size_t *block_floats, int *groups) {
+    *block_floats = 0;
     *groups = 0;
     for (int ct : {MOE_F16, MOE_BF16, MOE_E4M3})
         for (bool wide : {false, true}) {
             const attn::Form f = form_of(d, ct, wide);
             const cudaError_t ce = cudaFuncSetAttribute(reinterpret_cast<const void *>(f.fn),
                                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                        (int)f.smem(MOE_MAX_REQUESTS));
+                                                        (int)f.smem);
             if (ce != cudaSuccess) return ce;
             const int per = (d.n_heads / d.n_kv_heads + f.rows - 1) / f.rows;
-            if ((size_t)f.piece > *piece_floats) *piece_floats = f.piece;
+            const size_t n = (size_t)f.piece * (2 + f.threads / 32);
+            if (n > *block_floats) *block_floats = n;
             if (d.n_kv_heads * per > *groups) *groups = d.n_kv_heads * per;
         }
     return cudaSuccess;
+}
+
+// The line of all segments' steps is counted in 32 bits.
+bool attn_countable(const MoeAttnDesc &d, const MoeAttnArgs &a) {
+    const int64_t steps = (int64_t)a.max_pages * a.page_size / 16 + 2 + attn::kSegCost;
+    const int64_t groups = d.n_kv_heads * ((d.n_heads / d.n_kv_heads + 7) / 8);
+    return steps * a.n_requests <= INT32_MAX / 2 / groups;
 }
 
 cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaStream_t s) {
@@ -65,10 +73,11 @@ cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaSt
     p.by_page = FastDiv((uint32_t)a.page_size);
     p.part = h.part;
     p.arrived = h.arrived;
-    p.min_steps = 2 * (f.threads / 32);  // two steps a warp
+    p.by_hg = FastDiv((uint32_t)(p.n_kv * p.n_groups));
+    p.min_run = f.threads / 32;  // a step a warp
     void *args[] = {&p};
     return cudaLaunchKernel(reinterpret_cast<const void *>(f.fn), dim3(h.num_sms), dim3(f.threads), args,
-                            f.smem(a.n_requests), s);
+                            f.smem, s);
 }
 
 }  // namespace moe
