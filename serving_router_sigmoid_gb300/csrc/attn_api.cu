@@ -220,6 +220,10 @@ int moe_attn_decode(void *handle, const MoeAttnArgs *p, cudaStream_t stream) {
     if (!aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || a.kc_stride_page % per16 || a.kc_stride_tok % per16 ||
         a.kc_stride_head % per16 || a.vc_stride_page % per16 || a.vc_stride_tok % per16 || a.vc_stride_head % per16)
         return fail(MOE_ERR_INVALID_ARG, "cache rows must start on 16 bytes");
+    for (int64_t st : {a.kc_stride_page, a.kc_stride_tok, a.kc_stride_head, a.vc_stride_page, a.vc_stride_tok,
+                       a.vc_stride_head})
+        if (st < 0 || st > INT32_MAX / (int64_t)ce)
+            return fail(MOE_ERR_SHAPE, "cache strides must lie in [0, 2^31) bytes");
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");

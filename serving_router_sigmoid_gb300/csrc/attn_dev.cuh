@@ -50,8 +50,7 @@ struct Params {
     int q16, out16;       // rows of q / out start on 16 bytes
     int by16;             // pages hold whole runs of 16 tokens
     uint32_t n_pages;
-    int64_t k_page, k_tok, k_tok8, k_head;  // strides in bytes (tok8: of 8 tokens)
-    int64_t v_page, v_tok, v_tok8, v_head;
+    int k_page, k_tok, k_head, v_page, v_tok, v_head;  // strides in bytes
     FastDiv by_page, by_hg;
     float *part;          // pieces: two a block, then one a warp
     int *arrived;         // [requests, key heads * groups]
@@ -379,17 +378,21 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                 }
             }
 
-            const char *kb = static_cast<const char *>(a.k_cache) + kvh * p.k_head + g * p.k_tok + c * 16;
+            const char *kb = static_cast<const char *>(a.k_cache) + (int64_t)kvh * p.k_head +
+                             (int64_t)g * p.k_tok + c * 16;
             // Values are copied in another order than they are read in: a copy's
             // eight lanes take 8 pieces of one row (adjacent lanes on different
             // rows would halve its rate: 4.4 against 7.2 TB/s of plain copies),
             // and the pieces of row vc lie turned by 2 vc places, so that neither
             // side meets its own banks.
             const int vc = C::RING ? lane >> 3 : c, vg = C::RING ? lane & 7 : g;
-            const char *vb = static_cast<const char *>(a.v_cache) + kvh * p.v_head + 2 * vc * p.v_tok + vg * C::VB;
+            const char *vb = static_cast<const char *>(a.v_cache) + (int64_t)kvh * p.v_head +
+                             2 * (int64_t)vc * p.v_tok + vg * C::VB;
             auto v_place = [](int gg, int cc) { return cc * 8 + (C::VB == 16 ? gg ^ 2 * cc : gg ^ 4 * (cc >> 1)); };
             // A step is `plain` when all its tokens are seen and lie on whole
             // pages: its rows are then at fixed distances from one address a tile.
+            // (One branch for all of them: a branch a row cost 800 of a step's 3300
+            // cycles.  Pieces beyond the head's size stay the zeros they are.)
             uint4 kr[C::RING ? 1 : C::R][2][C::KCH];
             uint32_t vr[C::RING ? 1 : C::R][4][C::VCH][C::VB / 4];
             if constexpr (!C::RING) {
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
             }
             int page[C::R], at[C::R];
             bool plain = false, holes = false;  // holes: a page that is none came by
-            auto row_at = [&](int t, int r, int row, int64_t sp, int64_t st) -> int64_t {  // from row 0; -1: not seen
+            auto row_at = [&](int t, int r, int row, int sp, int st) -> int64_t {  // from row 0; -1: not seen
                 const int tok = t + 16 * r + row;
                 if (tok < from || tok >= len) return -1;
                 int pg, in;
@@ -423,7 +426,30 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                     holes = true;
                     return -1;
                 }
-                return pg * sp + in * st;
+                return (int64_t)pg * sp + (int64_t)in * st;
+            };
+            // One piece of a key or value row, into the ring or the registers.
+            auto fetch_key = [&](int r, int h, int i, uint32_t dst, const char *k, bool on) {
+                on = on && (4 * i + c) * EC < p.k_dim;
+                if constexpr (C::RING) copy16(dst + ((r * 2 + h) * C::KCH + i) * 512 + lane * 16, k + i * 64, on);
+                else if (on) kr[r][h][i] = ld16(k + i * 64);
+            };
+            auto fetch_value = [&](int r, int k, int i, uint32_t dst, const char *v, bool on) {
+                on = on && (8 * i + vg) * C::VE < p.v_dim;
+                if constexpr (C::RING) {
+                    const uint32_t to = dst + (((r * 4 + k) * C::VCH + i) * 32 + v_place(vg, vc)) * C::VB;
+                    if constexpr (C::VB == 16) copy16(to, v + i * 128, on);
+                    else copy8(to, v + i * 64, on);
+                } else if (on) {
+                    uint32_t(&w)[C::VB / 4] = vr[r][k][i];
+                    if constexpr (C::VB == 16) {
+                        const uint4 x = ld16(v + i * 128);
+                        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                    } else {
+                        const uint2 x = ld8(v + i * 64);
+                        w[0] = x.x; w[1] = x.y;
+                    }
+                }
             };
             auto request_keys = [&](int t, uint32_t dst) {
                 plain = p.by16 && t >= from && t + C::TT <= len;
@@ -441,73 +467,58 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         plain = plain && (uint32_t)page[r] < p.n_pages;
                     }
                 }
+                if (plain) {
+#pragma unroll
+                    for (int r = 0; r < C::R; ++r) {
+                        const char *k = kb + (int64_t)page[r] * p.k_page + (int64_t)at[r] * p.k_tok;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int i = 0; i < C::KCH; ++i) fetch_key(r, h, i, dst, k + h * 8 * (int64_t)p.k_tok, true);
+                    }
+                    return;
+                }
 #pragma unroll
                 for (int r = 0; r < C::R; ++r)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const char *k;
-                        bool on = true;
-                        if (plain) {
-                            k = kb + page[r] * p.k_page + at[r] * p.k_tok + h * p.k_tok8;
-                        } else {
-                            const int64_t off = row_at(t, r, g + 8 * h, p.k_page, p.k_tok);
-                            on = off >= 0;
-                            k = on ? kb + (off - g * p.k_tok) : kb;
-                        }
+                        const int64_t off = row_at(t, r, g + 8 * h, p.k_page, p.k_tok);
 #pragma unroll
                         for (int i = 0; i < C::KCH; ++i) {
-                            const bool in = (4 * i + c) * EC < p.k_dim;
-                            if constexpr (C::RING) {
-                                copy16(dst + ((r * 2 + h) * C::KCH + i) * 512 + lane * 16, k + i * 64, on && in);
-                            } else {
-                                // pieces beyond the head's size stay the zeros they are
-                                if (!plain) kr[r][h][i] = make_uint4(0u, 0u, 0u, 0u);
-                                if (on && in) kr[r][h][i] = ld16(k + i * 64);
-                            }
+                            if constexpr (!C::RING) kr[r][h][i] = make_uint4(0u, 0u, 0u, 0u);
+                            fetch_key(r, h, i, dst, off < 0 ? kb : kb + (off - (int64_t)g * p.k_tok), off >= 0);
                         }
                     }
             };
             auto request_values = [&](int t, uint32_t dst) {
+                if (plain) {
+#pragma unroll
+                    for (int r = 0; r < C::R; ++r) {
+                        const char *v = vb + (int64_t)page[r] * p.v_page + (int64_t)at[r] * p.v_tok;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int i = 0; i < C::VCH; ++i)
+                                fetch_value(r, k, i, dst, v + ((k & 1) + (k >> 1) * 8) * (int64_t)p.v_tok, true);
+                    }
+                    return;
+                }
 #pragma unroll
                 for (int r = 0; r < C::R; ++r)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const char *v;
-                        bool on = true;
-                        if (plain) {
-                            v = vb + page[r] * p.v_page + at[r] * p.v_tok + (k & 1) * p.v_tok + (k >> 1) * p.v_tok8;
-                        } else {
-                            const int64_t off = row_at(t, r, 2 * vc + (k & 1) + 8 * (k >> 1), p.v_page, p.v_tok);
-                            on = off >= 0;
-                            v = on ? vb + (off - 2 * vc * p.v_tok) : vb;
-                        }
+                        const int64_t off = row_at(t, r, 2 * vc + (k & 1) + 8 * (k >> 1), p.v_page, p.v_tok);
 #pragma unroll
                         for (int i = 0; i < C::VCH; ++i) {
-                            const uint32_t to = dst + (((r * 4 + k) * C::VCH + i) * 32 + v_place(vg, vc)) * C::VB;
-                            const bool in = (8 * i + vg) * C::VE < p.v_dim;
                             if constexpr (!C::RING) {
-                                uint32_t(&w)[C::VB / 4] = vr[r][k][i];
-                                if (!plain) {
 #pragma unroll
-                                    for (int j = 0; j < C::VB / 4; ++j) w[j] = 0u;
-                                }
-                                if (on && in) {
-                                    if constexpr (C::VB == 16) {
-                                        const uint4 x = ld16(v + i * 128);
-                                        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-                                    } else {
-                                        const uint2 x = ld8(v + i * 64);
-                                        w[0] = x.x; w[1] = x.y;
-                                    }
-                                }
-                            } else if constexpr (C::VB == 16) {
-                                copy16(to, v + i * 128, on && in);
-                            } else {
-                                copy8(to, v + i * 64, on && in);
+                                for (int j = 0; j < C::VB / 4; ++j) vr[r][k][i][j] = 0u;
                             }
+                            fetch_value(r, k, i, dst, off < 0 ? vb : vb + (off - 2 * (int64_t)vc * p.v_tok), off >= 0);
                         }
                     }
             };
+
             // Query fragments.  fac: what turns an accumulator into a logit in
             // units of log 2.
             uint32_t qf[C::QS ? 1 : C::QFRAGS][2];

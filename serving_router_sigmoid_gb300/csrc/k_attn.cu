@@ -61,15 +61,13 @@ cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaSt
     p.q16 = on16(a.q, a.q_stride_b, a.q_stride_h);
     p.out16 = on16(a.out, a.out_stride_b, a.out_stride_h);
     p.by16 = a.page_size % 16 == 0;
-    p.k_page = a.kc_stride_page * ce;
-    p.k_tok = a.kc_stride_tok * ce;
-    p.k_head = a.kc_stride_head * ce;
-    p.k_tok8 = 8 * p.k_tok;
     p.n_pages = (uint32_t)a.n_pages;
-    p.v_page = a.vc_stride_page * ce;
-    p.v_tok = a.vc_stride_tok * ce;
-    p.v_tok8 = 8 * p.v_tok;
-    p.v_head = a.vc_stride_head * ce;
+    p.k_page = (int)(a.kc_stride_page * ce);
+    p.k_tok = (int)(a.kc_stride_tok * ce);
+    p.k_head = (int)(a.kc_stride_head * ce);
+    p.v_page = (int)(a.vc_stride_page * ce);
+    p.v_tok = (int)(a.vc_stride_tok * ce);
+    p.v_head = (int)(a.vc_stride_head * ce);
     p.by_page = FastDiv((uint32_t)a.page_size);
     p.part = h.part;
     p.arrived = h.arrived;
