@@ -54,10 +54,10 @@ struct Params {
     FastDiv by_page, by_hg;
     float *part;          // pieces: two a block, then one a warp
     int *arrived;         // [requests, key heads * groups]
-    int min_run;          // shortest run worth a block
 };
 
 constexpr int kSegCost = 4;         // what a segment costs besides its steps, in steps
+constexpr int kShort = 4;           // steps a warp up to which a segment is not shared among blocks
 constexpr int kSmemMax = 227 * 1024 - 2048;  // dynamic shared memory of a block
 constexpr int kGroupReq = 32;       // requests whose costs are summed together
 constexpr float kLazy = 8.f;        // the maximum moves when a logit passes it by 2^kLazy
@@ -298,43 +298,70 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
     for (int r = lane; r < n_run; r += 32) total += group_cost[r];
     const int U = warp_sum_i(total) * HG;
 
-    // this block's and this warp's run of the line
-    int per = (U + gridDim.x - 1) / gridDim.x;
-    if (per < p.min_run) per = p.min_run;
-    if ((long long)blockIdx.x * per >= U) return;
-    const int lo = blockIdx.x * per, hi = U - lo > per ? lo + per : U;
-    const int per_w = (hi - lo + C::WARPS - 1) / C::WARPS;
-    const int wb = min(lo + warp * per_w, hi), we = min(wb + per_w, hi);
-
-    // The request at wb: runs of 32 requests, then the run's requests.
-    int b = 0, hg = 0, from = 0, len = 0, steps = 0;
-    int sb = 0;  // first step of the segment (b, hg) on the line, past its own cost
-    if (wb < we) {
-        const int key = (int)p.by_hg.div(wb);  // position / head groups
-        int below = 0, r = 0;
-        for (int r0 = 0; r0 < n_run; r0 += 32) {
+    // The segment at a place of the line: its request, head group, first place
+    // (kSegCost before its first step) and cost; by the warp, from the runs of 32
+    // requests and then the run's requests.
+    int run = -1, run_below = 0, run_cost = 0, run_before = 0;  // the run last looked at: its costs and their sums
+    struct Segment { int b, hg, begin, cost; };
+    auto locate = [&](int x) {
+        const int key = (int)p.by_hg.div(x);  // place / head groups
+        int r = 0, below = 0;
+        for (int r0 = 0; n_run > 1 && r0 < n_run; r0 += 32) {
             const int v = r0 + lane < n_run ? group_cost[r0 + lane] : 0, s = warp_scan(v, lane) - v;
             const unsigned m = __ballot_sync(0xffffffffu, v > 0 && below + s <= key);
             const int all = __shfl_sync(0xffffffffu, s + v, 31);
-            if (m) {
-                const int l = 31 - __clz(m), at = __shfl_sync(0xffffffffu, s, l);
-                if (key < below + all) {
-                    r = r0 + l;
-                    below += at;
-                    break;
-                }
+            if (m && key < below + all) {
+                const int l = 31 - __clz(m);
+                below += __shfl_sync(0xffffffffu, s, l);
+                r = r0 + l;
+                break;
             }
             below += all;
         }
-        const int v = cost_of(r * kGroupReq + lane), s = warp_scan(v, lane) - v;
-        const unsigned m = __ballot_sync(0xffffffffu, v > 0 && below + s <= key);
+        if (r != run) {
+            run = r;
+            run_below = below;
+            run_cost = cost_of(r * kGroupReq + lane);
+            run_before = warp_scan(run_cost, lane) - run_cost;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, run_cost > 0 && run_below + run_before <= key);
         const int l = 31 - __clz(m);
-        b = r * kGroupReq + l;
-        const int cost = __shfl_sync(0xffffffffu, v, l);
-        sb = (below + __shfl_sync(0xffffffffu, s, l)) * HG;
-        steps = cost - kSegCost;
-        hg = (wb - sb) / cost;
-        sb += hg * cost + kSegCost;
+        Segment sg;
+        sg.b = run * kGroupReq + l;
+        sg.cost = __shfl_sync(0xffffffffu, run_cost, l);
+        sg.begin = (run_below + __shfl_sync(0xffffffffu, run_before, l)) * HG;
+        sg.hg = (x - sg.begin) / sg.cost;
+        sg.begin += sg.hg * sg.cost;
+        return sg;
+    };
+
+    // This block's run of the line.  A boundary inside a short segment moves to
+    // its nearer end: sharing a segment among blocks costs more (some 4 us: fence,
+    // arrival, the last block's join) than the steps it would even out.
+    int per = (U + gridDim.x - 1) / gridDim.x;
+    if (per < C::WARPS) per = C::WARPS;
+    auto boundary = [&](long long x) {
+        if (x >= U) return U;
+        if (x == 0) return 0;
+        const Segment sg = locate((int)x);
+        if (sg.cost > kShort * C::WARPS) return (int)x;
+        return 2 * ((int)x - sg.begin) < sg.cost ? sg.begin : sg.begin + sg.cost;
+    };
+    if ((long long)blockIdx.x * per >= U) return;
+    const int lo = boundary((long long)blockIdx.x * per), hi = boundary((long long)(blockIdx.x + 1) * per);
+    if (lo >= hi) return;
+    // and this warp's
+    const int per_w = (hi - lo + C::WARPS - 1) / C::WARPS;
+    const int wb = min(lo + warp * per_w, hi), we = min(wb + per_w, hi);
+
+    int b = 0, hg = 0, from = 0, len = 0, steps = 0;
+    int sb = 0;  // first step of the segment (b, hg) on the line, past its own cost
+    if (wb < we) {
+        const Segment sg = locate(wb);
+        b = sg.b;
+        hg = sg.hg;
+        sb = sg.begin + kSegCost;
+        steps = sg.cost - kSegCost;
         seen(a, b, from, len);
     }
     for (int u = wb; u < we;) {
@@ -890,7 +917,8 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                 sh.warp = warp;
                 sh.n = (min(se, hi) - 1 - lo) / per_w - warp + 1;
                 sh.before = sb < lo ? (int)blockIdx.x - sb / per : 0;
-                sh.more = (se - 1) / per - sb / per;
+                // (no boundary inside a long segment moved, so the blocks are per apart)
+                sh.more = sb >= lo && se <= hi ? 0 : (se - 1) / per - sb / per;
             }
         }
         u = min(se, we);
@@ -930,16 +958,18 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
     if (!open) return;
 
     // Segments shared with other blocks: the last block to arrive joins them.
-    __threadfence();
     __syncthreads();
     if (tid < ns && shared[tid].more) {
         const Shared &sh = shared[tid];
         int *cnt = p.arrived + sh.b * HG + sh.hg;
-        if (atomicAdd(cnt, 1) == sh.more) {
+        // release: the block's pieces (the barrier orders the other threads' before
+        // this); acquire: those of the blocks that came before
+        int arrived;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(arrived) : "l"(cnt) : "memory");
+        if (arrived == sh.more) {
             *cnt = 0;  // for the next launch
             last_of[sh.before ? 0 : 1] = tid;
         }
-        __threadfence();
     }
     __syncthreads();
     for (int k = 0; k < 2; ++k) {

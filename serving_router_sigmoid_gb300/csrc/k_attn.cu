@@ -72,7 +72,6 @@ cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaSt
     p.part = h.part;
     p.arrived = h.arrived;
     p.by_hg = FastDiv((uint32_t)(p.n_kv * p.n_groups));
-    p.min_run = f.threads / 32;  // a step a warp
     void *args[] = {&p};
     return cudaLaunchKernel(reinterpret_cast<const void *>(f.fn), dim3(h.num_sms), dim3(f.threads), args,
                             f.smem, s);
