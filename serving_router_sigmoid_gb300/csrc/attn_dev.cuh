@@ -89,13 +89,14 @@ struct Cfg {
     static constexpr int QFRAGS = NQ * NT * KSTEPS;
     static constexpr int UNIT = TT * DMAX * ES;      // bytes of a step's keys (or values)
     // steps requested ahead; a ring of 2 AHEAD + 1 units holds them and the one read last
-    static constexpr int FIT = (kSmemMax - WARPS * QFRAGS * 256) / (WARPS * UNIT);
+    static constexpr int QBYTES = QS ? QFRAGS * 256 : 0;
+    static constexpr int FIT = (kSmemMax - WARPS * QBYTES) / (WARPS * UNIT);
     static constexpr int AHEAD = FIT >= 9 ? 4 : (FIT - 1) / 2;
     static constexpr int NU = 2 * AHEAD + 1;
     static_assert(AHEAD >= 1 && NU * UNIT >= PIECE * 4, "");
     // a warp's shared memory: its ring, or room for its last piece
     static constexpr int SPACE = RING ? NU * UNIT : PIECE * 4;
-    static constexpr size_t kSmem = (size_t)WARPS * (SPACE + QFRAGS * 256);
+    static constexpr size_t kSmem = (size_t)WARPS * (SPACE + QBYTES);
     // weights are held times 2^kOff: f16's subnormals then start at 2^-31 of the maximum
     static constexpr float kOff = kF16 ? 7.f : 0.f;
 };
@@ -391,19 +392,26 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
             for (int nt = 0; nt < NT; ++nt) {
                 const char *q = static_cast<const char *>(a.q) +
                                 (b * a.q_stride_b + (int64_t)(h0 + nt * 8 + g) * a.q_stride_h) * q_bytes;
-                const bool on = nt * 8 + g < heads;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const bool in = on && q_dim(i) < p.k_dim;
+                    const bool in = nt * 8 + g < heads && q_dim(i) < p.k_dim;
                     const char *s = q + q_dim(i) * q_bytes;
+                    if (!p.q16) {  // rows off 16 bytes: by twos, through the ring, which is still empty
+                        char *mine = my_ring + lane * 32;
+#pragma unroll 1
+                        for (int e = 0; in && e < 8 * q_bytes; e += 2)
+                            *reinterpret_cast<uint16_t *>(mine + e) = *reinterpret_cast<const uint16_t *>(s + e);
+                        s = mine;
+                    }
                     qraw[nt][i][0] = make_uint4(0u, 0u, 0u, 0u);
                     if (WIDE) qraw[nt][i][WIDE ? 1 : 0] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && p.q16) {
+                    if (in) {
                         qraw[nt][i][0] = *reinterpret_cast<const uint4 *>(s);
                         if (WIDE && q_bytes == 4) qraw[nt][i][WIDE ? 1 : 0] = *reinterpret_cast<const uint4 *>(s + 16);
                     }
                 }
             }
+            if (!p.q16) __syncwarp();
 
             const char *kb = static_cast<const char *>(a.k_cache) + (int64_t)kvh * p.k_head +
                              (int64_t)g * p.k_tok + c * 16;
@@ -551,27 +559,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
             uint32_t qf[C::QS ? 1 : C::QFRAGS][2];
             float fac[NT][2];
             auto build_query = [&]() {
-                if (!p.q16) {  // rows off 16 bytes: element by element, through shared memory
-    #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const char *q = static_cast<const char *>(a.q) +
-                                        (b * a.q_stride_b + (int64_t)(h0 + nt * 8 + g) * a.q_stride_h) * q_bytes;
-                        char *mine = reinterpret_cast<char *>(qsm) + lane * 32;
-    #pragma unroll
-                        for (int i = 0; i < NI; ++i) {
-                            if (nt * 8 + g < heads && q_dim(i) < p.k_dim) {
-    #pragma unroll 1
-                                for (int e = 0; e < 8 * q_bytes; e += 2)
-                                    *reinterpret_cast<uint16_t *>(mine + e) =
-                                        *reinterpret_cast<const uint16_t *>(q + q_dim(i) * q_bytes + e);
-                                qraw[nt][i][0] = *reinterpret_cast<const uint4 *>(mine);
-                                if (WIDE) qraw[nt][i][WIDE ? 1 : 0] = *reinterpret_cast<const uint4 *>(mine + 16);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                }
-    #pragma unroll
+#pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float v[NI][8];
     #pragma unroll
