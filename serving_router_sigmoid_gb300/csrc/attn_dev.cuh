@@ -203,24 +203,44 @@ struct Shared {
 
 // Joins n pieces (O, m, l) of one segment, the i-th at piece(i): row and
 // dimensions [d, d + 4) of it, into the output or into a piece `to`.
-template <int ROWS, int DMAX, typename Piece>
+template <int ROWS, int DMAX, int BATCH, typename Piece>
 __device__ __forceinline__ void join_pieces(const Params &p, Piece piece, int n, int b, int hg, int row, int d, float *to) {
     const int kvh = hg / p.n_groups, h0 = kvh * p.group + (hg - kvh * p.n_groups) * ROWS;
     if (h0 + row >= (kvh + 1) * p.group || d >= p.v_dim) return;
-    float top = kFloor;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) top = fmaxf(top, piece(i)[ROWS * DMAX + row]);
-    float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float *q = piece(i);
-        const float f = exp2_fast(q[ROWS * DMAX + row] - top);
-        sum = fmaf(q[ROWS * (DMAX + 1) + row], f, sum);
-        const float4 v = *reinterpret_cast<const float4 *>(q + row * DMAX + d);
-        x[0] = fmaf(v.x, f, x[0]);
-        x[1] = fmaf(v.y, f, x[1]);
-        x[2] = fmaf(v.z, f, x[2]);
-        x[3] = fmaf(v.w, f, x[3]);
+    float top = kFloor, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += BATCH) {  // a batch's loads go out together
+        float pm[BATCH], pl[BATCH];
+        float4 po[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            pm[i] = kFloor;
+            pl[i] = 0.f;
+            po[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + i < n) {
+                const float *q = piece(i0 + i);
+                pm[i] = q[ROWS * DMAX + row];
+                pl[i] = q[ROWS * (DMAX + 1) + row];
+                po[i] = *reinterpret_cast<const float4 *>(q + row * DMAX + d);
+            }
+        }
+        float high = top;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) high = fmaxf(high, pm[i]);
+        const float keep = exp2_fast(top - high);
+        top = high;
+        sum *= keep;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] *= keep;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const float f = exp2_fast(pm[i] - top);
+            sum = fmaf(pl[i], f, sum);
+            x[0] = fmaf(po[i].x, f, x[0]);
+            x[1] = fmaf(po[i].y, f, x[1]);
+            x[2] = fmaf(po[i].z, f, x[2]);
+            x[3] = fmaf(po[i].w, f, x[3]);
+        }
     }
     if (to) {
         store_vec(to + row * DMAX + d, x);
@@ -275,8 +295,9 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
     if (tid == 0) n_shared = 0;
     if (tid < 2) last_of[tid] = -1;
     const int n_run = (n_req + kGroupReq - 1) / kGroupReq;
+    const int own_cost = n_run <= 1 ? cost_of(lane) : 0;
     for (int r = warp; r < n_run; r += C::WARPS) {
-        const int b = r * kGroupReq + lane, n = cost_of(b);
+        const int b = r * kGroupReq + lane, n = n_run == 1 ? own_cost : cost_of(b);
         const int sum = warp_sum_i(n);
         if (lane == 0) group_cost[r] = sum;
         // requests that see nothing: zeros, by the blocks in turn
@@ -295,18 +316,29 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
         }
     }
     __syncthreads();
+    // (one run of requests at most: every warp has looked at it itself)
+    int run = -1, run_below = 0, run_cost = 0, run_before = 0;  // the run last looked at: its costs and their sums
     int total = 0;
-    for (int r = lane; r < n_run; r += 32) total += group_cost[r];
-    const int U = warp_sum_i(total) * HG;
+    if (n_run <= 1) {
+        run = 0;
+        run_cost = own_cost;
+        total = warp_scan(run_cost, lane);
+        run_before = total - run_cost;
+        total = __shfl_sync(0xffffffffu, total, 31);
+    } else {
+        for (int r = lane; r < n_run; r += 32) total += group_cost[r];
+        total = warp_sum_i(total);
+    }
+    const int U = total * HG;
 
     // The segment at a place of the line: its request, head group, first place
     // (kSegCost before its first step) and cost; by the warp, from the runs of 32
     // requests and then the run's requests.
-    int run = -1, run_below = 0, run_cost = 0, run_before = 0;  // the run last looked at: its costs and their sums
     struct Segment { int b, hg, begin, cost; };
     auto locate = [&](int x) {
         const int key = (int)p.by_hg.div(x);  // place / head groups
         int r = 0, below = 0;
+#pragma unroll 1
         for (int r0 = 0; n_run > 1 && r0 < n_run; r0 += 32) {
             const int v = r0 + lane < n_run ? group_cost[r0 + lane] : 0, s = warp_scan(v, lane) - v;
             const unsigned m = __ballot_sync(0xffffffffu, v > 0 && below + s <= key);
@@ -894,7 +926,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
             if (whole) {
 #pragma unroll 1
                 for (int e = lane; e < C::ROWS * (DMAX / 4); e += 32)
-                    join_pieces<C::ROWS, DMAX>(p, [&](int) { return pc; }, 1, b, hg, e / (DMAX / 4),
+                    join_pieces<C::ROWS, DMAX, 1>(p, [&](int) { return pc; }, 1, b, hg, e / (DMAX / 4),
                                                4 * (e % (DMAX / 4)), nullptr);
                 __syncwarp();
             } else if (lane == 0 && (!before || warp == 0)) {
@@ -938,7 +970,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
         const float *of0 = sh.before ? p.part + (size_t)(2 * gridDim.x + blockIdx.x * C::WARPS) * C::PIECE
                                      : reinterpret_cast<const float *>(smem + sh.warp * C::SPACE);
         const float *rest = p.part + (size_t)(2 * gridDim.x + blockIdx.x * C::WARPS + sh.warp) * C::PIECE;
-        join_pieces<C::ROWS, DMAX>(p, [&](int i) { return i == 0 ? of0 : rest + i * C::PIECE; }, sh.n, sh.b, sh.hg,
+        join_pieces<C::ROWS, DMAX, 8>(p, [&](int i) { return i == 0 ? of0 : rest + i * C::PIECE; }, sh.n, sh.b, sh.hg,
                                    row, d, to);
     }
     bool open = false;
