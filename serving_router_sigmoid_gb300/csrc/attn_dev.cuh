@@ -733,6 +733,11 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                                 else x[h][j] = w[j];
                             }
                         }
+                        float part[WIDE ? NT : 1][4];  // (see the second product)
+                        if constexpr (WIDE) {
+#pragma unroll
+                            for (int e = 0; e < NT * 4; ++e) part[e / 4][e % 4] = 0.f;
+                        }
 #pragma unroll
                         for (int w = 0; w < WORDS / 2; ++w)
 #pragma unroll
@@ -743,9 +748,13 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                                     uint2 qq;
                                     if constexpr (C::QS) qq = qsm[f * 32 + lane];
                                     else qq = make_uint2(qf[f][0], qf[f][1]);
-                                    mma<F16>(C::RING && w & 1 ? s1[r][nt] : s[r][nt], x[0][2 * w], x[1][2 * w], x[0][2 * w + 1],
-                                             x[1][2 * w + 1], qq.x, qq.y);
+                                    mma<F16>(WIDE ? part[WIDE ? nt : 0] : C::RING && w & 1 ? s1[r][nt] : s[r][nt],
+                                             x[0][2 * w], x[1][2 * w], x[0][2 * w + 1], x[1][2 * w + 1], qq.x, qq.y);
                                 }
+                        if constexpr (WIDE) {
+#pragma unroll
+                            for (int e = 0; e < NT * 4; ++e) s[r][e / 4][e % 4] += part[e / 4][e % 4];
+                        }
                     }
 
                 if constexpr (!C::RING) put_keys(step + LEAD);
@@ -877,14 +886,29 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                                     m[3] = __byte_perm(w2, w3, 0x7632);
                                 }
                             }
+                            // The tensor cores cut a sum's last bits off: over many
+                            // steps that shows in fp32 outputs (3.3e-6 of 24 x 8192
+                            // tokens), so those take a step's sum by a rounded add.
+                            float part[WIDE ? 2 * PER : 1][NT][4];
+                            if constexpr (WIDE) {
+#pragma unroll
+                                for (int x = 0; x < 2 * PER * NT * 4; ++x) part[x / (NT * 4)][x / 4 % NT][x % 4] = 0.f;
+                            }
 #pragma unroll
                             for (int q = 0; q < C::NP; ++q)
 #pragma unroll
                                 for (int e = 0; e < 2 * PER; ++e)
 #pragma unroll
                                     for (int nt = 0; nt < NT; ++nt)
-                                        mma<F16>(o[nt][i * (C::VE / 2) + j * PER + e], am[e][0], am[e][1], am[e][2],
-                                                 am[e][3], pb[r][nt][q][0], pb[r][nt][q][1]);
+                                        mma<F16>(WIDE ? part[WIDE ? e : 0][nt] : o[nt][i * (C::VE / 2) + j * PER + e],
+                                                 am[e][0], am[e][1], am[e][2], am[e][3], pb[r][nt][q][0],
+                                                 pb[r][nt][q][1]);
+                            if constexpr (WIDE) {
+#pragma unroll
+                                for (int x = 0; x < 2 * PER * NT * 4; ++x)
+                                    o[x / 4 % NT][i * (C::VE / 2) + j * PER + x / (NT * 4)][x % 4] +=
+                                        part[x / (NT * 4)][x / 4 % NT][x % 4];
+                            }
                         }
                     }
             }
