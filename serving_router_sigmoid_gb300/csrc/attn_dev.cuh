@@ -12,14 +12,15 @@
 //   block per SM) takes an equal run of it, found from the lengths by each warp
 //   itself.  A batch of one long and many short requests keeps every SM busy to
 //   the end, with one launch and no plan on the host.
-// - A warp needs no other warp until its run ends.  It copies rows with cp.async
-//   into a ring of its own, NU units of 4 to 8 KB (a step's keys, a step's
-//   values): its own wait is all the ring needs, no barrier.  NU - 1 units stay
-//   in flight, 128 KB an SM.
-// - The pieces a lane copies are the tensor cores' fragments: with the tokens on
-//   the MMA's M side a lane's 16 bytes of a key row ARE its A fragment (the
-//   order of the contraction is free, the query takes the same order), and four
-//   pieces of value rows become A fragments of V^T by byte permutes.
+// - A warp needs no other warp until its run ends.  Rows go from HBM straight
+//   into the registers of the tensor cores' fragments: with the tokens on the
+//   MMA's M side a lane's 16 bytes of a key row ARE its A fragment (the order of
+//   the contraction is free, the query takes the same order), and four pieces of
+//   value rows become A fragments of V^T by byte permutes.  No shared memory, no
+//   barrier, no transposition; a step is 8 KB (16 at 256 dimensions), its values
+//   requested at its start and the next step's keys once its own are read.  (A
+//   ring of cp.async copies in shared memory, 128 to 192 KB in flight, was slower
+//   in every form: 64 x 4096 tokens E4M3 113 against 97 us.)
 // - The heads of a group sit on N (8 a tile), so S^T = K q^T leaves each lane
 //   the logits of its own two heads: the running maximum, the sum and the
 //   rescale of O^T need no exchange.  The maximum moves only when a logit
@@ -58,7 +59,6 @@ struct Params {
 
 constexpr int kSegCost = 4;         // what a segment costs besides its steps, in steps
 constexpr int kShort = 4;           // steps a warp up to which a segment is not shared among blocks
-constexpr int kSmemMax = 227 * 1024 - 2048;  // dynamic shared memory of a block
 constexpr int kGroupReq = 32;       // requests whose costs are summed together
 constexpr float kLazy = 8.f;        // the maximum moves when a logit passes it by 2^kLazy
 constexpr float kFloor = -1e38f;    // running maximum before any token
@@ -80,23 +80,15 @@ struct Cfg {
     static constexpr int NP = WIDE ? NQ : 2;
     static constexpr int ROWS = 8 * NT;
     static constexpr bool QS = NQ * NT * DMAX > 128;  // query fragments stay in shared memory
-    static constexpr bool RING = CT == MOE_E4M3 || NT * DMAX > 128 || WIDE;
-    // one block per SM; registers allow 12 warps of the form that loads into
-    // them; the largest query fragments leave shared memory for 4
-    static constexpr int WARPS = !RING ? 12 : DMAX == 256 && WIDE ? 4 : 8;
+    // one block per SM; registers allow 12 warps of the plain form
+    static constexpr int WARPS = DMAX <= 128 && NT == 1 && !WIDE ? 12 : 8;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int PIECE = ROWS * (DMAX + 2);  // floats of a piece: O, m, l
     static constexpr int QFRAGS = NQ * NT * KSTEPS;
-    static constexpr int UNIT = TT * DMAX * ES;      // bytes of a step's keys (or values)
-    // steps requested ahead; a ring of 2 AHEAD + 1 units holds them and the one read last
     static constexpr int QBYTES = QS ? QFRAGS * 256 : 0;
-    static constexpr int FIT = (kSmemMax - WARPS * QBYTES) / (WARPS * UNIT);
-    static constexpr int AHEAD = FIT >= 9 ? 4 : (FIT - 1) / 2;
-    static constexpr int NU = 2 * AHEAD + 1;
-    static_assert(AHEAD >= 1 && NU * UNIT >= PIECE * 4, "");
-    // a warp's shared memory: its ring, or room for its last piece
-    static constexpr int SPACE = RING ? NU * UNIT : PIECE * 4;
-    static constexpr size_t kSmem = (size_t)WARPS * (SPACE + QBYTES);
+    // shared memory: a warp's last piece, and its query fragments
+    static constexpr size_t kSmem = (size_t)WARPS * (PIECE * 4 + QBYTES);
+    static_assert(kSmem <= 227 * 1024 - 2048, "");
     // weights are held times 2^kOff: f16's subnormals then start at 2^-31 of the maximum
     static constexpr float kOff = kF16 ? 7.f : 0.f;
 };
@@ -125,28 +117,21 @@ __device__ __forceinline__ float exp2_fast(float x) {  // within 2^-22
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// Asynchronous copies of 16 or 8 bytes to shared memory; zeros if not `on`.
-__device__ __forceinline__ void copy16(uint32_t dst, const char *src, bool on) {
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const char *src, bool on) {
-    asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0)
-                 : "memory");
-}
+// A piece of a row, read once.  (No L2 prefetch beyond it: where a head's row is shorter than 256 bytes
+// it fetches other heads' rows, whose readers come at other times.  64 x 4096
+// tokens, 16 key heads of 64 dimensions, bf16: 239 us with 256-byte prefetches,
+// 171 without; rows of 256 bytes lose 1% at most.)
 __device__ __forceinline__ uint4 ld16(const char *p) {
-    const int4 v = ld_stream16(p);
-    return make_uint4(v.x, v.y, v.z, v.w);
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
 }
 __device__ __forceinline__ uint2 ld8(const char *p) {
     uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
     return r;
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 // Four e4m3 codes -> two pairs of f16 (exact).
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
@@ -281,9 +266,8 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
     const MoeAttnArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int n_req = a.n_requests, HG = p.n_kv * p.n_groups;
-    char *my_ring = smem + warp * C::SPACE;
-    uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::WARPS * C::SPACE) + warp * C::QFRAGS * 32;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(my_ring);
+    float *my_piece = reinterpret_cast<float *>(smem) + warp * C::PIECE;
+    uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::WARPS * C::PIECE * 4) + warp * C::QFRAGS * 32;
 
     // cost of each run of 32 requests (steps, and kSegCost for each request that has any)
     auto cost_of = [&](int b) {
@@ -428,8 +412,8 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                 for (int i = 0; i < NI; ++i) {
                     const bool in = nt * 8 + g < heads && q_dim(i) < p.k_dim;
                     const char *s = q + q_dim(i) * q_bytes;
-                    if (!p.q16) {  // rows off 16 bytes: by twos, through the ring, which is still empty
-                        char *mine = my_ring + lane * 32;
+                    if (!p.q16) {  // rows off 16 bytes: by twos, through shared memory
+                        char *mine = reinterpret_cast<char *>(my_piece) + lane * 32;
 #pragma unroll 1
                         for (int e = 0; in && e < 8 * q_bytes; e += 2)
                             *reinterpret_cast<uint16_t *>(mine + e) = *reinterpret_cast<const uint16_t *>(s + e);
@@ -447,33 +431,24 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
 
             const char *kb = static_cast<const char *>(a.k_cache) + (int64_t)kvh * p.k_head +
                              (int64_t)g * p.k_tok + c * 16;
-            // Values are copied in another order than they are read in: a copy's
-            // eight lanes take 8 pieces of one row (adjacent lanes on different
-            // rows would halve its rate: 4.4 against 7.2 TB/s of plain copies),
-            // and the pieces of row vc lie turned by 2 vc places, so that neither
-            // side meets its own banks.
-            const int vc = C::RING ? lane >> 3 : c, vg = C::RING ? lane & 7 : g;
             const char *vb = static_cast<const char *>(a.v_cache) + (int64_t)kvh * p.v_head +
-                             2 * (int64_t)vc * p.v_tok + vg * C::VB;
-            auto v_place = [](int gg, int cc) { return cc * 8 + (C::VB == 16 ? gg ^ 2 * cc : gg ^ 4 * (cc >> 1)); };
+                             2 * (int64_t)c * p.v_tok + g * C::VB;
             // A step is `plain` when all its tokens are seen and lie on whole
             // pages: its rows are then at fixed distances from one address a tile.
             // (One branch for all of them: a branch a row cost 800 of a step's 3300
             // cycles.  Pieces beyond the head's size stay the zeros they are.)
-            uint4 kr[C::RING ? 1 : C::R][2][C::KCH];
-            uint32_t vr[C::RING ? 1 : C::R][4][C::VCH][C::VB / 4];
-            if constexpr (!C::RING) {
+            uint4 kr[C::R][2][C::KCH];
+            uint32_t vr[C::R][4][C::VCH][C::VB / 4];
 #pragma unroll
-                for (int r = 0; r < C::R; ++r) {
+            for (int r = 0; r < C::R; ++r) {
 #pragma unroll
-                    for (int i = 0; i < 2 * C::KCH; ++i) kr[r][i / C::KCH][i % C::KCH] = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = 0; i < 2 * C::KCH; ++i) kr[r][i / C::KCH][i % C::KCH] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int i = 0; i < C::VCH; ++i)
+                    for (int i = 0; i < C::VCH; ++i)
 #pragma unroll
-                            for (int j = 0; j < C::VB / 4; ++j) vr[r][k][i][j] = 0u;
-                }
+                        for (int j = 0; j < C::VB / 4; ++j) vr[r][k][i][j] = 0u;
             }
             int page[C::R], at[C::R];
             bool plain = false, holes = false;  // holes: a page that is none came by
@@ -495,30 +470,21 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                 }
                 return (int64_t)pg * sp + (int64_t)in * st;
             };
-            // One piece of a key or value row, into the ring or the registers.
-            auto fetch_key = [&](int r, int h, int i, uint32_t dst, const char *k, bool on) {
-                on = on && (4 * i + c) * EC < p.k_dim;
-                if constexpr (C::RING) copy16(dst + ((r * 2 + h) * C::KCH + i) * 512 + lane * 16, k + i * 64, on);
-                else if (on) kr[r][h][i] = ld16(k + i * 64);
+            auto fetch_key = [&](int r, int h, int i, const char *k) {
+                if ((4 * i + c) * EC < p.k_dim) kr[r][h][i] = ld16(k + i * 64);
             };
-            auto fetch_value = [&](int r, int k, int i, uint32_t dst, const char *v, bool on) {
-                on = on && (8 * i + vg) * C::VE < p.v_dim;
-                if constexpr (C::RING) {
-                    const uint32_t to = dst + (((r * 4 + k) * C::VCH + i) * 32 + v_place(vg, vc)) * C::VB;
-                    if constexpr (C::VB == 16) copy16(to, v + i * 128, on);
-                    else copy8(to, v + i * 64, on);
-                } else if (on) {
-                    uint32_t(&w)[C::VB / 4] = vr[r][k][i];
-                    if constexpr (C::VB == 16) {
-                        const uint4 x = ld16(v + i * 128);
-                        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-                    } else {
-                        const uint2 x = ld8(v + i * 64);
-                        w[0] = x.x; w[1] = x.y;
-                    }
+            auto fetch_value = [&](int r, int k, int i, const char *v) {
+                if ((8 * i + g) * C::VE >= p.v_dim) return;
+                uint32_t(&w)[C::VB / 4] = vr[r][k][i];
+                if constexpr (C::VB == 16) {
+                    const uint4 x = ld16(v + i * 128);
+                    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                } else {
+                    const uint2 x = ld8(v + i * 64);
+                    w[0] = x.x; w[1] = x.y;
                 }
             };
-            auto request_keys = [&](int t, uint32_t dst) {
+            auto request_keys = [&](int t) {
                 plain = p.by16 && t >= from && t + C::TT <= len;
                 if (p.by16) {
 #pragma unroll
@@ -541,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
-                            for (int i = 0; i < C::KCH; ++i) fetch_key(r, h, i, dst, k + h * 8 * (int64_t)p.k_tok, true);
+                            for (int i = 0; i < C::KCH; ++i) fetch_key(r, h, i, k + h * 8 * (int64_t)p.k_tok);
                     }
                     return;
                 }
@@ -552,12 +518,12 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         const int64_t off = row_at(t, r, g + 8 * h, p.k_page, p.k_tok);
 #pragma unroll
                         for (int i = 0; i < C::KCH; ++i) {
-                            if constexpr (!C::RING) kr[r][h][i] = make_uint4(0u, 0u, 0u, 0u);
-                            fetch_key(r, h, i, dst, off < 0 ? kb : kb + (off - (int64_t)g * p.k_tok), off >= 0);
+                            kr[r][h][i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (off >= 0) fetch_key(r, h, i, kb + (off - (int64_t)g * p.k_tok));
                         }
                     }
             };
-            auto request_values = [&](int t, uint32_t dst) {
+            auto request_values = [&](int t) {
                 if (plain) {
 #pragma unroll
                     for (int r = 0; r < C::R; ++r) {
@@ -566,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         for (int k = 0; k < 4; ++k)
 #pragma unroll
                             for (int i = 0; i < C::VCH; ++i)
-                                fetch_value(r, k, i, dst, v + ((k & 1) + (k >> 1) * 8) * (int64_t)p.v_tok, true);
+                                fetch_value(r, k, i, v + ((k & 1) + (k >> 1) * 8) * (int64_t)p.v_tok);
                     }
                     return;
                 }
@@ -574,14 +540,12 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                 for (int r = 0; r < C::R; ++r)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int64_t off = row_at(t, r, 2 * vc + (k & 1) + 8 * (k >> 1), p.v_page, p.v_tok);
+                        const int64_t off = row_at(t, r, 2 * c + (k & 1) + 8 * (k >> 1), p.v_page, p.v_tok);
 #pragma unroll
                         for (int i = 0; i < C::VCH; ++i) {
-                            if constexpr (!C::RING) {
 #pragma unroll
-                                for (int j = 0; j < C::VB / 4; ++j) vr[r][k][i][j] = 0u;
-                            }
-                            fetch_value(r, k, i, dst, off < 0 ? vb : vb + (off - 2 * (int64_t)vc * p.v_tok), off >= 0);
+                            for (int j = 0; j < C::VB / 4; ++j) vr[r][k][i][j] = 0u;
+                            if (off >= 0) fetch_value(r, k, i, vb + (off - 2 * (int64_t)c * p.v_tok));
                         }
                     }
             };
@@ -666,53 +630,20 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                 l[nt][0] = l[nt][1] = 0.f;
             }
 
-            // Units K(first), V(first), K(first + 1), ...: AHEAD steps are on
-            // their way; each new one takes the place of the one read before.
-            int get = 0, put = 0;
-            // (Without a ring: keys one step ahead, values at the step's start.)
-            auto after = [](int i) { return i + 1 == C::NU ? 0 : i + 1; };
-            constexpr int LEAD = C::RING ? C::AHEAD : 1;
-            auto put_keys = [&](int step) {
-                if (step < last) request_keys(tok0 + step * C::TT, ring + put * C::UNIT);
-                if constexpr (C::RING) {
-                    copy_commit();
-                    put = after(put);
-                }
-            };
-            auto put_values = [&](int step) {
-                if (step < last) request_values(tok0 + step * C::TT, ring + put * C::UNIT);
-                if constexpr (C::RING) {
-                    copy_commit();
-                    put = after(put);
-                }
-            };
-#pragma unroll 1
-            for (int i = 0; i < LEAD; ++i) {
-                put_keys(first + i);
-                if constexpr (C::RING) put_values(first + i);
-            }
+            request_keys(tok0 + first * C::TT);
             build_query();
 #pragma unroll 1
             for (int step = first; step < last; ++step) {
                 const int t = tok0 + step * C::TT;
-                if constexpr (C::RING) {
-                    copy_wait<2 * C::AHEAD - 1>();
-                    __syncwarp();
-                    put_keys(step + LEAD);
-                } else {
-                    put_values(step);
-                }
+                request_values(t);
                 // S^T = K q^T
-                const char *ks = my_ring + get * C::UNIT + lane * 16;
-                get = after(get);
-                // (two accumulators a tile where registers allow: a chain of products waits for itself)
-                float s[C::R][NT][4], s1[C::R][NT][4];
+                float s[C::R][NT][4];
 #pragma unroll
                 for (int r = 0; r < C::R; ++r)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) s[r][nt][i] = s1[r][nt][i] = 0.f;
+                        for (int i = 0; i < 4; ++i) s[r][nt][i] = 0.f;
 #pragma unroll
                 for (int i = 0; i < C::KCH; ++i)
 #pragma unroll
@@ -721,11 +652,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         uint32_t x[2][WORDS];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            uint4 y;
-                            if constexpr (C::RING)
-                                y = *reinterpret_cast<const uint4 *>(ks + ((r * 2 + h) * C::KCH + i) * 512);
-                            else
-                                y = kr[r][h][i];
+                            const uint4 y = kr[r][h][i];
                             const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -748,7 +675,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                                     uint2 qq;
                                     if constexpr (C::QS) qq = qsm[f * 32 + lane];
                                     else qq = make_uint2(qf[f][0], qf[f][1]);
-                                    mma<F16>(WIDE ? part[WIDE ? nt : 0] : C::RING && w & 1 ? s1[r][nt] : s[r][nt],
+                                    mma<F16>(WIDE ? part[WIDE ? nt : 0] : s[r][nt],
                                              x[0][2 * w], x[1][2 * w], x[0][2 * w + 1], x[1][2 * w + 1], qq.x, qq.y);
                                 }
                         if constexpr (WIDE) {
@@ -757,7 +684,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         }
                     }
 
-                if constexpr (!C::RING) put_keys(step + LEAD);
+                if (step + 1 < last) request_keys(t + C::TT);
 
                 // softmax weights against the running maximum
 #pragma unroll
@@ -765,7 +692,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) s[r][nt][i] = (C::RING ? s[r][nt][i] + s1[r][nt][i] : s[r][nt][i]) * fac[nt][i & 1];
+                        for (int i = 0; i < 4; ++i) s[r][nt][i] *= fac[nt][i & 1];
                 if (t < from || t + C::TT > len || __any_sync(0xffffffffu, holes)) {
 #pragma unroll
                     for (int r = 0; r < C::R; ++r)
@@ -836,32 +763,10 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                     }
 
                 // O^T += V^T P^T
-                if constexpr (C::RING) {
-                    copy_wait<2 * C::AHEAD - 1>();
-                    __syncwarp();  // the other lanes' copies, and their reads of the place taken next
-                    put_values(step + LEAD);
-                }
-                const char *vs = my_ring + get * C::UNIT + v_place(g, c) * C::VB;
-                get = after(get);
 #pragma unroll
                 for (int r = 0; r < C::R; ++r)
 #pragma unroll
                     for (int i = 0; i < C::VCH; ++i) {
-                        uint32_t vw[4][C::VB / 4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const char *at_v = vs + ((r * 4 + k) * C::VCH + i) * 32 * C::VB;
-                            if constexpr (!C::RING) {
-#pragma unroll
-                                for (int j = 0; j < C::VB / 4; ++j) vw[k][j] = vr[r][k][i][j];
-                            } else if constexpr (C::VB == 16) {
-                                const uint4 x = *reinterpret_cast<const uint4 *>(at_v);
-                                vw[k][0] = x.x; vw[k][1] = x.y; vw[k][2] = x.z; vw[k][3] = x.w;
-                            } else {
-                                const uint2 x = *reinterpret_cast<const uint2 *>(at_v);
-                                vw[k][0] = x.x; vw[k][1] = x.y;
-                            }
-                        }
                         // (two words together, so that an accumulator's terms do not
                         // follow one another)
                         constexpr int PER = C::ES == 1 ? 2 : 1;  // pairs of dimensions a word
@@ -870,8 +775,8 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                             uint32_t am[2 * PER][4];
 #pragma unroll
                             for (int jj = 0; jj < 2; ++jj) {
-                                const uint32_t w0 = vw[0][j + jj], w1 = vw[1][j + jj], w2 = vw[2][j + jj],
-                                               w3 = vw[3][j + jj];
+                                const uint32_t w0 = vr[r][0][i][j + jj], w1 = vr[r][1][i][j + jj],
+                                               w2 = vr[r][2][i][j + jj], w3 = vr[r][3][i][j + jj];
                                 uint32_t(&m)[4] = am[jj * PER];
                                 if constexpr (C::ES == 1) {  // a dimension's codes of two tokens side by side
                                     uint32_t(&m1)[4] = am[jj * PER + PER - 1];
@@ -912,16 +817,15 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         }
                     }
             }
-            copy_wait<0>();
             __syncwarp();
 
             // The segment's end, or the run's.  The whole segment goes to the
             // output; a piece of it to the block: one that began before the run
-            // to the warp's place in the workspace, one that goes on to the
-            // ring, which is free until the block's join.
+            // to the warp's place in the workspace, one that goes on to its place
+            // in shared memory.
             const bool whole = sb >= wb && se <= we, before = sb < wb;
             float *pc = before ? p.part + (size_t)(2 * gridDim.x + blockIdx.x * C::WARPS + warp) * C::PIECE
-                               : reinterpret_cast<float *>(my_ring);
+                               : my_piece;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -992,7 +896,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
         float *to = sh.more ? p.part + (size_t)(2 * blockIdx.x + (sh.before ? 0 : 1)) * C::PIECE : nullptr;
         // the first warp's piece began in its run, unless the segment did in another block
         const float *of0 = sh.before ? p.part + (size_t)(2 * gridDim.x + blockIdx.x * C::WARPS) * C::PIECE
-                                     : reinterpret_cast<const float *>(smem + sh.warp * C::SPACE);
+                                     : reinterpret_cast<const float *>(smem) + sh.warp * C::PIECE;
         const float *rest = p.part + (size_t)(2 * gridDim.x + blockIdx.x * C::WARPS + sh.warp) * C::PIECE;
         join_pieces<C::ROWS, DMAX, 8>(p, [&](int i) { return i == 0 ? of0 : rest + i * C::PIECE; }, sh.n, sh.b, sh.hg,
                                    row, d, to);
