@@ -33,7 +33,8 @@ __device__ __forceinline__ float sigmoid(float x) {
 // V elements per access (8 or 4: aligned 16-byte pieces, 1: any alignment),
 // M accesses per thread.
 template <int DT, int V, int M, bool EARLY>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && M == 4 && !EARLY ? 2 : 1) block_norm_kernel(const __grid_constant__ MoeNormArgs a) {
+__global__ void __launch_bounds__(V == 1 ? 1024 : 512, EARLY || V == 1 ? 1 : V * M == 8 ? 3 : V * M == 16 ? 2 : 1)
+    block_norm_kernel(const __grid_constant__ MoeNormArgs a) {
     using A = typename Elem<DT>::type;
     __shared__ float red[2][32];
     const int nw = blockDim.x >> 5;
@@ -64,7 +65,30 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && M == 4 && !EARL
         else store_vec(p, v);
     };
 
-    float r[M][V], u[M][V];
+    float u[M][V];               // the block's output, then r
+    uint4 xr[V == 1 ? 1 : M];    // the residual stream as loaded
+    float x1[V == 1 ? M : 1];
+    auto ldx = [&](int m, int d) {
+        if constexpr (V == 1) x1[m] = to_f32(x[d]);
+        else xr[m] = ld_once16(x + d);
+    };
+    auto getx = [&](int m, float(&v)[V]) {
+        if constexpr (V == 1) {
+            v[0] = x1[m];
+        } else {
+            const uint32_t w[4] = {xr[m].x, xr[m].y, xr[m].z, xr[m].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (V == 4) {
+                    v[j] = __uint_as_float(w[j]);
+                } else {
+                    const float2 f = half_pair(w[j], A());
+                    v[2 * j] = f.x;
+                    v[2 * j + 1] = f.y;
+                }
+            }
+        }
+    };
     float wp[EARLY ? M : 1][V], wn[EARLY ? M : 1][V];
     auto weights = [&](const float *w, float(&v)[V], int d) {
 #pragma unroll
@@ -79,11 +103,11 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && M == 4 && !EARL
         for (int m = 0; m < M; ++m) {
             const int d = (m * blockDim.x + threadIdx.x) * V;
 #pragma unroll
-            for (int j = 0; j < V; ++j) r[m][j] = u[m][j] = 0.f, f[m][j] = g1;
+            for (int j = 0; j < V; ++j) u[m][j] = 0.f, f[m][j] = g1;
             if (d < a.dim) {
                 if (y) ld(y + d, u[m]);
                 if (g && a.gate_stride_d) ld(g + d, f[m]);
-                if (EARLY) ld(x + d, r[m]);
+                if (EARLY) ldx(m, d);
             }
             if constexpr (EARLY) {
                 weights(a.w_post, wp[m], d);
@@ -111,7 +135,7 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && M == 4 && !EARL
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const int d = (m * blockDim.x + threadIdx.x) * V;
-            if (d < a.dim) ld(x + d, r[m]);
+            if (d < a.dim) ldx(m, d);
         }
     }
     float post = a.beta;
@@ -121,12 +145,14 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && M == 4 && !EARL
     for (int m = 0; m < M; ++m) {
         const int d = (m * blockDim.x + threadIdx.x) * V;
         if (d >= a.dim) continue;
+        float v[V];
+        getx(m, v);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            r[m][j] = fmaf(post, u[m][j], a.alpha * r[m][j]);
-            sq = fmaf(r[m][j], r[m][j], sq);
+            u[m][j] = fmaf(post, u[m][j], a.alpha * v[j]);
+            sq = fmaf(u[m][j], u[m][j], sq);
         }
-        st(out + d, r[m]);
+        st(out + d, u[m]);
     }
     if (!nrm) return;
     const float pre = rsqrtf(block_sum(sq, red[1], nw) / (float)a.dim + a.eps);
@@ -137,8 +163,8 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && M == 4 && !EARL
         float(&w)[V] = wn[EARLY ? m : 0];
         if constexpr (!EARLY) weights(a.w_pre, w, d);
 #pragma unroll
-        for (int j = 0; j < V; ++j) r[m][j] *= pre * w[j];
-        st(nrm + d, r[m]);
+        for (int j = 0; j < V; ++j) u[m][j] *= pre * w[j];
+        st(nrm + d, u[m]);
     }
 }
 
@@ -292,13 +318,15 @@ cudaError_t launch_rows(const MoeNormArgs &a, int m, int threads, cudaStream_t s
 
 // The form of the kernel, from sizes alone.  Measured on fp32 / bf16 rows with
 // a full gate (us):
-//   weights early     1 x 6144: 4.0 against 4.3; 1216 x 4096 fp32: 17.8 against
-//                     19.8; but 304 x 6144: 9.2 against 7.5 (registers: one
-//                     block per SM), so where a thread has few pieces or there
-//                     is at most one row an SM
-//   ring of copies    2048 x 6144 fp32: 40.4 against 46.4; 1216 x 8192 bf16: 24.0
-//                     against 35.1; but 304 x 6144: 9.5 against 7.5 and rows of
-//                     4 KB 33.9 against 17.8, so from 8 rows an SM, of more than 8 KB
+//   weights early     152 x 6144: 5.2 / 3.8 against 5.7 / 4.2, 608 x 4096: 9.7 /
+//                     7.5 against 9.7 / 8.1; but 4096 x 4096 bf16: 43.6 against
+//                     36.9 and 304 x 6144: 9.2 / 7.5 against 7.5 / 5.9 (registers:
+//                     fewer rows an SM); so by the rows an SM, the fewer the more
+//                     registers the weights take
+//   ring of copies    2048 x 6144: 40 against 46 fp32, 4096 x 6144: 76 / 61 against
+//                     82 / 67 (floor 75 / 38); but 608 x 6144: 14.5 / 11.8 against
+//                     13.0 / 10.3 and rows of 4 KB 33.9 against 17.8; so from 8 rows
+//                     an SM, of more than 8 KB
 template <int DT>
 cudaError_t launch_dt(const MoeNormArgs &a, int num_sms, cudaStream_t s) {
     constexpr int V = DT == MOE_F32 ? 4 : 8;
@@ -325,7 +353,7 @@ cudaError_t launch_dt(const MoeNormArgs &a, int num_sms, cudaStream_t s) {
     while (acc > m * most) m *= 2;
     const int threads = ((acc + m - 1) / m + 31) / 32 * 32;
     if (!vec) return launch_rows<DT, 1, false>(a, m, threads, s);
-    const bool early = m == 1 || (m == 2 && V == 4) || (m * V <= 16 && a.n_tokens <= num_sms);
+    const bool early = m * V <= 4 || a.n_tokens <= (m * V <= 8 ? 4 : m * V <= 16 ? 1 : 0) * (int64_t)num_sms;
     return early ? launch_rows<DT, V, true>(a, m, threads, s) : launch_rows<DT, V, false>(a, m, threads, s);
 }
 
