@@ -537,10 +537,10 @@ typedef struct {
 } MoeAttnDesc;
 
 /*
- * Create / destroy an attention handle: the workspace that a forward splits
- * long requests over and joins them in.  It owns that device memory (about 5
- * MiB at 128 dimensions, and 4 bytes for each request and group of 8 query
- * heads) and serves one stream at a time, on the device current at create.
+ * Create / destroy an attention handle: the workspace in which a call joins
+ * what it splits.  It owns that device memory (8 to 12 MiB at 128 dimensions on
+ * 152 SMs, and 4 bytes for each request and group of 8 query heads) and serves
+ * one stream at a time, on the device current at create.
  * Destroying NULL is accepted.  Errors: INVALID_ARG, SHAPE, NOMEM, CUDA.
  */
 int moe_attn_create(const MoeAttnDesc *desc, void **handle_out);
@@ -560,7 +560,8 @@ typedef struct {
     int64_t table_stride;
     int64_t n_pages;             /* pages of the caches; tokens on other page ids are not seen */
     const void *q;               /* [n_requests, n_heads, k_dim] */
-    const void *k_cache, *v_cache; /* 16-byte aligned; strides multiples of 16 bytes */
+    const void *k_cache, *v_cache; /* 16-byte aligned; strides multiples of 16
+                                    * bytes, in [0, 2^31) bytes */
     void *out;                   /* [n_requests, n_heads, v_dim] */
     float *lse;                  /* [n_requests, n_heads] contiguous, or NULL */
     int64_t q_stride_b, q_stride_h, out_stride_b, out_stride_h;
@@ -576,6 +577,8 @@ typedef struct {
  * A request that sees no token (seq_len <= 0) gets out = 0 and lse = -inf.
  * Logits, softmax statistics and sums are held in 32 bits.  The result does
  * not depend on which block finishes first.  May be captured in a CUDA graph.
+ * n_requests * max_pages * page_size * (key heads, each counted once for every
+ * 8 query heads) stays below 2^34; rows of a cache are 16-byte aligned.
  * Errors: INVALID_ARG, SHAPE, CUDA.
  */
 int moe_attn_decode(void *handle, const MoeAttnArgs *args, cudaStream_t stream);
