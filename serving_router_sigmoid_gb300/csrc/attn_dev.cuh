@@ -53,7 +53,7 @@ struct Params {
     uint32_t n_pages;
     int k_page, k_tok, k_head, v_page, v_tok, v_head;  // strides in bytes
     FastDiv by_page, by_hg;
-    float *part;          // pieces: two a block, then one a warp
+    float *part;          // [2 grid] pieces
     int *arrived;         // [requests, key heads * groups]
 };
 
@@ -81,13 +81,14 @@ struct Cfg {
     static constexpr int ROWS = 8 * NT;
     static constexpr bool QS = NQ * NT * DMAX > 128;  // query fragments stay in shared memory
     // one block per SM; registers allow 12 warps of the plain form
-    static constexpr int WARPS = DMAX <= 128 && NT == 1 && !WIDE ? 12 : 8;
+    // (and shared memory 7 of the largest query fragments)
+    static constexpr int WARPS = DMAX <= 128 && NT == 1 && !WIDE ? 12 : DMAX * NT * NQ > 512 ? 7 : 8;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int PIECE = ROWS * (DMAX + 2);  // floats of a piece: O, m, l
     static constexpr int QFRAGS = NQ * NT * KSTEPS;
     static constexpr int QBYTES = QS ? QFRAGS * 256 : 0;
-    // shared memory: a warp's last piece, and its query fragments
-    static constexpr size_t kSmem = (size_t)WARPS * (PIECE * 4 + QBYTES);
+    // shared memory: a warp's first and last piece, and its query fragments
+    static constexpr size_t kSmem = (size_t)WARPS * (2 * PIECE * 4 + QBYTES);
     static_assert(kSmem <= 227 * 1024 - 2048, "");
     // weights are held times 2^kOff: f16's subnormals then start at 2^-31 of the maximum
     static constexpr float kOff = kF16 ? 7.f : 0.f;
@@ -266,8 +267,9 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
     const MoeAttnArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int n_req = a.n_requests, HG = p.n_kv * p.n_groups;
-    float *my_piece = reinterpret_cast<float *>(smem) + warp * C::PIECE;
-    uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::WARPS * C::PIECE * 4) + warp * C::QFRAGS * 32;
+    float *pieces = reinterpret_cast<float *>(smem);  // [2 warps]
+    float *my_piece = pieces + 2 * warp * C::PIECE;   // a segment that began before the run; one that starts in it
+    uint2 *qsm = reinterpret_cast<uint2 *>(pieces + 2 * C::WARPS * C::PIECE) + warp * C::QFRAGS * 32;
 
     // cost of each run of 32 requests (steps, and kSegCost for each request that has any)
     auto cost_of = [&](int b) {
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                     const bool in = nt * 8 + g < heads && q_dim(i) < p.k_dim;
                     const char *s = q + q_dim(i) * q_bytes;
                     if (!p.q16) {  // rows off 16 bytes: by twos, through shared memory
-                        char *mine = reinterpret_cast<char *>(my_piece) + lane * 32;
+                        char *mine = reinterpret_cast<char *>(my_piece + C::PIECE) + lane * 32;
 #pragma unroll 1
                         for (int e = 0; in && e < 8 * q_bytes; e += 2)
                             *reinterpret_cast<uint16_t *>(mine + e) = *reinterpret_cast<const uint16_t *>(s + e);
@@ -820,12 +822,9 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
             __syncwarp();
 
             // The segment's end, or the run's.  The whole segment goes to the
-            // output; a piece of it to the block: one that began before the run
-            // to the warp's place in the workspace, one that goes on to its place
-            // in shared memory.
+            // output, a piece of it to the block's join.
             const bool whole = sb >= wb && se <= we, before = sb < wb;
-            float *pc = before ? p.part + (size_t)(2 * gridDim.x + blockIdx.x * C::WARPS + warp) * C::PIECE
-                               : my_piece;
+            float *pc = my_piece + (before ? 0 : C::PIECE);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -895,10 +894,9 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
         const int row = e % CELLS / (DMAX / 4), d = 4 * (e % (DMAX / 4));
         float *to = sh.more ? p.part + (size_t)(2 * blockIdx.x + (sh.before ? 0 : 1)) * C::PIECE : nullptr;
         // the first warp's piece began in its run, unless the segment did in another block
-        const float *of0 = sh.before ? p.part + (size_t)(2 * gridDim.x + blockIdx.x * C::WARPS) * C::PIECE
-                                     : reinterpret_cast<const float *>(smem) + sh.warp * C::PIECE;
-        const float *rest = p.part + (size_t)(2 * gridDim.x + blockIdx.x * C::WARPS + sh.warp) * C::PIECE;
-        join_pieces<C::ROWS, DMAX, 8>(p, [&](int i) { return i == 0 ? of0 : rest + i * C::PIECE; }, sh.n, sh.b, sh.hg,
+        const float *of = pieces + (2 * sh.warp + (sh.before ? 0 : 1)) * C::PIECE;
+        const float *rest = pieces + 2 * sh.warp * C::PIECE;
+        join_pieces<C::ROWS, DMAX, 8>(p, [&](int i) { return i == 0 ? of : rest + 2 * i * C::PIECE; }, sh.n, sh.b, sh.hg,
                                    row, d, to);
     }
     bool open = false;

@@ -28,7 +28,7 @@ cudaError_t attn_prepare(const MoeAttnDesc &d, size_t *block_floats, int *groups
                                                         (int)f.smem);
             if (ce != cudaSuccess) return ce;
             const int per = (d.n_heads / d.n_kv_heads + f.rows - 1) / f.rows;
-            const size_t n = (size_t)f.piece * (2 + f.threads / 32);
+            const size_t n = 2 * (size_t)f.piece;
             if (n > *block_floats) *block_floats = n;
             if (d.n_kv_heads * per > *groups) *groups = d.n_kv_heads * per;
         }
