@@ -129,6 +129,28 @@ __device__ __forceinline__ void store_vec(uint8_t *p, const float (&v)[8]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
 }
 
+// The operators of a decode step follow one another in a stream, each a few
+// microseconds long: they are launched with programmatic stream serialisation,
+// so that a kernel's launch overlaps the one before it, and touch no memory
+// before that one is done (1 x 6144 block norm 3.35 -> 2.94 us a call in a row).
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+inline cudaError_t launch_after(const void *fn, int grid, int block, size_t smem, cudaStream_t s, void **args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelExC(&c, fn, args);
+}
+
 // Host launchers (defined in the .cu files).
 struct KvPlanArgs {
     const int32_t *past, *fresh;

@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
     __shared__ int group_cost[MOE_MAX_REQUESTS / kGroupReq];
     __shared__ Shared shared[C::WARPS + 1];
     __shared__ int n_shared, last_of[2];
+    after_previous();
     const MoeAttnArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int n_req = a.n_requests, HG = p.n_kv * p.n_groups;

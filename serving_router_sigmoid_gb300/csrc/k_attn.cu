@@ -73,8 +73,7 @@ cudaError_t launch_attn_decode(const AttnHandle &h, const MoeAttnArgs &a, cudaSt
     p.arrived = h.arrived;
     p.by_hg = FastDiv((uint32_t)(p.n_kv * p.n_groups));
     void *args[] = {&p};
-    return cudaLaunchKernel(reinterpret_cast<const void *>(f.fn), dim3(h.num_sms), dim3(f.threads), args,
-                            f.smem, s);
+    return launch_after(reinterpret_cast<const void *>(f.fn), h.num_sms, f.threads, f.smem, s, args);
 }
 
 }  // namespace moe

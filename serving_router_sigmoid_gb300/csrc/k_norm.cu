@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, EARLY || V == 1 ? 1 : V *
     block_norm_kernel(const __grid_constant__ MoeNormArgs a) {
     using A = typename Elem<DT>::type;
     __shared__ float red[2][32];
+    after_previous();
     const int nw = blockDim.x >> 5;
     const int64_t t = blockIdx.x;
     const A *x = static_cast<const A *>(a.x) + t * a.x_stride;
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(512, 1)
     constexpr int V = DT == MOE_F32 ? 4 : 8;
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ float red[2][32];
+    after_previous();
     const int nw = blockDim.x >> 5, n_arr = 1 + (a.y != nullptr) + (a.gate != nullptr && a.gate_stride_d != 0);
     auto slot = [&](int st, int arr, int m) -> uint4 & {
         return ring[((st * n_arr + arr) * M + m) * blockDim.x + threadIdx.x];
@@ -294,26 +296,28 @@ cudaError_t launch_ring(const MoeNormArgs &a, int threads, int stages, size_t sm
     const cudaError_t ce = cudaFuncSetAttribute(block_norm_ring_kernel<DT, M>,
                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
     if (ce != cudaSuccess) return ce;
-    block_norm_ring_kernel<DT, M><<<num_sms, threads, smem, s>>>(a, stages);
-    return cudaGetLastError();
+    void *args[] = {const_cast<MoeNormArgs *>(&a), &stages};
+    return launch_after(reinterpret_cast<const void *>(block_norm_ring_kernel<DT, M>), num_sms, threads, smem, s, args);
 }
 
 // One block a row, m accesses a thread.
 template <int DT, int V, bool EARLY>
 cudaError_t launch_rows(const MoeNormArgs &a, int m, int threads, cudaStream_t s) {
+    void (*fn)(MoeNormArgs) = nullptr;
     switch (m) {
-        case 1: block_norm_kernel<DT, V, 1, EARLY><<<a.n_tokens, threads, 0, s>>>(a); break;
-        case 2: block_norm_kernel<DT, V, 2, EARLY><<<a.n_tokens, threads, 0, s>>>(a); break;
+        case 1: fn = block_norm_kernel<DT, V, 1, EARLY>; break;
+        case 2: fn = block_norm_kernel<DT, V, 2, EARLY>; break;
         case 4:
-            if constexpr (!EARLY || V == 4) block_norm_kernel<DT, V, 4, EARLY><<<a.n_tokens, threads, 0, s>>>(a);
+            if constexpr (!EARLY || V == 4) fn = block_norm_kernel<DT, V, 4, EARLY>;
             break;
         case 8:
-            if constexpr (!EARLY && V <= 4) block_norm_kernel<DT, V, 8, EARLY><<<a.n_tokens, threads, 0, s>>>(a);
+            if constexpr (!EARLY && V <= 4) fn = block_norm_kernel<DT, V, 8, EARLY>;
             break;
         default:
-            if constexpr (V == 1) block_norm_kernel<DT, V, 16, EARLY><<<a.n_tokens, threads, 0, s>>>(a);
+            if constexpr (V == 1) fn = block_norm_kernel<DT, V, 16, EARLY>;
     }
-    return cudaGetLastError();
+    void *args[] = {const_cast<MoeNormArgs *>(&a)};
+    return launch_after(reinterpret_cast<const void *>(fn), a.n_tokens, threads, 0, s, args);
 }
 
 // The form of the kernel, from sizes alone.  Measured on fp32 / bf16 rows with
