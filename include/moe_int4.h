@@ -538,7 +538,7 @@ typedef struct {
 
 /*
  * Create / destroy an attention handle: the workspace in which a call joins
- * what it splits.  It owns that device memory (8 to 12 MiB at 128 dimensions on
+ * what it splits.  It owns that device memory (1 to 3 MiB at 128 dimensions on
  * 152 SMs, and 4 bytes for each request and group of 8 query heads) and serves
  * one stream at a time, on the device current at create.
  * Destroying NULL is accepted.  Errors: INVALID_ARG, SHAPE, NOMEM, CUDA.

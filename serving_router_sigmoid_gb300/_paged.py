@@ -96,22 +96,26 @@ def _ints(name, t, shape, dtype=torch.int32):
 
 
 def _table(t, rows):
-    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] < rows or (t.shape[1] > 1 and t.stride(1) != 1):
+    """Entries of a row of a block table, and their distance between rows."""
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != 2 or shape[0] < rows or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"block_table: expected int32 [>= {rows}, pages] with contiguous rows, "
-                         f"got {t.dtype} {tuple(t.shape)}")
+                         f"got {t.dtype} {tuple(shape)}")
+    return shape[1], t.stride(0)
 
 
 def _caches(k_cache, v_cache, heads, k_dim, v_dim):
-    """MOE_* type of a pair of caches [pages, page_size, heads, dim] (any strides, contiguous rows)."""
-    kind = _CACHE.get(k_cache.dtype)
-    ks = k_cache.shape
-    if kind is None or len(ks) != 4 or ks[2] != heads or ks[3] != k_dim or k_cache.stride(3) != 1 or (
-            v_cache is not None and (v_cache.dtype is not k_cache.dtype or v_cache.stride(-1) != 1 or
-                                     v_cache.shape != (ks[0], ks[1], heads, v_dim))):
+    """Of a pair of caches [pages, page_size, heads, dim] (any strides, contiguous
+    rows; v_cache None: no values): MOE_* type, strides, pages and page size."""
+    dt, ks, kst = k_cache.dtype, k_cache.shape, k_cache.stride()
+    kind, vst = _CACHE.get(dt), (0, 0, 0, 1) if v_cache is None else v_cache.stride()
+    if kind is None or len(ks) != 4 or ks[2] != heads or ks[3] != k_dim or kst[3] != 1 or (
+            v_cache is not None and (v_cache.dtype is not dt or v_cache.shape != (ks[0], ks[1], heads, v_dim) or
+                                     vst[3] != 1)):
         raise ValueError(f"expected caches [pages, page_size, {heads}, {k_dim}] and [.., .., {heads}, {v_dim}] of one "
                          f"type (float16, bfloat16 or float8_e4m3fn) with contiguous rows, got "
                          f"{[None if c is None else (c.dtype, tuple(c.shape)) for c in (k_cache, v_cache)]}")
-    return kind
+    return kind, kst, vst, ks[0], ks[1]
 
 
 class KvPlan:
@@ -144,12 +148,12 @@ class KvPlan:
         _ints("new_len", new_len, (n,))
         _ints("free_pages", free_pages, (free_pages.numel(),))
         _ints("free_head", free_head, (1,))
-        _table(block_table, n)
+        cols, row = _table(block_table, n)
         if self.q_start.shape[0] != n + 1:
             self.q_start, self.seq_len = self._start[:n + 1], self._len[:n]
         _check(_lib.moe_kv_plan(past_len.data_ptr(), new_len.data_ptr(), n, free_pages.data_ptr(), free_pages.shape[0],
-                                free_head.data_ptr(), self.page_size, block_table.data_ptr(), block_table.stride(0),
-                                block_table.shape[1], self.max_new_tokens, *self._out, _raw(stream, dev)))
+                                free_head.data_ptr(), self.page_size, block_table.data_ptr(), row, cols,
+                                self.max_new_tokens, *self._out, _raw(stream, dev)))
         return self
 
 
@@ -175,8 +179,6 @@ class Rope:
         self.amplitude, self._dev = amplitude.value, _device(device)
         self.turns = turns.to(torch.device("cuda", self._dev))
         self._turns_ptr = self.turns.data_ptr()
-        self._args = ctypes.create_string_buffer(_ROPE_ARGS.size)
-        self._args_ptr = ctypes.addressof(self._args)
 
     def append(self, q, k, v, positions, slots, k_cache, v_cache, q_out=None, k_scale=1.0, v_scale=1.0, stream=None):
         """q [n, heads, dim] -> rotated (q_out, or a new tensor, returned);
@@ -186,34 +188,35 @@ class Rope:
         head strides are free.  E4M3 caches hold x / scale."""
         dev = self._dev
         _here(dev, q, k, v, positions, slots, k_cache, v_cache, q_out)
-        n, heads, dim = q.shape
-        kv_heads = k.shape[1]
-        act, v_dim = _ACT.get(q.dtype), 0 if v is None else v.shape[2]
+        if q.dim() != 3 or k.dim() != 3 or (v is not None and v.dim() != 3) or (q_out is not None and q_out.dim() != 3):
+            raise ValueError("q, k, v and q_out: expected [n, heads, dim]")
+        shape, dt, kv_heads = q.shape, q.dtype, k.shape[1]
+        n, heads, dim = shape
+        act, v_dim = _ACT.get(dt), 0 if v is None else v.shape[2]
         if act is None:
-            raise ValueError(f"q: expected float32, float16 or bfloat16, got {q.dtype}")
+            raise ValueError(f"q: expected float32, float16 or bfloat16, got {dt}")
         if q_out is None:
-            q_out = _empty((n, heads, dim), q, q.dtype, dev, stream)
-        if k.dtype is not q.dtype or k.shape != (n, kv_heads, dim) or q.stride(2) != 1 or k.stride(2) != 1 or \
-                (v is not None and (v.dtype is not q.dtype or v.shape != (n, kv_heads, v_dim) or v.stride(2) != 1)) or \
-                q_out.dtype is not q.dtype or q_out.shape != q.shape or q_out.stride(2) != 1:
-            raise ValueError(f"expected q, q_out {(n, heads, dim)}, k {(n, kv_heads, dim)} and v of {q.dtype} with "
-                             f"contiguous rows, got {[None if t is None else (t.dtype, tuple(t.shape)) for t in (q, q_out, k, v)]}")
+            q_out = _empty((n, heads, dim), q, dt, dev, stream)
+        qs, ks, os, vs = q.stride(), k.stride(), q_out.stride(), (0, 0, 1) if v is None else v.stride()
+        if k.dtype is not dt or k.shape != (n, kv_heads, dim) or q_out.dtype is not dt or q_out.shape != shape or \
+                qs[2] != 1 or ks[2] != 1 or os[2] != 1 or vs[2] != 1 or \
+                (v is not None and (v.dtype is not dt or v.shape != (n, kv_heads, v_dim))):
+            raise ValueError(f"expected q, q_out {(n, heads, dim)}, k {(n, kv_heads, dim)} and v of {dt} with contiguous "
+                             f"rows, got {[None if t is None else (t.dtype, tuple(t.shape)) for t in (q, q_out, k, v)]}")
         if positions.dtype is not torch.int32 or slots.dtype is not torch.int64 or positions.dim() != 1 or \
                 slots.dim() != 1 or positions.shape[0] < n or slots.shape[0] < n or \
                 not positions.is_contiguous() or not slots.is_contiguous():
             raise ValueError(f"expected contiguous positions int32 and slots int64 of at least {n} entries")
-        cache = _caches(k_cache, v_cache, kv_heads, dim, v_dim)
         if (v is None) != (v_cache is None):
             raise ValueError("v and v_cache go together")
-        qs, ks, os, kcs = q.stride(), k.stride(), q_out.stride(), k_cache.stride()
-        vs, vcs = (0, 0, 1) if v is None else v.stride(), (0, 0, 0, 1) if v is None else v_cache.stride()
-        _ROPE_ARGS.pack_into(
-            self._args, 0, n, heads, kv_heads, dim, v_dim, self.rot_dim, self.rot_offset, self.interleaved, act, cache,
-            k_cache.shape[1], self._turns_ptr, self.amplitude, k_scale, v_scale, positions.data_ptr(),
-            slots.data_ptr(), k_cache.shape[0], q.data_ptr(), k.data_ptr(), 0 if v is None else v.data_ptr(),
-            q_out.data_ptr(), k_cache.data_ptr(), 0 if v is None else v_cache.data_ptr(),
-            qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], kcs[0], kcs[1], kcs[2], vcs[0], vcs[1], vcs[2])
-        _check(_lib.moe_rope_append(self._args_ptr, _raw(stream, dev)))
+        cache, kcs, vcs, pages, page = _caches(k_cache, v_cache, kv_heads, dim, v_dim)
+        args = _ROPE_ARGS.pack(
+            n, heads, kv_heads, dim, v_dim, self.rot_dim, self.rot_offset, self.interleaved, act, cache,
+            page, self._turns_ptr, self.amplitude, k_scale, v_scale, positions.data_ptr(), slots.data_ptr(), pages,
+            q.data_ptr(), k.data_ptr(), 0 if v is None else v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+            0 if v is None else v_cache.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], kcs[0],
+            kcs[1], kcs[2], vcs[0], vcs[1], vcs[2])
+        _check(_lib.moe_rope_append(args, _raw(stream, dev)))
         return q_out
 
 
@@ -224,14 +227,12 @@ class PagedAttention:
     def __init__(self, max_requests, n_heads, n_kv_heads, head_dim, v_dim=None, device="cuda"):
         self.n_heads, self.n_kv_heads = int(n_heads), int(n_kv_heads)
         self.head_dim, self.v_dim = int(head_dim), int(head_dim if v_dim is None else v_dim)
-        self._dev = _device(device)
+        self._dev, self._scale = _device(device), 1.0 / math.sqrt(self.head_dim)
         desc = MoeAttnDesc(int(max_requests), self.n_heads, self.n_kv_heads, self.head_dim, self.v_dim)
         h = ctypes.c_void_p()
         with torch.cuda.device(self._dev):
             _check(_lib.moe_attn_create(ctypes.byref(desc), ctypes.byref(h)))
         self.handle = h
-        self._args = ctypes.create_string_buffer(_ATTN_ARGS.size)
-        self._args_ptr = ctypes.addressof(self._args)
 
     def close(self):
         if getattr(self, "handle", None) is not None and self.handle.value:
@@ -252,34 +253,33 @@ class PagedAttention:
         sqrt(dim) unless given; window > 0: the last `window` tokens only.
         Returns (out [n, heads, v_dim], lse [n, heads] fp32); a request that
         sees no token gets 0 and -inf."""
-        dev = self._dev
+        dev, heads, v_dim, dt = self._dev, self.n_heads, self.v_dim, q.dtype
         _here(dev, q, k_cache, v_cache, block_table, seq_len, out, lse)
-        n = q.shape[0]
-        act = _ACT.get(q.dtype)
-        if act is None or q.shape != (n, self.n_heads, self.head_dim) or q.stride(2) != 1:
-            raise ValueError(f"q: expected float32, float16 or bfloat16 [n, {self.n_heads}, {self.head_dim}] with "
-                             f"contiguous rows, got {q.dtype} {tuple(q.shape)}")
-        cache = _caches(k_cache, v_cache, self.n_kv_heads, self.head_dim, self.v_dim)
-        _table(block_table, n)
+        shape, act, qs = q.shape, _ACT.get(dt), q.stride()
+        n = shape[0] if shape else 0
+        if act is None or shape != (n, heads, self.head_dim) or qs[2] != 1:
+            raise ValueError(f"q: expected float32, float16 or bfloat16 [n, {heads}, {self.head_dim}] with contiguous "
+                             f"rows, got {dt} {tuple(shape)}")
+        cache, ks, vs, pages, page = _caches(k_cache, v_cache, self.n_kv_heads, self.head_dim, v_dim)
+        cols, row = _table(block_table, n)
         if seq_len.dtype is not torch.int32 or seq_len.dim() != 1 or seq_len.shape[0] < n or \
                 not seq_len.is_contiguous():
             raise ValueError(f"seq_len: expected a contiguous int32 tensor of at least {n} entries")
         if out is None:
-            out = _empty((n, self.n_heads, self.v_dim), q if self.v_dim == self.head_dim else None, q.dtype, dev, stream)
-        elif out.dtype is not q.dtype or out.shape != (n, self.n_heads, self.v_dim) or out.stride(2) != 1:
-            raise ValueError(f"out: expected {q.dtype} {(n, self.n_heads, self.v_dim)} with contiguous rows")
+            out = _empty((n, heads, v_dim), q if v_dim == self.head_dim else None, dt, dev, stream)
+        elif out.dtype is not dt or out.shape != (n, heads, v_dim) or out.stride(2) != 1:
+            raise ValueError(f"out: expected {dt} {(n, heads, v_dim)} with contiguous rows")
         if lse is None:
-            lse = _empty((n, self.n_heads), None, torch.float32, dev, stream)
+            lse = _empty((n, heads), None, torch.float32, dev, stream)
         else:
-            _ints("lse", lse, (n, self.n_heads), torch.float32)
-        qs, os, ks, vs = q.stride(), out.stride(), k_cache.stride(), v_cache.stride()
-        _ATTN_ARGS.pack_into(
-            self._args, 0, n, act, cache, k_cache.shape[1], block_table.shape[1], window,
-            1.0 / math.sqrt(self.head_dim) if scale is None else scale, k_scale, v_scale, seq_len.data_ptr(),
-            block_table.data_ptr(), block_table.stride(0), k_cache.shape[0], q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), qs[0], qs[1], os[0], os[1], ks[0], ks[1], ks[2], vs[0],
-            vs[1], vs[2])
-        _check(_lib.moe_attn_decode(self.handle, self._args_ptr, _raw(stream, dev)))
+            _ints("lse", lse, (n, heads), torch.float32)
+        os = out.stride()
+        args = _ATTN_ARGS.pack(
+            n, act, cache, page, cols, window, self._scale if scale is None else scale, k_scale,
+            v_scale, seq_len.data_ptr(), block_table.data_ptr(), row, pages, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), qs[0], qs[1], os[0], os[1], ks[0], ks[1], ks[2],
+            vs[0], vs[1], vs[2])
+        _check(_lib.moe_attn_decode(self.handle, args, _raw(stream, dev)))
         return out, lse
 
 

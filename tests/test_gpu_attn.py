@@ -311,3 +311,15 @@ def test_long_fp32_sums_keep_fp32_accuracy(moe, cache, dim):
         s = torch.einsum("hgd,lhd->hgl", b.q[i].double().unflatten(0, (8, -1)), k) / math.sqrt(dim)
         want = torch.einsum("hgl,lhd->hgd", torch.softmax(s, -1), v).flatten(0, 1)
         assert float((out[i].double() - want).norm() / want.norm()) < 2e-6
+
+
+def test_refuses_other_ranks(moe):
+    b = Batch([20, 30], 8, 2, 64, BF16, BF16, 16, seed=1)
+    attn = moe.PagedAttention(2, 8, 2, 64)
+    for bad in (dict(q=b.q[0]), dict(q=b.q[0, 0, 0]), dict(k_cache=b.k[0]), dict(v_cache=b.v[0]),
+                dict(v_cache=b.v[0, 0, 0, 0]), dict(block_table=b.table[0]), dict(seq_len=b.seq[0]), dict(out=b.q[0]),
+                dict(lse=torch.empty(2, device="cuda"))):
+        a = dict(q=b.q, k_cache=b.k, v_cache=b.v, block_table=b.table, seq_len=b.seq)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            attn.decode(**a)

@@ -198,3 +198,40 @@ def test_refusals(moe):
             rope.append(x, x, x, pos, slots, kc, vc, **bad)
     with pytest.raises(moe.MoeError):  # a rotated part longer than the head
         moe.Rope(128).append(x, x, x, pos, slots, kc, vc)
+
+
+def test_refuses_other_ranks(moe):
+    rope = moe.Rope(64)
+    x = torch.randn((4, 2, 64), device="cuda")
+    kc, vc = (torch.zeros((2, 16, 2, 64), dtype=BF16, device="cuda") for _ in range(2))
+    pos, slots = torch.arange(4, dtype=torch.int32, device="cuda"), torch.arange(4, device="cuda")
+    for bad in (dict(q=x[0]), dict(k=x[0]), dict(v=x[0]), dict(q_out=x[0]), dict(positions=pos[0]), dict(slots=slots[0]),
+                dict(k_cache=kc[0]), dict(v_cache=vc[0]), dict(v_cache=vc[0, 0, 0, 0])):
+        a = dict(q=x, k=x, v=x, positions=pos, slots=slots, k_cache=kc, v_cache=vc)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            rope.append(**a)
+
+
+def test_one_object_in_two_threads(moe):
+    """A Rope keeps nothing of a call: threads on streams of their own share it."""
+    from concurrent.futures import ThreadPoolExecutor
+    rope = moe.Rope(64)
+
+    def work(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            x = torch.randn((5 + seed, 2, 64), device="cuda", generator=g)
+            kc, vc = (torch.zeros((2, 16, 2, 64), dtype=BF16, device="cuda") for _ in range(2))
+            n = x.shape[0]
+            pos, slots = torch.arange(n, dtype=torch.int32, device="cuda"), torch.arange(n, device="cuda")
+            first = rope.append(x, x, x, pos, slots, kc, vc)
+            same = torch.ones((), dtype=torch.bool, device="cuda")
+            for _ in range(200):
+                same &= (rope.append(x, x, x, pos, slots, kc, vc) == first).all()
+            s.synchronize()
+            return bool(same) and torch.equal(vc.view(-1, 2, 64)[:n], x.to(BF16))
+
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(work, range(4)))
