@@ -37,6 +37,11 @@
 // bits of it, so that the output's own rounding is the only one that shows;
 // fp32 queries enter in 2 (f16) or 3 (bf16) terms.  For f16 products each query
 // row is scaled by a power of two to about 1, which the logit's factor undoes.
+//
+// Measured: 64 requests of up to 32768 tokens, bf16, 8 key heads of 128 (1.8 GB):
+// 265 to 269 us, 6.8 TB/s; 2 x 131072 tokens E4M3 (537 MB): 95 to 100 us, 5.5
+// TB/s; short calls are a chain of round trips (lengths, page ids, rows, joins):
+// 1 x 777 tokens 9.3 us, 32 x 1024 fp32 queries, 16 key heads of 64: 26.7 us.
 #pragma once
 
 #include "attn_args.cuh"
