@@ -41,7 +41,7 @@
 // Measured: 64 requests of up to 32768 tokens, bf16, 8 key heads of 128 (1.8 GB):
 // 265 to 269 us, 6.8 TB/s; 2 x 131072 tokens E4M3 (537 MB): 95 to 100 us, 5.5
 // TB/s; short calls are a chain of round trips (lengths, page ids, rows, joins):
-// 1 x 777 tokens 9.3 us, 32 x 1024 fp32 queries, 16 key heads of 64: 26.7 us.
+// 1 x 777 tokens 9.3 us, 32 x 1024 fp32 queries, 16 key heads of 64: 24.7 us.
 #pragma once
 
 #include "attn_args.cuh"
@@ -85,9 +85,12 @@ struct Cfg {
     static constexpr int NP = WIDE ? NQ : 2;
     static constexpr int ROWS = 8 * NT;
     static constexpr bool QS = NQ * NT * DMAX > 128;  // query fragments stay in shared memory
-    // one block per SM; registers allow 12 warps of the plain form
-    // (and shared memory 7 of the largest query fragments)
-    static constexpr int WARPS = DMAX <= 128 && NT == 1 && !WIDE ? 12 : DMAX * NT * NQ > 512 ? 7 : 8;
+    // One block per SM.  12 warps of 168 registers up to 128 dimensions and 8 heads
+    // (fp32 queries against 8 warps: 64 x 4096 tokens of 128 dimensions bf16 189 ->
+    // 177 us, E4M3 121 -> 106, 32 ragged windows of 64 f16 26.8 -> 24.7, E4M3 22.3 ->
+    // 23.4).  Larger forms would spill (256 dimensions E4M3 106 -> 145): 8, or the
+    // 7 that shared memory holds with the largest query fragments.
+    static constexpr int WARPS = DMAX <= 128 && NT == 1 ? 12 : DMAX * NT * NQ > 512 ? 7 : 8;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int PIECE = ROWS * (DMAX + 2);  // floats of a piece: O, m, l
     static constexpr int QFRAGS = NQ * NT * KSTEPS;
