@@ -451,7 +451,9 @@ int moe_layer_static_status(cudaStream_t stream, int *status_out);
  *   info      [4] int32 out: new tokens, free_head after the call, MOE_PLAN_*
  *     flags (0: all well), largest seq_len
  * A request that gets no page has -1 in its table row from there on, and the
- * list head stops at n_free.  Nothing but the outputs is changed: a second
+ * list head stops at n_free.  A request that needs more pages than its row
+ * holds takes those that fit; its tokens beyond them have no slot.  So the
+ * pages up to info[1] are those that rows received, whatever the flags.  Nothing but the outputs is changed: a second
  * call on the same inputs gives the same outputs (to go on, copy info[1] to
  * *free_head).  No output may overlap an input (block_table is both).  The
  * lengths' sums stay below 2^31.

@@ -1,8 +1,9 @@
 // k_kvplan.cu -- page allocation, positions and cache slots of a batch's new
 // tokens, from the lengths on the GPU (moe_kv_plan).
 //
-// With have = ceil(past / P), take = ceil((past + new) / P) - have and off the
-// exclusive prefix sum of take over the requests:
+// With have = ceil(past / P) and need = ceil((past + new) / P), both at most the
+// entries of a table row (a page that no row can hold stays on the free list),
+// take = need - have and off the exclusive prefix sum of take over the requests:
 //   table[b, have + j] = free[head + off[b] + j]           (j < take[b])
 //   token i of request b: pos = past + i, slot = table[b, pos / P] * P + pos % P
 //
@@ -78,7 +79,8 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a, FastDiv
             fresh = max(fresh, 0);
         }
         const int need = (int)by_page.div((uint32_t)(past + fresh) + a.page - 1);
-        const int take = need - (int)by_page.div((uint32_t)past + a.page - 1);
+        const int have = (int)by_page.div((uint32_t)past + a.page - 1);
+        const int take = min(need, a.max_pages) - min(have, a.max_pages);
         if (need > a.max_pages) flags |= MOE_PLAN_ROW_FULL;
         longest = max(longest, past + fresh);
         int s = fresh, o = take, ts, to;
@@ -118,7 +120,8 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a, FastDiv
     for (int i = me; i < n_take; i += nthr) {
         const int b = last_le(off, a.n_req, i);
         const int col = (int)by_page.div((uint32_t)max(__ldg(a.past + b), 0) + a.page - 1) + i - off[b];
-        if (col >= 0 && col < a.max_pages) a.table[b * a.table_stride + col] = i < avail ? __ldg(a.free_pages + head + i) : -1;
+        if (col >= 0 && col < a.max_pages)
+            a.table[b * a.table_stride + col] = i < avail ? __ldg(a.free_pages + head + i) : -1;
     }
     // positions and slots
     const bool vec = (reinterpret_cast<uintptr_t>(a.positions) & 15u) == 0 &&
