@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a, FastDiv
     }
     const int nthr = gridDim.x * kThreads, me = blockIdx.x * kThreads + tid;
     // the new pages' table entries
-    for (int i = me; i < n_take; i += nthr) {
+    for (int64_t j = me; j < n_take; j += nthr) {
+        const int i = (int)j;
         const int b = last_le(off, a.n_req, i);
         const int col = (int)by_page.div((uint32_t)max(__ldg(a.past + b), 0) + a.page - 1) + i - off[b];
         if (col >= 0 && col < a.max_pages)

@@ -302,7 +302,7 @@ cudaError_t launch(const MoeRopeArgs &a, bool fast, int num_sms, cudaStream_t s)
     w.by_kv = FastDiv((uint32_t)(a.n_kv_heads > 0 ? a.n_kv_heads : 1));
     w.head_slots = kThreads / w.per_q;
     w.v_slots = w.per_v > 0 ? kThreads / w.per_v : 0;
-    const int grid = (a.n_tokens + w.tok - 1) / w.tok;
+    const int grid = (int)((a.n_tokens + (int64_t)w.tok - 1) / w.tok);
     void (*fn)(MoeRopeArgs, RopeSplit) = !fast            ? rope_append_any_kernel<AT, CT>
                                          : a.interleaved ? rope_append_kernel<AT, CT, false>
                                                          : rope_append_kernel<AT, CT, true>;
