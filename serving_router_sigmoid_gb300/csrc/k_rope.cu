@@ -291,7 +291,7 @@ cudaError_t launch(const MoeRopeArgs &a, bool fast, int num_sms, cudaStream_t s)
     // against 5 of 8)
     int64_t best = INT64_MAX;
     for (int tok = 1; tok <= kMaxTok; ++tok) {
-        const int64_t blocks = (a.n_tokens + tok - 1) / tok, row = (blocks + 3 * num_sms - 1) / (3 * num_sms) * tok;
+        const int64_t blocks = ((int64_t)a.n_tokens + tok - 1) / tok, row = (blocks + 3 * num_sms - 1) / (3 * num_sms) * tok;
         if (row <= best) best = row, w.tok = tok;
         if (blocks <= num_sms) break;
     }
