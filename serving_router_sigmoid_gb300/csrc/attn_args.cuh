@@ -68,6 +68,31 @@ __device__ __forceinline__ uint4 ld_once16(const void *p) {
     return v;
 }
 
+// Loads of a kernel's inputs.  Coherent ones: the kernel before this one may
+// have written them while this one was already resident (after_previous), and
+// the read-only path (__ldg, ld.global.nc) holds only for what nobody writes in
+// a kernel's lifetime.  Volatile, so that none moves above that wait.
+__device__ __forceinline__ int32_t ld_in(const int32_t *p) {
+    int32_t v;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int64_t ld_in(const int64_t *p) {
+    int64_t v;
+    asm volatile("ld.global.s64 %0, [%1];" : "=l"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float ld_in(const float *p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 ld_in4(const float *p) {
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
 // N consecutive elements <-> fp32 registers, in vector accesses of up to 16
 // bytes (the caller guarantees the alignment of N elements, at most 16 bytes).
 template <int N>

@@ -132,14 +132,14 @@ __device__ __forceinline__ float exp2_fast(float x) {  // within 2^-22
 // 171 without; rows of 256 bytes lose 1% at most.)
 __device__ __forceinline__ uint4 ld16(const char *p) {
     uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                  : "l"(p));
     return r;
 }
 __device__ __forceinline__ uint2 ld8(const char *p) {
     uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
     return r;
 }
 // Four e4m3 codes -> two pairs of f16 (exact).
@@ -161,7 +161,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 
 // The tokens of request b that are seen: [from, len).
 __device__ __forceinline__ void seen(const MoeAttnArgs &a, int b, int &from, int &len) {
-    len = min(max(__ldg(a.seq_len + b), 0), a.max_pages * a.page_size);
+    len = min(max(ld_in(a.seq_len + b), 0), a.max_pages * a.page_size);
     from = a.window > 0 ? max(0, len - a.window) : 0;
 }
 
@@ -406,8 +406,8 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
             const int ncol = (int)p.by_page.div(len - 1) + 1;
             if (p.by16) {
                 wcol = (int)p.by_page.div(tok0 + first * C::TT);
-                cur = wcol + lane < ncol ? __ldg(bt + wcol + lane) : -1;
-                nxt = wcol + 32 + lane < ncol ? __ldg(bt + wcol + 32 + lane) : -1;
+                cur = wcol + lane < ncol ? ld_in(bt + wcol + lane) : -1;
+                nxt = wcol + 32 + lane < ncol ? ld_in(bt + wcol + 32 + lane) : -1;
             }
 
             // this lane's pieces of the query, on their way before the first keys
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                     in = at[r] + row;
                 } else {
                     const int col = (int)p.by_page.div(tok);
-                    pg = __ldg(bt + col);
+                    pg = ld_in(bt + col);
                     in = tok - col * a.page_size;
                 }
                 if ((uint32_t)pg >= p.n_pages) {
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         if (col - wcol >= 32) {
                             wcol += 32;
                             cur = nxt;
-                            nxt = wcol + 32 + lane < ncol ? __ldg(bt + wcol + 32 + lane) : -1;
+                            nxt = wcol + 32 + lane < ncol ? ld_in(bt + wcol + 32 + lane) : -1;
                         }
                         page[r] = __shfl_sync(0xffffffffu, cur, (col - wcol) & 31);
                         at[r] = tok - col * a.page_size;
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         for (int h = 0; h < 2; ++h) {
                             const int tok = t + 16 * r + g + 8 * h;
                             bool on = tok >= from && tok < len;
-                            if (on && holes) on = (uint32_t)__ldg(bt + p.by_page.div(tok)) < p.n_pages;
+                            if (on && holes) on = (uint32_t)ld_in(bt + p.by_page.div(tok)) < p.n_pages;
                             if (!on) {
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) s[r][nt][2 * h] = s[r][nt][2 * h + 1] = -INFINITY;

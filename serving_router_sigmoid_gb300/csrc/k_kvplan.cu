@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a, FastDiv
         const int b = base + tid;
         int past = 0, fresh = 0;
         if (b < a.n_req) {
-            past = __ldg(a.past + b);
-            fresh = __ldg(a.fresh + b);
+            past = ld_in(a.past + b);
+            fresh = ld_in(a.fresh + b);
             if (past < 0 || fresh < 0) flags |= MOE_PLAN_NEGATIVE;
             past = max(past, 0);
             fresh = max(fresh, 0);
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a, FastDiv
         n_take += to;
     }
     if (tid == 0) start[a.n_req] = n_new, off[a.n_req] = n_take;
-    int head = __ldg(a.free_head);
+    int head = ld_in(a.free_head);
     if (head < 0) flags |= MOE_PLAN_NEGATIVE, head = 0;
     const int avail = max(a.n_free - head, 0);
     if (first) {
@@ -120,9 +120,9 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a, FastDiv
     for (int64_t j = me; j < n_take; j += nthr) {
         const int i = (int)j;
         const int b = last_le(off, a.n_req, i);
-        const int col = (int)by_page.div((uint32_t)max(__ldg(a.past + b), 0) + a.page - 1) + i - off[b];
+        const int col = (int)by_page.div((uint32_t)max(ld_in(a.past + b), 0) + a.page - 1) + i - off[b];
         if (col >= 0 && col < a.max_pages)
-            a.table[b * a.table_stride + col] = i < avail ? __ldg(a.free_pages + head + i) : -1;
+            a.table[b * a.table_stride + col] = i < avail ? ld_in(a.free_pages + head + i) : -1;
     }
     // positions and slots
     const bool vec = (reinterpret_cast<uintptr_t>(a.positions) & 15u) == 0 &&
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a, FastDiv
             if (t0 + i >= a.max_new || t >= n_new) continue;
             if (b < 0 || t >= start[b + 1]) {
                 b = last_le(start, a.n_req, t);
-                past = max(__ldg(a.past + b), 0);
+                past = max(ld_in(a.past + b), 0);
                 have = (int)by_page.div((uint32_t)past + a.page - 1);
             }
             const int p = past + t - start[b];
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a, FastDiv
                     page = a.table[b * a.table_stride + col];
                 } else {
                     const int f = off[b] + col - have;
-                    if (f >= 0 && f < avail) page = __ldg(a.free_pages + head + f);
+                    if (f >= 0 && f < avail) page = ld_in(a.free_pages + head + f);
                 }
             }
             if (page >= 0) slot[i] = (long long)page * a.page + (p - col * a.page);

@@ -55,9 +55,9 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, EARLY || V == 1 ? 1 : V *
 #pragma unroll
         for (int j = 0; j < V; j += V == 1 ? 1 : 4) {
             if constexpr (V == 1) {
-                v[j] = __ldg(p + j);
+                v[j] = ld_in(p + j);
             } else {
-                const float4 w = __ldg(reinterpret_cast<const float4 *>(p + j));
+                const float4 w = ld_in4(p + j);
                 v[j] = w.x; v[j + 1] = w.y; v[j + 2] = w.z; v[j + 3] = w.w;
             }
         }
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
         for (int j = 0; j < V; j += 4) {
             float4 p = make_float4(1.f, 1.f, 1.f, 1.f), n = p;
-            if (a.w_post && d < a.dim) p = __ldg(reinterpret_cast<const float4 *>(a.w_post + d + j));
-            if (a.w_pre && d < a.dim) n = __ldg(reinterpret_cast<const float4 *>(a.w_pre + d + j));
+            if (a.w_post && d < a.dim) p = ld_in4(a.w_post + d + j);
+            if (a.w_pre && d < a.dim) n = ld_in4(a.w_pre + d + j);
             wp[m][j] = p.x; wp[m][j + 1] = p.y; wp[m][j + 2] = p.z; wp[m][j + 3] = p.w;
             wn[m][j] = n.x; wn[m][j + 1] = n.y; wn[m][j + 2] = n.z; wn[m][j + 3] = n.w;
         }

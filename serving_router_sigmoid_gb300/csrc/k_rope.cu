@@ -56,7 +56,7 @@ __device__ __forceinline__ void fill_angles(const MoeRopeArgs &a, int t0, int nt
     const int half = a.rot_dim >> 1;
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
         const int t = i / half, j = i - t * half;
-        const uint64_t part = a.turns[j] * (uint64_t)(int64_t)__ldg(a.positions + t0 + t);
+        const uint64_t part = a.turns[j] * (uint64_t)(int64_t)ld_in(a.positions + t0 + t);
         // nearest signed 32-bit fraction of a turn = units of 2^-31 half turns
         const int32_t top = (int32_t)(uint32_t)((part + 0x80000000ull) >> 32);
         float s, c;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const __grid_c
     // the first rows are on their way while the angles are formed
     load(hs);
     if (threadIdx.x < nt) {
-        const long long slot = __ldg(a.slots + t0 + threadIdx.x);
+        const long long slot = ld_in(a.slots + t0 + threadIdx.x);
         longlong2 r = make_longlong2(-1, -1);
         if (slot >= 0 && slot < (long long)a.n_pages * a.page_size) {
             const long long page = slot / a.page_size, at = slot - page * a.page_size;
