@@ -173,6 +173,15 @@ __device__ __forceinline__ int block_sum_i(int v, int *red) {
     return r;
 }
 
+// Load of activations: a coherent one, since the kernel before this one in the
+// stream may have written them while this one was already resident (the layer
+// kernel waits for it, griddepcontrol.wait, before these loads).
+__device__ __forceinline__ float4 ld_act(const float4 *p) {
+    float4 r;
+    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "l"(p));
+    return r;
+}
+
 // Streaming 16-byte load of read-once weights: no L1 allocation.
 __device__ __forceinline__ int4 ld_stream16(const void *p) {
     int4 r;

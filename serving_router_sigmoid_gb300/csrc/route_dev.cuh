@@ -34,8 +34,8 @@ __device__ __forceinline__ void quant_token_perm(const float *__restrict__ xrow,
     for (int k = 0; k < G; ++k) {
         const int g = threadIdx.x + 256 * k;
         if (g < ng) {
-            v[2 * k] = __ldg(reinterpret_cast<const float4 *>(xrow + 8 * g));
-            v[2 * k + 1] = __ldg(reinterpret_cast<const float4 *>(xrow + 8 * g + 4));
+            v[2 * k] = ld_act(reinterpret_cast<const float4 *>(xrow + 8 * g));
+            v[2 * k + 1] = ld_act(reinterpret_cast<const float4 *>(xrow + 8 * g + 4));
         } else {
             v[2 * k] = v[2 * k + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -363,7 +363,7 @@ __device__ __forceinline__ void logits_request(WrRegs<NW, X0> &r, const float *_
     for (int j = 0; j < NW; ++j) {
         const int c = j * 32 + lane;
         r.w[j] = c < L8 ? __ldg(wr + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (X0) r.x0[j] = c < L8 ? __ldg(xr + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (X0) r.x0[j] = c < L8 ? ld_act(xr + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -379,7 +379,7 @@ __device__ __forceinline__ float logits_finish(const WrRegs<NW, X0> &r, const fl
         for (int j = 0; j < NW; ++j) {
             const int c = j * 32 + lane;
             if (c < L8) {
-                const float4 xv = (X0 && t == 0) ? r.x0[X0 ? j : 0] : __ldg(xr + c);
+                const float4 xv = (X0 && t == 0) ? r.x0[X0 ? j : 0] : ld_act(xr + c);
                 v = fmaf(r.w[j].x, xv.x, v);
                 v = fmaf(r.w[j].y, xv.y, v);
                 v = fmaf(r.w[j].z, xv.z, v);
@@ -425,7 +425,7 @@ __device__ __forceinline__ void x0_request(WrRegs<NW, true> &r, const float *__r
 #pragma unroll
     for (int j = 0; j < NW; ++j) {
         const int c = j * 32 + lane;
-        r.x0[j] = c < L8 ? __ldg(xr + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        r.x0[j] = c < L8 ? ld_act(xr + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
