@@ -33,9 +33,8 @@
 //
 // Precision: products of the cache's own type (E4M3 codes widen exactly to
 // f16) accumulate in fp32; logits, m, l and O are fp32.  A weight enters the
-// second product in NP terms of 16 bits: 2 terms keep 16 (bf16) or 22 (f16)
-// bits of it, so that the output's own rounding is the only one that shows;
-// fp32 queries enter in 2 (f16) or 3 (bf16) terms.  For f16 products each query
+// second product in NP terms of 16 bits: 3 terms of bf16 keep 24 bits of it, 2
+// of f16 keep 22; fp32 queries enter in as many.  For f16 products each query
 // row is scaled by a power of two to about 1, which the logit's factor undoes.
 //
 // Measured: 64 requests of up to 32768 tokens, bf16, 8 key heads of 128 (1.8 GB):
@@ -82,7 +81,10 @@ struct Cfg {
     static constexpr int R = 32 * DMAX * ES >= 8192 ? 1 : 8192 / (32 * DMAX * ES);
     static constexpr int TT = 16 * R;
     static constexpr int NQ = !WIDE ? 1 : kF16 ? 2 : 3;
-    static constexpr int NP = WIDE ? NQ : 2;
+    static constexpr int NP = kF16 ? 2 : 3;
+    // Weighted values are summed over SUM tiles by the tensor cores and then added
+    // to O in fp32; 0: every product goes straight into O (see the second product).
+    static constexpr int SUM = WIDE ? 1 : kF16 ? 0 : R;
     static constexpr int ROWS = 8 * NT;
     static constexpr bool QS = NQ * NT * DMAX > 128;  // query fragments stay in shared memory
     // One block per SM.  12 warps of 168 registers up to 128 dimensions and 8 heads
@@ -762,20 +764,42 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float x = s[r][nt][2 * h], y = s[r][nt][2 * h + 1];
+                            if constexpr (F16) {
 #pragma unroll
-                            for (int q = 0; q < C::NP; ++q) {
-                                const uint32_t pk = pack2<F16>(x, y);
-                                pb[r][nt][q][h] = transpose8x8(pk);
-                                const float2 z = unpack2<F16>(pk);
-                                x -= z.x;
-                                y -= z.y;
+                                for (int q = 0; q < C::NP; ++q) {
+                                    const uint32_t pk = pack2<F16>(x, y);
+                                    pb[r][nt][q][h] = transpose8x8(pk);
+                                    const float2 z = unpack2<F16>(pk);
+                                    x -= z.x;
+                                    y -= z.y;
+                                }
+                            } else {
+                                // bf16 terms by cutting, 8 bits each, exactly: a weight's
+                                // upper half is its first term.  Both halves change
+                                // lanes, and the rest is cut up there.
+                                const uint32_t a = __float_as_uint(x), e = __float_as_uint(y);
+                                const uint32_t hi = transpose8x8(__byte_perm(a, e, 0x7632));
+                                const uint32_t lo = transpose8x8(__byte_perm(a, e, 0x5410));
+                                pb[r][nt][0][h] = hi;
+                                x = __uint_as_float(__byte_perm(lo, hi, 0x5410)) - __uint_as_float(hi << 16);
+                                y = __uint_as_float(__byte_perm(lo, hi, 0x7632)) - __uint_as_float(hi & 0xFFFF0000u);
+#pragma unroll
+                                for (int q = 1; q < C::NP; ++q) {
+                                    pb[r][nt][q][h] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+                                    x -= __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+                                    y -= __uint_as_float(__float_as_uint(y) & 0xFFFF0000u);
+                                }
                             }
                         }
                     }
 
-                // O^T += V^T P^T
+                // O^T += V^T P^T.  The tensor cores cut a sum's last bits off, and do so
+                // with O's own each time they add to it.  Over many steps that shows (fp32
+                // outputs of 24 x 8192 tokens: 3.3e-6; bf16 caches, 64 ragged requests:
+                // other last places in 0.2% of the outputs), so fp32 queries and bf16
+                // caches take a step's products by a rounded add, fp32 ones of each tile.
 #pragma unroll
-                for (int r = 0; r < C::R; ++r)
+                for (int r0 = 0; r0 < C::R; r0 += C::SUM ? C::SUM : C::R)
 #pragma unroll
                     for (int i = 0; i < C::VCH; ++i) {
                         // (two words together, so that an accumulator's terms do not
@@ -783,43 +807,44 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         constexpr int PER = C::ES == 1 ? 2 : 1;  // pairs of dimensions a word
 #pragma unroll
                         for (int j = 0; j < C::VB / 4; j += 2) {
-                            uint32_t am[2 * PER][4];
-#pragma unroll
-                            for (int jj = 0; jj < 2; ++jj) {
-                                const uint32_t w0 = vr[r][0][i][j + jj], w1 = vr[r][1][i][j + jj],
-                                               w2 = vr[r][2][i][j + jj], w3 = vr[r][3][i][j + jj];
-                                uint32_t(&m)[4] = am[jj * PER];
-                                if constexpr (C::ES == 1) {  // a dimension's codes of two tokens side by side
-                                    uint32_t(&m1)[4] = am[jj * PER + PER - 1];
-                                    e4m3x4_to_f16x4(__byte_perm(w0, w1, 0x5140), m[0], m[1]);
-                                    e4m3x4_to_f16x4(__byte_perm(w2, w3, 0x5140), m[2], m[3]);
-                                    e4m3x4_to_f16x4(__byte_perm(w0, w1, 0x7362), m1[0], m1[1]);
-                                    e4m3x4_to_f16x4(__byte_perm(w2, w3, 0x7362), m1[2], m1[3]);
-                                } else {
-                                    m[0] = __byte_perm(w0, w1, 0x5410);
-                                    m[1] = __byte_perm(w0, w1, 0x7632);
-                                    m[2] = __byte_perm(w2, w3, 0x5410);
-                                    m[3] = __byte_perm(w2, w3, 0x7632);
-                                }
-                            }
-                            // The tensor cores cut a sum's last bits off: over many
-                            // steps that shows in fp32 outputs (3.3e-6 of 24 x 8192
-                            // tokens), so those take a step's sum by a rounded add.
-                            float part[WIDE ? 2 * PER : 1][NT][4];
-                            if constexpr (WIDE) {
+                            float part[C::SUM ? 2 * PER : 1][NT][4];
+                            if constexpr (C::SUM > 0) {
 #pragma unroll
                                 for (int x = 0; x < 2 * PER * NT * 4; ++x) part[x / (NT * 4)][x / 4 % NT][x % 4] = 0.f;
                             }
 #pragma unroll
-                            for (int q = 0; q < C::NP; ++q)
+                            for (int r = r0; r < r0 + (C::SUM ? C::SUM : C::R); ++r) {
+                                uint32_t am[2 * PER][4];
 #pragma unroll
-                                for (int e = 0; e < 2 * PER; ++e)
+                                for (int jj = 0; jj < 2; ++jj) {
+                                    const uint32_t w0 = vr[r][0][i][j + jj], w1 = vr[r][1][i][j + jj],
+                                                   w2 = vr[r][2][i][j + jj], w3 = vr[r][3][i][j + jj];
+                                    uint32_t(&m)[4] = am[jj * PER];
+                                    if constexpr (C::ES == 1) {  // a dimension's codes of two tokens side by side
+                                        uint32_t(&m1)[4] = am[jj * PER + PER - 1];
+                                        e4m3x4_to_f16x4(__byte_perm(w0, w1, 0x5140), m[0], m[1]);
+                                        e4m3x4_to_f16x4(__byte_perm(w2, w3, 0x5140), m[2], m[3]);
+                                        e4m3x4_to_f16x4(__byte_perm(w0, w1, 0x7362), m1[0], m1[1]);
+                                        e4m3x4_to_f16x4(__byte_perm(w2, w3, 0x7362), m1[2], m1[3]);
+                                    } else {
+                                        m[0] = __byte_perm(w0, w1, 0x5410);
+                                        m[1] = __byte_perm(w0, w1, 0x7632);
+                                        m[2] = __byte_perm(w2, w3, 0x5410);
+                                        m[3] = __byte_perm(w2, w3, 0x7632);
+                                    }
+                                }
 #pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-                                        mma<F16>(WIDE ? part[WIDE ? e : 0][nt] : o[nt][i * (C::VE / 2) + j * PER + e],
-                                                 am[e][0], am[e][1], am[e][2], am[e][3], pb[r][nt][q][0],
-                                                 pb[r][nt][q][1]);
-                            if constexpr (WIDE) {
+                                for (int q = 0; q < C::NP; ++q)
+#pragma unroll
+                                    for (int e = 0; e < 2 * PER; ++e)
+#pragma unroll
+                                        for (int nt = 0; nt < NT; ++nt)
+                                            mma<F16>(C::SUM ? part[C::SUM ? e : 0][nt]
+                                                            : o[nt][i * (C::VE / 2) + j * PER + e],
+                                                     am[e][0], am[e][1], am[e][2], am[e][3], pb[r][nt][q][0],
+                                                     pb[r][nt][q][1]);
+                            }
+                            if constexpr (C::SUM > 0) {
 #pragma unroll
                                 for (int x = 0; x < 2 * PER * NT * 4; ++x)
                                     o[x / 4 % NT][i * (C::VE / 2) + j * PER + x / (NT * 4)][x % 4] +=
