@@ -65,7 +65,7 @@ constexpr int kSegCost = 4;         // what a segment costs besides its steps, i
 constexpr int kShort = 4;           // steps a warp up to which a segment is not shared among blocks
 constexpr int kGroupReq = 32;       // requests whose costs are summed together
 constexpr float kLazy = 8.f;        // the maximum moves when a logit passes it by 2^kLazy
-constexpr float kFloor = -1e38f;    // running maximum before any token
+constexpr float kFloor = -3.4028235e38f;  // running maximum before any token: no logit lies below
 
 template <int CT, int DMAX, int NT, bool WIDE>
 struct Cfg {
