@@ -34,8 +34,9 @@
 // Precision: products of the cache's own type (E4M3 codes widen exactly to
 // f16) accumulate in fp32; logits, m, l and O are fp32.  A weight enters the
 // second product in NP terms of 16 bits: 3 terms of bf16 keep 24 bits of it, 2
-// of f16 keep 22; fp32 queries enter in as many.  For f16 products each query
-// row is scaled by a power of two to about 1, which the logit's factor undoes.
+// of f16 keep 22; fp32 queries enter in as many.  For f16 products, and where a
+// first bf16 term could round to infinity, each query row is scaled by a power of
+// two to about 1, which the logit's factor undoes.
 //
 // Measured: 64 requests of up to 32768 tokens, bf16, 8 key heads of 128 (1.8 GB):
 // 265 to 269 us, 6.8 TB/s; 2 x 131072 tokens E4M3 (537 MB): 95 to 100 us, 5.5
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(Cfg<CT, DMAX, NT, WIDE>::THREADS, 1)
                         }
                     }
                     float pw = 1.f;
-                    if (F16) {
+                    if (F16 || WIDE) {
                         float top = 0.f;
     #pragma unroll
                         for (int i = 0; i < NI; ++i)

@@ -85,3 +85,14 @@ def test_logits_near_the_end_of_fp32(moe, act, cache, k_size, length):
         keys = torch.full((n, length), least, device="cuda")
         keys[torch.arange(n), winner] = most
         check(moe, act, cache, length, winner, torch.full((n,), sign * 2.0**126 / k_size, device="cuda"), keys * k_size, 2.0)
+
+
+@pytest.mark.parametrize("length", [2, 300])
+def test_the_largest_queries(moe, length):
+    """Queries of the type's largest value on keys so small that the logits are ordinary."""
+    n = 4
+    winner = torch.arange(n, device="cuda") * (length - 1) // (n - 1)
+    for act, top in ((F32, 3.4028234e38), (BF16, 3.3895314e38)):
+        keys = torch.full((n, length), -2.0**-119, device="cuda")
+        keys[torch.arange(n), winner] = 2.0**-119
+        check(moe, act, BF16, length, winner, torch.full((n,), top, device="cuda"), keys, 0.5)
