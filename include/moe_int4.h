@@ -543,6 +543,8 @@ typedef struct {
  * what it splits.  It owns that device memory (1 to 3 MiB at 128 dimensions on
  * 152 SMs, and 4 bytes for each request and group of 8 query heads) and serves
  * one stream at a time, on the device current at create.
+ * Both wait for the device: not while a stream is capturing.  Graphs that
+ * captured a call use the workspace: destroy the handle after them.
  * Destroying NULL is accepted.  Errors: INVALID_ARG, SHAPE, NOMEM, CUDA.
  */
 int moe_attn_create(const MoeAttnDesc *desc, void **handle_out);

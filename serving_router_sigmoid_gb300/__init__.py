@@ -93,6 +93,19 @@ def _check(rc: int) -> None:
         raise MoeError(rc, _lib.moe_last_error().decode(errors="replace"))
 
 
+_parked = []  # handles dropped while a stream was capturing
+
+
+def _destroy(destroy, handle) -> None:
+    """Destroys a handle; during a stream capture, which the wait for the device
+    that belongs to it would break, leaves that to the next call outside one."""
+    _parked.append((destroy, handle))
+    if not torch.cuda.is_current_stream_capturing():
+        while _parked:
+            f, h = _parked.pop()
+            _check(f(h))
+
+
 def _ptr(t):
     if t is None:
         return None
@@ -203,8 +216,8 @@ class MoeLayer:
 
     def close(self):
         if getattr(self, "handle", None) is not None and self.handle.value:
-            _check(_lib.moe_layer_destroy(self.handle))
-            self.handle = None
+            handle, self.handle = self.handle, None
+            _destroy(_lib.moe_layer_destroy, handle)
 
     def __del__(self):
         try:

@@ -14,7 +14,7 @@ import struct
 
 import torch
 
-from . import _check, _lib, _stream
+from . import _check, _destroy, _lib, _stream
 
 MOE_F32, MOE_F16, MOE_BF16, MOE_E4M3 = 0, 1, 2, 3
 MOE_PLAN_NO_PAGES, MOE_PLAN_ROW_FULL, MOE_PLAN_NO_ROOM, MOE_PLAN_NEGATIVE = 1, 2, 4, 8
@@ -222,7 +222,8 @@ class Rope:
 
 class PagedAttention:
     """Attention of one new token per request over a paged cache (an owned
-    handle of moe_attn_create; one stream at a time)."""
+    handle of moe_attn_create; one stream at a time).  Keep it as long as a CUDA
+    graph that captured its calls."""
 
     def __init__(self, max_requests, n_heads, n_kv_heads, head_dim, v_dim=None, device="cuda"):
         self.n_heads, self.n_kv_heads = int(n_heads), int(n_kv_heads)
@@ -236,8 +237,8 @@ class PagedAttention:
 
     def close(self):
         if getattr(self, "handle", None) is not None and self.handle.value:
-            _check(_lib.moe_attn_destroy(self.handle))
-            self.handle = None
+            handle, self.handle = self.handle, None
+            _destroy(_lib.moe_attn_destroy, handle)
 
     def __del__(self):
         try:

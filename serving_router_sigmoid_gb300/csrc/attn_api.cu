@@ -174,9 +174,13 @@ int moe_attn_destroy(void *handle) {
     if (!handle) return MOE_OK;
     AttnHandle *h = static_cast<AttnHandle *>(handle);
     if (h->magic != kAttnMagic) return fail(MOE_ERR_INVALID_ARG, "invalid handle");
+    int dev = h->device;
+    cudaGetDevice(&dev);
+    if (dev != h->device) cudaSetDevice(h->device);  // its device is the one to wait for
     const cudaError_t ce = cudaDeviceSynchronize();
     cudaFree(h->part);
     cudaFree(h->arrived);
+    if (dev != h->device) cudaSetDevice(dev);
     h->magic = 0;
     delete h;
     return ce == cudaSuccess ? MOE_OK : cuda_fail(ce, "destroy");
