@@ -175,11 +175,12 @@ __device__ __forceinline__ void copy16(void *smem, const void *gmem) {
                  : "memory");
 }
 
-// The same for many rows of at least 8 KB: one block per SM goes through rows
-// blockIdx, + gridDim, ...; a ring of row copies in shared memory keeps
-// `stages` - 1 rows on their way while one is computed.  A thread copies just
-// the pieces it will read, so its own wait_group is all the ring needs.  Both
-// weights stay in registers.
+// The same for many long rows: one block per SM goes through rows blockIdx,
+// + gridDim, ...; a ring of row copies in shared memory keeps `stages` - 1 rows
+// on their way while one is computed.  A thread copies just the pieces it will
+// read, so its own wait_group is all the ring needs.  Both weights stay in
+// registers (of four 16-bit pieces a thread, dim > 12288, some 18 of the 64
+// spill: 1216 x 16384 bf16 49 us against 63 with a block a row).
 constexpr int kRing = 220 * 1024;
 template <int DT, int M>
 __global__ void __launch_bounds__(512, 1)
@@ -328,10 +329,18 @@ cudaError_t launch_rows(const MoeNormArgs &a, int m, int threads, cudaStream_t s
 //                     36.9 and 304 x 6144: 9.2 / 7.5 against 7.5 / 5.9 (registers:
 //                     fewer rows an SM); so by the rows an SM, the fewer the more
 //                     registers the weights take
-//   ring of copies    2048 x 6144: 40 against 46 fp32, 4096 x 6144: 76 / 61 against
-//                     82 / 67 (floor 75 / 38); but 608 x 6144: 14.5 / 11.8 against
-//                     13.0 / 10.3 and rows of 4 KB 33.9 against 17.8; so from 8 rows
-//                     an SM, of more than 8 KB
+//   ring of copies    from 8 rows an SM, where a block a row is few rows an SM
+//                     (registers): of 16 bits, one row beyond 8192: 1216 x 9216 26.9
+//                     against 52.8, 4096 x 16384 152 against 206; two beyond 5120:
+//                     4096 x 8192 67.7 against 79.3, 4096 x 6144 59.9 against 66.5,
+//                     1216 x 6144 19.6 against 19.2; three below: 4096 x 5120 58.3
+//                     against 47.2.  fp32 brings twice the bytes a row: 4096 x 6144
+//                     77.0 against 81.1, 2048 x 5632 39.9 against 40.3; but beyond, with
+//                     fewer copies, 4096 x 8192 without a gate 93.0 against 81.9 (with
+//                     one 100.6 against 104.7), and
+//                     below, with three rows an SM, 4096 x 4096 54.8 against 53.7, 4096 x
+//                     2304 46.2 against 29.9; and at 4 rows an SM 608 x 6144 14.5 / 11.8
+//                     against 13.0 / 10.3
 template <int DT>
 cudaError_t launch_dt(const MoeNormArgs &a, int num_sms, cudaStream_t s) {
     constexpr int V = DT == MOE_F32 ? 4 : 8;
@@ -344,19 +353,21 @@ cudaError_t launch_dt(const MoeNormArgs &a, int num_sms, cudaStream_t s) {
                      on(a.w_post, 0) && on(a.w_pre, 0) && (!full_gate || on(a.gate, a.gate_stride_t));
     const int most = vec ? 512 : 1024;  // threads a block
     const int acc = vec ? a.dim / V : a.dim;
-    if (vec && acc > 512 && a.n_tokens >= 8 * (int64_t)num_sms) {
-        const int m = (acc + 511) / 512, threads = ((acc + m - 1) / m + 31) / 32 * 32;
-        const size_t row = (size_t)16 * m * threads * (1 + (a.y != nullptr) + full_gate);
-        const int stages = (int)(kRing / row < 4 ? kRing / row : 4);
-        if (stages >= 2 && m <= 4) {
-            if (m == 2) return launch_ring<DT, 2>(a, threads, stages, row * stages, num_sms, s);
-            if (m == 3) return launch_ring<DT, 3>(a, threads, stages, row * stages, num_sms, s);
-            return launch_ring<DT, 4>(a, threads, stages, row * stages, num_sms, s);
-        }
-    }
     int m = 1;
     while (acc > m * most) m *= 2;
     const int threads = ((acc + m - 1) / m + 31) / 32 * 32;
+    const int pieces = (acc + 511) / 512;  // a thread of the ring
+    if (vec && a.n_tokens >= 8 * (int64_t)num_sms && (m * V > 16 || (m * V == 16 && threads > 65536 / 64 / 3)) &&
+        (DT != MOE_F32 || pieces == 3)) {
+        const int ring = ((acc + pieces - 1) / pieces + 31) / 32 * 32;
+        const size_t row = (size_t)16 * pieces * ring * (1 + (a.y != nullptr) + full_gate);
+        const int stages = (int)(kRing / row < 4 ? kRing / row : 4);  // 2 at least: 96 KB are the longest rows
+        if constexpr (DT != MOE_F32) {
+            if (pieces == 2) return launch_ring<DT, 2>(a, ring, stages, row * stages, num_sms, s);
+            if (pieces == 4) return launch_ring<DT, 4>(a, ring, stages, row * stages, num_sms, s);
+        }
+        return launch_ring<DT, 3>(a, ring, stages, row * stages, num_sms, s);
+    }
     if (!vec) return launch_rows<DT, 1, false>(a, m, threads, s);
     const bool early = m * V <= 4 || a.n_tokens <= (m * V <= 8 ? 4 : m * V <= 16 ? 1 : 0) * (int64_t)num_sms;
     return early ? launch_rows<DT, V, true>(a, m, threads, s) : launch_rows<DT, V, false>(a, m, threads, s);
