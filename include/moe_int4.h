@@ -521,9 +521,9 @@ typedef struct {
 /*
  * Rotary positions on q and k, and k and v into the paged cache.
  *   (a, b) -> amplitude * (a cos - b sin, a sin + b cos), the angle position *
- *   theta_i reduced to a part of a turn in 64-bit integers (no error but that
- *   of theta_i, 2^-53 of it, times the position), the rest in 32 bits, one
- *   rounding to the output type.
+ *   theta_i reduced to the nearest quarter turn in 64-bit integers (no error
+ *   but that of theta_i, 2^-53 of it, times the position), the rest of the
+ *   angle and all else in 32 bits, one rounding to the output type.
  * Distinct tokens have distinct slots.  q, k, v may be views of one buffer.
  * Any alignment; fastest when every row starts on 16 bytes.
  * Errors: INVALID_ARG, SHAPE, CUDA.

@@ -4,8 +4,10 @@
 // Pair i of a rotated head turns by position * theta_i.  theta_i / (2 pi) is
 // held as a fraction of 2^64, so the part of a turn is the low half of a
 // 64-bit integer product, exact at every position, where an fp32 angle would
-// lose 17 bits at position 131072; sincospif takes its top 32 bits as a signed
-// fraction of half a turn.  (No 64-bit floating point, which is slow here.)
+// lose 17 bits at position 131072.  Quarter turns are taken off in integers, and
+// sincospif takes what is left, rounded to fp32: off by 2^-24 of itself, 2^-27
+// half turns at most, and by 2^-33.  (No 64-bit floating point, which is slow
+// here.)
 //
 // Bound by HBM: each element is read once and written once.  A block handles a
 // few tokens; it forms their cos and sin once in shared memory (every head of a
@@ -57,10 +59,18 @@ __device__ __forceinline__ void fill_angles(const MoeRopeArgs &a, int t0, int nt
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
         const int t = i / half, j = i - t * half;
         const uint64_t part = a.turns[j] * (uint64_t)(int64_t)ld_in(a.positions + t0 + t);
-        // nearest signed 32-bit fraction of a turn = units of 2^-31 half turns
-        const int32_t top = (int32_t)(uint32_t)((part + 0x80000000ull) >> 32);
+        // the nearest quarter turn, and the rest in units of 2^-32 half turns (at
+        // most 2^30 of them)
+        const uint32_t quarter = (uint32_t)((part + (1ull << 61)) >> 62);
+        const int64_t rest = (int64_t)(part - ((uint64_t)quarter << 62));
         float s, c;
-        sincospif((float)top * 0x1p-31f, &s, &c);
+        sincospif((float)(int32_t)((rest + (1ll << 30)) >> 31) * 0x1p-32f, &s, &c);
+        if (quarter & 1) {
+            const float t = c;
+            c = -s;
+            s = t;
+        }
+        if (quarter & 2) c = -c, s = -s;
         cs[i] = make_float2(c * a.amplitude, s * a.amplitude);
     }
 }
