@@ -472,16 +472,23 @@ int moe_kv_plan(const int32_t *past_len, const int32_t *new_len, int n_requests,
 #define MOE_ROPE_PARTS 3  /* by parts: pairs that turn more than beta_fast times
                            * in original_len positions keep their frequency, those
                            * below beta_slow turns are divided by factor, linear
-                           * between; amplitude 0.1 ln(factor) + 1 (YaRN, Peng et
-                           * al. 2023) */
+                           * in the turns between; amplitude 0.1 ln(factor) + 1
+                           * (the formula of YaRN, Peng et al. 2023; with
+                           * amplitude 1 in MoeRopeArgs the form that some
+                           * checkpoints take) */
+#define MOE_ROPE_PARTS_INDEX 4 /* the same, but linear in the pair's index: from the
+                           * last whole index with beta_fast turns or more to the
+                           * first with beta_slow or fewer, both in [0, rot_dim);
+                           * what checkpoints trained under that name take */
 
 typedef struct {
     int rot_dim;        /* rotated dimensions of a head; even, 2..512 */
     double base;        /* frequency of pair i: base^(-2 i / rot_dim); > 0 */
     int scaling;        /* MOE_ROPE_* */
-    double factor;      /* >= 1 (LINEAR, NTK, PARTS) */
-    int original_len;   /* context length before scaling (PARTS), >= 1 */
-    double beta_fast, beta_slow; /* PARTS: turns, beta_fast > beta_slow */
+    double factor;      /* >= 1 (all but NONE) */
+    int original_len;   /* context length before scaling (PARTS*), >= 1 */
+    double beta_fast, beta_slow; /* PARTS*: turns, beta_fast > beta_slow;
+                                  * PARTS_INDEX: beta_slow > 0 and base > 1 */
 } MoeRopeDesc;
 
 /*

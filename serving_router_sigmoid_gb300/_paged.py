@@ -18,7 +18,7 @@ from . import _check, _destroy, _lib, _stream
 
 MOE_F32, MOE_F16, MOE_BF16, MOE_E4M3 = 0, 1, 2, 3
 MOE_PLAN_NO_PAGES, MOE_PLAN_ROW_FULL, MOE_PLAN_NO_ROOM, MOE_PLAN_NEGATIVE = 1, 2, 4, 8
-MOE_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+MOE_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "parts_by_index": 4}
 
 _ACT = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
 _CACHE = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_E4M3}
@@ -162,21 +162,24 @@ class Rope:
     head (moe_rope_turns, moe_rope_append).
 
     interleaved: pairs (2i, 2i+1), else (i, i + rot_dim/2).  scaling: "none",
-    "linear", "ntk" or "parts" (with factor; parts also original_len,
-    beta_fast, beta_slow), for contexts longer than the trained one.
+    "linear", "ntk", "parts" or "parts_by_index" (with factor; parts also
+    original_len, beta_fast, beta_slow), for contexts longer than the trained
+    one: "parts" goes from kept to divided frequencies linearly in a pair's
+    turns, "parts_by_index" in its index.  amplitude: factor on cos and sin,
+    that of the scaling unless given (parts: 0.1 ln(factor) + 1, else 1).
     """
 
     def __init__(self, rot_dim, base=10000.0, interleaved=False, rot_offset=0, scaling="none", factor=1.0,
-                 original_len=4096, beta_fast=32.0, beta_slow=1.0, device="cuda"):
+                 original_len=4096, beta_fast=32.0, beta_slow=1.0, device="cuda", amplitude=None):
         if scaling not in MOE_ROPE_SCALINGS:
             raise ValueError(f"scaling {scaling!r}: expected one of {sorted(MOE_ROPE_SCALINGS)}")
         self.rot_dim, self.rot_offset, self.interleaved = int(rot_dim), int(rot_offset), bool(interleaved)
         desc = MoeRopeDesc(self.rot_dim, float(base), MOE_ROPE_SCALINGS[scaling], float(factor), int(original_len),
                            float(beta_fast), float(beta_slow))
         turns = torch.zeros(max(1, self.rot_dim // 2), dtype=torch.int64)
-        amplitude = ctypes.c_float(0)
-        _check(_lib.moe_rope_turns(ctypes.byref(desc), turns.data_ptr(), ctypes.byref(amplitude)))
-        self.amplitude, self._dev = amplitude.value, _device(device)
+        own = ctypes.c_float(0)
+        _check(_lib.moe_rope_turns(ctypes.byref(desc), turns.data_ptr(), ctypes.byref(own)))
+        self.amplitude, self._dev = own.value if amplitude is None else float(amplitude), _device(device)
         self.turns = turns.to(torch.device("cuda", self._dev))
         self._turns_ptr = self.turns.data_ptr()
 

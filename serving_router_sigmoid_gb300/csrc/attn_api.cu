@@ -33,6 +33,18 @@ double rope_theta(const MoeRopeDesc &d, int i) {
         keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
         theta *= keep + (1 - keep) / d.factor;
     }
+    if (d.scaling == MOE_ROPE_PARTS_INDEX) {
+        // the index, a real number, whose pair turns n times in original_len
+        const auto index = [&](double n) {
+            return d.rot_dim * std::log(d.original_len / (2 * M_PI * n)) / (2 * std::log(d.base));
+        };
+        const double last = d.rot_dim - 1;
+        const double from = std::fmin(std::fmax(std::floor(index(d.beta_fast)), 0), last);
+        const double to = std::fmin(std::fmax(std::ceil(index(d.beta_slow)), 0), last);
+        double part = to > from ? (i - from) / (to - from) : i > from;
+        part = part < 0 ? 0 : part > 1 ? 1 : part;
+        theta *= 1 - part + part / d.factor;
+    }
     return theta;
 }
 
@@ -69,20 +81,23 @@ int moe_rope_turns(const MoeRopeDesc *d, uint64_t *turns_host, float *amplitude_
     if (d->rot_dim < 2 || d->rot_dim > kMaxRopeDim || d->rot_dim % 2)
         return fail(MOE_ERR_SHAPE, "rot_dim=%d: need an even number in 2..%d", d->rot_dim, kMaxRopeDim);
     if (!finite_pos(d->base)) return fail(MOE_ERR_INVALID_ARG, "base must be positive");
-    if (d->scaling < MOE_ROPE_NONE || d->scaling > MOE_ROPE_PARTS)
+    if (d->scaling < MOE_ROPE_NONE || d->scaling > MOE_ROPE_PARTS_INDEX)
         return fail(MOE_ERR_INVALID_ARG, "unknown scaling %d", d->scaling);
     if (d->scaling != MOE_ROPE_NONE && !(d->factor >= 1 && std::isfinite(d->factor)))
         return fail(MOE_ERR_INVALID_ARG, "factor must be at least 1");
-    if (d->scaling == MOE_ROPE_PARTS &&
+    const bool parts = d->scaling == MOE_ROPE_PARTS || d->scaling == MOE_ROPE_PARTS_INDEX;
+    if (parts &&
         (d->original_len < 1 || !(d->beta_fast > d->beta_slow) || !std::isfinite(d->beta_fast - d->beta_slow)))
         return fail(MOE_ERR_INVALID_ARG, "parts scaling needs original_len >= 1 and beta_fast > beta_slow");
+    if (d->scaling == MOE_ROPE_PARTS_INDEX && !(d->beta_slow > 0 && d->base > 1))
+        return fail(MOE_ERR_INVALID_ARG, "parts scaling by index needs beta_slow > 0 and base > 1");
     for (int i = 0; i < d->rot_dim / 2; ++i) {
         double turns = rope_theta(*d, i) / (2 * M_PI);
         turns -= std::floor(turns);
         const double fixed = std::rint(std::ldexp(turns, 64));
         turns_host[i] = fixed >= 0x1p64 ? 0 : (uint64_t)fixed;
     }
-    *amplitude_host = d->scaling == MOE_ROPE_PARTS ? (float)(0.1 * std::log(d->factor) + 1.0) : 1.f;
+    *amplitude_host = parts ? (float)(0.1 * std::log(d->factor) + 1.0) : 1.f;
     return MOE_OK;
 }
 
