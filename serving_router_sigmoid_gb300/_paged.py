@@ -53,6 +53,13 @@ for _name, _args in {
     getattr(_lib, _name).restype = _ci
 
 
+_UNPACKABLE = (struct.error, OverflowError)
+
+
+def _refuse(error):
+    raise ValueError(f"an argument is out of range or of another kind: {error}") from None
+
+
 def _device(device) -> int:
     d = torch.device(device)
     if d.type != "cuda":
@@ -140,7 +147,7 @@ class KvPlan:
     def update(self, past_len, new_len, free_pages, free_head, block_table, stream=None):
         """past_len, new_len int32 [n]; free_pages int32 [n_free]; free_head
         int32 [1]; block_table int32 [>= n, pages], updated in place."""
-        n, dev = past_len.shape[0], self._dev
+        n, dev = past_len.shape[0] if past_len.dim() else -1, self._dev
         if n > self.max_requests:
             raise ValueError(f"{n} requests: the plan holds {self.max_requests}")
         _here(dev, past_len, new_len, free_pages, free_head, block_table)
@@ -213,12 +220,15 @@ class Rope:
         if (v is None) != (v_cache is None):
             raise ValueError("v and v_cache go together")
         cache, kcs, vcs, pages, page = _caches(k_cache, v_cache, kv_heads, dim, v_dim)
-        args = _ROPE_ARGS.pack(
-            n, heads, kv_heads, dim, v_dim, self.rot_dim, self.rot_offset, self.interleaved, act, cache,
-            page, self._turns_ptr, self.amplitude, k_scale, v_scale, positions.data_ptr(), slots.data_ptr(), pages,
-            q.data_ptr(), k.data_ptr(), 0 if v is None else v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
-            0 if v is None else v_cache.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], kcs[0],
-            kcs[1], kcs[2], vcs[0], vcs[1], vcs[2])
+        try:
+            args = _ROPE_ARGS.pack(
+                n, heads, kv_heads, dim, v_dim, self.rot_dim, self.rot_offset, self.interleaved, act, cache,
+                page, self._turns_ptr, self.amplitude, k_scale, v_scale, positions.data_ptr(), slots.data_ptr(), pages,
+                q.data_ptr(), k.data_ptr(), 0 if v is None else v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+                0 if v is None else v_cache.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], kcs[0],
+                kcs[1], kcs[2], vcs[0], vcs[1], vcs[2])
+        except _UNPACKABLE as e:
+            _refuse(e)
         _check(_lib.moe_rope_append(args, _raw(stream, dev)))
         return q_out
 
@@ -278,11 +288,14 @@ class PagedAttention:
         else:
             _ints("lse", lse, (n, heads), torch.float32)
         os = out.stride()
-        args = _ATTN_ARGS.pack(
-            n, act, cache, page, cols, window, self._scale if scale is None else scale, k_scale,
-            v_scale, seq_len.data_ptr(), block_table.data_ptr(), row, pages, q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), qs[0], qs[1], os[0], os[1], ks[0], ks[1], ks[2],
-            vs[0], vs[1], vs[2])
+        try:
+            args = _ATTN_ARGS.pack(
+                n, act, cache, page, cols, window, self._scale if scale is None else scale, k_scale,
+                v_scale, seq_len.data_ptr(), block_table.data_ptr(), row, pages, q.data_ptr(), k_cache.data_ptr(),
+                v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), qs[0], qs[1], os[0], os[1], ks[0], ks[1], ks[2],
+                vs[0], vs[1], vs[2])
+        except _UNPACKABLE as e:
+            _refuse(e)
         _check(_lib.moe_attn_decode(self.handle, args, _raw(stream, dev)))
         return out, lse
 
@@ -327,9 +340,12 @@ def block_norm(x, y=None, w_post=None, gate=None, w_pre=None, alpha=1.0, beta=1.
         gt = 0 if gate.shape[0] == 1 else gate.stride(0)
         gd = 0 if gate.shape[1] == 1 else gate.stride(1)
     ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    args = _NORM_ARGS.pack(n, dim, act, gate_act == "sigmoid", alpha, beta, eps, x.data_ptr(), ptr(y), ptr(w_post),
-                           ptr(w_pre), ptr(gate), out.data_ptr(), ptr(normed), x.stride(0),
-                           0 if y is None else y.stride(0), out.stride(0), 0 if normed is None else normed.stride(0),
-                           gt, gd)
+    try:
+        args = _NORM_ARGS.pack(n, dim, act, gate_act == "sigmoid", alpha, beta, eps, x.data_ptr(), ptr(y), ptr(w_post),
+                               ptr(w_pre), ptr(gate), out.data_ptr(), ptr(normed), x.stride(0),
+                               0 if y is None else y.stride(0), out.stride(0), 0 if normed is None else normed.stride(0),
+                               gt, gd)
+    except _UNPACKABLE as e:
+        _refuse(e)
     _check(_lib.moe_block_norm(args, _raw(stream, dev)))
     return out, normed

@@ -1,0 +1,50 @@
+"""Arguments that do not fit their field or have another rank are refused as
+ValueError, like all other arguments of the paged-cache operators; numbers
+beyond fp32 reach the library as infinities and are refused there."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import serving_router_sigmoid_gb300 as m
+    torch.cuda.set_device(0)
+    return m
+
+
+def test_numbers(moe):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.randn((2, 4, 64), device="cuda")
+    cache = torch.zeros((4, 16, 4, 64), dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.zeros((2, 2), **i32), torch.ones(2, **i32)
+    attn, rope = moe.PagedAttention(2, 4, 4, 64), moe.Rope(64)
+    attn.decode(q, cache, cache, table, lens)
+    for bad in (dict(window=2**31), dict(window=1.5), dict(window=None), dict(scale="1"), dict(v_scale=None)):
+        with pytest.raises(ValueError):
+            attn.decode(q, cache, cache, table, lens, **bad)
+    for bad in (dict(scale=1e39), dict(k_scale=1e300)):
+        with pytest.raises(moe.MoeError):
+            attn.decode(q, cache, cache, table, lens, **bad)
+    slots = torch.arange(2, device="cuda")
+    for bad, error in ((dict(k_scale=1e39), moe.MoeError), (dict(v_scale="1"), ValueError)):
+        with pytest.raises(error):
+            rope.append(q, q, q, lens, slots, cache, cache.clone(), **bad)
+    x = torch.randn((2, 64), device="cuda")
+    for bad, error in ((dict(alpha=1e39), moe.MoeError), (dict(beta=None), ValueError), (dict(eps="0"), ValueError)):
+        with pytest.raises(error):
+            moe.block_norm(x, x.clone(), **bad)
+
+
+def test_plan_ranks(moe):
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    plan, t = moe.KvPlan(2, 8, 16), torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    ok = [i32([1, 2]), i32([1, 1]), i32([3, 4]), i32([0]), t]
+    plan.update(*ok)
+    for at in range(5):
+        for other in (lambda a: a.flatten()[0], lambda a: a[None]):
+            bad = list(ok)
+            bad[at] = other(bad[at])
+            with pytest.raises(ValueError):
+                plan.update(*bad)
