@@ -44,12 +44,6 @@ __device__ __forceinline__ void from_f32(float v, float &o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, __half &o) { o = __float2half_rn(v); }
 __device__ __forceinline__ void from_f32(float v, __nv_bfloat16 &o) { o = __float2bfloat16_rn(v); }
 
-// Two e4m3 codes of the low 16 bits -> two f16 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-    uint32_t r;
-    asm("{ .reg .b16 c; cvt.u16.u32 c, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(r) : "r"(codes));
-    return r;
-}
 // lo, hi -> two e4m3 codes (nearest, ties to even, saturating), lo in the low byte.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     uint32_t r;
@@ -195,8 +189,9 @@ cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t s);
 cudaError_t launch_rope_append(const MoeRopeArgs &a, cudaStream_t s);
 cudaError_t launch_block_norm(const MoeNormArgs &a, cudaStream_t s);
 
-// What an attention handle holds; ws: partial results, counters: arrivals of
-// the blocks that share a request's head group.
+// What an attention handle holds; part: pieces of the segments that blocks
+// share, arrived: how many of a segment's blocks have left theirs (a counter a
+// request and head group, zero between calls).
 struct AttnHandle {
     uint32_t magic;
     int device, num_sms;
