@@ -453,10 +453,12 @@ int moe_layer_static_status(cudaStream_t stream, int *status_out);
  * A request that gets no page has -1 in its table row from there on, and the
  * list head stops at n_free.  A request that needs more pages than its row
  * holds takes those that fit; its tokens beyond them have no slot.  So the
- * pages up to info[1] are those that rows received, whatever the flags.  Nothing but the outputs is changed: a second
- * call on the same inputs gives the same outputs (to go on, copy info[1] to
- * *free_head).  No output may overlap an input (block_table is both).  The
- * lengths' sums stay below 2^31.
+ * pages up to info[1] are those that rows received, whatever the flags.
+ * Nothing but the outputs is changed: a second call on the same inputs gives
+ * the same outputs (to go on, copy info[1] to *free_head).  No output may
+ * overlap an input or another output (block_table is both): lengths and head
+ * of the next call come from a copy of this one's seq_len and info[1], or from
+ * another plan's.  The lengths' sums stay below 2^31.
  * 0 <= n_requests <= MOE_MAX_REQUESTS, 1 <= page_size <= 65536.
  * Errors: INVALID_ARG, SHAPE, CUDA.
  */

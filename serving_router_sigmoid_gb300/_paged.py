@@ -131,7 +131,8 @@ class KvPlan:
     Owns the outputs of `update`: q_start [n + 1], seq_len [n], positions
     [max_new_tokens] int32, slots [max_new_tokens] int64 (-1: no token, or no
     page for it) and info [4] int32 (new tokens, list head after the call,
-    MOE_PLAN_* flags, largest seq_len).  To go on, copy info[1:2] to free_head.
+    MOE_PLAN_* flags, largest seq_len).  To go on, copy info[1:2] to free_head and
+    seq_len to past_len: the plan's own outputs are refused as its inputs.
     """
 
     def __init__(self, max_requests, max_new_tokens, page_size, device="cuda"):

@@ -21,6 +21,16 @@ bool is_act(int t) { return t == MOE_F32 || t == MOE_F16 || t == MOE_BF16; }
 bool is_cache(int t) { return t == MOE_F16 || t == MOE_BF16 || t == MOE_E4M3; }
 bool finite_pos(double v) { return v > 0 && std::isfinite(v); }
 
+// Bytes of an array.
+struct Span {
+    const void *p;
+    size_t n;
+    bool meets(const Span &o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return n && o.n && a < b + o.n && b < a + n;
+    }
+};
+
 // Frequencies theta_i of a rotary description, in 64 bits.
 double rope_theta(const MoeRopeDesc &d, int i) {
     double base = d.base;
@@ -70,6 +80,18 @@ int moe_kv_plan(const int32_t *past_len, const int32_t *new_len, int n_requests,
         return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
     if ((n_free > 0 && !free_pages) || (max_new_tokens > 0 && (!positions || !slots)))
         return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+    // every block reads the inputs while others write the outputs
+    const size_t n = (size_t)n_requests;
+    const size_t row = max_pages > 0 && n ? (n - 1) * (size_t)table_stride + max_pages : 0;
+    const Span in[] = {{past_len, 4 * n}, {new_len, 4 * n}, {free_pages, 4 * (size_t)n_free}, {free_head, 4}};
+    const Span out[] = {{q_start, 4 * (n + 1)}, {seq_len, 4 * n}, {positions, 4 * (size_t)max_new_tokens},
+                        {slots, 8 * (size_t)max_new_tokens}, {info, 16}, {block_table, 4 * row}};
+    for (const Span &o : out) {
+        for (const Span &i : in)
+            if (o.meets(i)) return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input");
+        for (const Span &p : out)
+            if (&o != &p && o.meets(p)) return fail(MOE_ERR_INVALID_ARG, "two outputs overlap");
+    }
     moe::KvPlanArgs a{past_len, new_len, n_requests, free_pages, n_free, free_head, page_size, block_table,
                       table_stride, max_pages, max_new_tokens, q_start, seq_len, positions, slots, info};
     const cudaError_t ce = moe::launch_kv_plan(a, stream);

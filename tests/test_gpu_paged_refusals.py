@@ -48,3 +48,20 @@ def test_plan_ranks(moe):
             bad[at] = other(bad[at])
             with pytest.raises(ValueError):
                 plan.update(*bad)
+
+
+def test_plan_outputs_as_inputs(moe):
+    """The plan's own outputs would be read while they are written; another plan's are fine."""
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    past, one, free, head = i32([0, 40]), i32([1, 1]), i32([7, 3, 5, 6]), i32([0])
+    table = i32([[-1] * 4, [1, 2, 4, -1]])
+    plan, other = moe.KvPlan(2, 4, 16), moe.KvPlan(2, 4, 16)
+    plan.update(past, one, free, head, table)
+    for bad in ((plan.seq_len, one, free, head, table), (past, plan.seq_len, free, head, table),
+                (past, one, free, plan.info[1:2], table), (past, one, plan.positions, head, table),
+                (table[0, 1:3], one, free, head, table), (past, one, free, table[1, 3:], table)):
+        with pytest.raises(moe.MoeError):
+            plan.update(*bad)
+    other.update(plan.seq_len, one, free, plan.info[1:2], table)
+    assert other.seq_len.tolist() == [2, 42] and other.slots.tolist() == [7 * 16 + 1, 4 * 16 + 9, -1, -1]
+    assert other.info.tolist() == [2, 1, 0, 42]
