@@ -590,8 +590,9 @@ typedef struct {
  * A request that sees no token (seq_len <= 0) gets out = 0 and lse = -inf.
  * Logits, softmax statistics and sums are held in 32 bits.  The result does
  * not depend on which block finishes first.  May be captured in a CUDA graph.
- * n_requests * max_pages * page_size * (key heads, each counted once for every
- * 8 query heads) stays below 2^34; rows of a cache are 16-byte aligned.
+ * max_pages * page_size stays below 2^31 - 64, n_requests * max_pages *
+ * page_size * (key heads, each counted once for every 8 query heads) below 2^34;
+ * rows of a cache are 16-byte aligned and hold finite numbers where they are read.
  * Errors: INVALID_ARG, SHAPE, CUDA.
  */
 int moe_attn_decode(void *handle, const MoeAttnArgs *args, cudaStream_t stream);

@@ -266,7 +266,8 @@ class PagedAttention:
         strides of 16 bytes, contiguous rows); block_table int32 [>= n, pages];
         seq_len int32 [>= n], the new token's own key included.  scale: 1 /
         sqrt(dim) unless given; window > 0: the last `window` tokens only.
-        Returns (out [n, heads, v_dim], lse [n, heads] fp32); a request that
+        Keys and values that are read are finite (an infinity among the values
+        makes NaN of outputs that the formula gives as infinite).  Returns (out [n, heads, v_dim], lse [n, heads] fp32); a request that
         sees no token gets 0 and -inf."""
         dev, heads, v_dim, dt = self._dev, self.n_heads, self.v_dim, q.dtype
         _here(dev, q, k_cache, v_cache, block_table, seq_len, out, lse)

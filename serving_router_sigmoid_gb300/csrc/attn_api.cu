@@ -235,8 +235,8 @@ int moe_attn_decode(void *handle, const MoeAttnArgs *p, cudaStream_t stream) {
     if (a.max_pages < 0 || a.n_pages < 0 || a.n_pages > INT32_MAX || a.window < 0)
         return fail(MOE_ERR_SHAPE, "max_pages=%d n_pages=%lld window=%d must be >= 0", a.max_pages,
                     (long long)a.n_pages, a.window);
-    if ((int64_t)a.max_pages * a.page_size > INT32_MAX)
-        return fail(MOE_ERR_SHAPE, "max_pages * page_size must stay below 2^31");
+    if ((int64_t)a.max_pages * a.page_size > INT32_MAX - 64)  // a step's end is counted in 32 bits
+        return fail(MOE_ERR_SHAPE, "max_pages * page_size must stay below 2^31 - 64");
     if (!moe::attn_countable(h->d, a))
         return fail(MOE_ERR_SHAPE, "n_requests * max_pages * page_size * key heads is beyond 2^34 token heads");
     if (a.n_requests > 1 && a.table_stride < a.max_pages)

@@ -65,3 +65,14 @@ def test_plan_outputs_as_inputs(moe):
     other.update(plan.seq_len, one, free, plan.info[1:2], table)
     assert other.seq_len.tolist() == [2, 42] and other.slots.tolist() == [7 * 16 + 1, 4 * 16 + 9, -1, -1]
     assert other.info.tolist() == [2, 1, 0, 42]
+
+
+def test_tables_near_2_31_tokens(moe):
+    """A step that ends at a request's last tokens would end beyond 2^31."""
+    q = torch.randn((1, 1, 8), device="cuda")
+    cache, lens = torch.zeros((1, 3, 1, 8), dtype=torch.float16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    table = torch.empty((1, 2**31 // 3), dtype=torch.int32, device="cuda")
+    attn = moe.PagedAttention(1, 1, 1, 8)
+    with pytest.raises(moe.MoeError):
+        attn.decode(q, cache, cache, table, lens)
+    attn.decode(q, cache, cache, table[:, :-22], lens)
