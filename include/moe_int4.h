@@ -622,6 +622,157 @@ typedef struct {
  */
 int moe_block_norm(const MoeNormArgs *args, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The dense half of a block whose checkpoint holds E4M3 matrices with one
+ * scale a 128 x 128 block and whose cache holds one latent row a token
+ * (reader.mx §06: the FP8 blocks; §09: 512 latent and 64 rotary numbers):
+ *   moe_quant_act_fp8   activations as E4M3 codes, one scale for each 128
+ *   moe_fp8_linear      their product with such a matrix
+ *   moe_latent_decode   attention of one new token per request over a paged
+ *                       cache of latent rows (absorbed form)
+ *   moe_latent_prompt   attention of ragged prompts over keys and values
+ *                       expanded a head (expanded form)
+ * They follow the conventions at the top of this file; strides are in
+ * elements.  moe_rope_append writes the latent cache (one key head, no
+ * values, rot_offset = latent_dim).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Rows of activations as E4M3 codes with one fp32 scale for each group of 128
+ * elements (the last group of a row may be shorter):
+ *   scale[t, b] = max(max |x[t, 128 b ..]| / 448, 1e-12)
+ *   x8[t, i]    = E4M3(x[t, i] / scale[t, i / 128]), nearest, ties to even
+ *   x     [n_tokens] rows of dim elements of act_type, x_stride apart
+ *   x8    [n_tokens] rows of dim codes out, x8_stride apart
+ *   scale [n_tokens, ceil(dim / 128)] out, contiguous
+ * dim is a multiple of 16, 16..65536; every row of x and x8 starts on 16 bytes.
+ * No output overlaps x or the other output.
+ * Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+int moe_quant_act_fp8(const void *x, int act_type, int64_t x_stride, int n_tokens, int dim, uint8_t *x8,
+                      int64_t x8_stride, float *scale, cudaStream_t stream);
+
+/* Arguments of moe_fp8_linear (host struct; pointers are device pointers). */
+typedef struct {
+    int n_tokens, n_in, n_out;  /* n_in a multiple of 16, 16..65536; n_out 1..2^20 */
+    int out_type;               /* MOE_F32 / F16 / BF16 */
+    const uint8_t *x8;          /* [n_tokens] rows of n_in E4M3 codes, x_stride apart */
+    const float *x_scale;       /* [n_tokens, ceil(n_in / 128)], contiguous */
+    const uint8_t *w8;          /* [n_out] rows of n_in E4M3 codes, w_stride apart */
+    const float *w_scale;       /* [ceil(n_out / 128), ceil(n_in / 128)], contiguous */
+    void *out;                  /* [n_tokens] rows of n_out, out_stride apart */
+    int64_t x_stride, w_stride, out_stride;
+} MoeFp8LinearArgs;
+
+/*
+ * out[t, o] = sum over blocks b of 128 inputs of
+ *   x_scale[t, b] * w_scale[o / 128, b] * sum over i in b of x8[t, i] * w8[o, i]
+ * Sums are held in fp32; one rounding to out_type.  The layout of w_scale is
+ * that of moe_fp8_block_to_int4.  Rows of x8 and w8 start on 16 bytes.  out
+ * overlaps no input.  Codes of NaN give NaN.
+ * Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+int moe_fp8_linear(const MoeFp8LinearArgs *args, cudaStream_t stream);
+
+/* Sizes of a latent attention handle. */
+typedef struct {
+    int max_requests;  /* 1..MOE_MAX_REQUESTS */
+    int n_heads;       /* 1..1024 */
+    int latent_dim;    /* a multiple of 64, 64..512 */
+    int rope_dim;      /* a multiple of 16, 0..64 */
+} MoeLatentDesc;
+
+/*
+ * Create / destroy a latent attention handle: the workspace in which a call
+ * joins what it splits (it owns that device memory, up to 41 MB).  One stream
+ * at a time, on the device current at create; as with moe_attn_create, both
+ * wait for the device, and graphs that captured a call use the workspace.
+ * Destroying NULL is accepted.  Errors: INVALID_ARG, SHAPE, NOMEM, CUDA.
+ */
+int moe_latent_create(const MoeLatentDesc *desc, void **handle_out);
+int moe_latent_destroy(void *handle);
+
+/* Arguments of moe_latent_decode (host struct; pointers are device pointers). */
+typedef struct {
+    int n_requests;
+    int act_type, cache_type;   /* q and out: MOE_F16 / BF16; cache: the same type, or MOE_E4M3 */
+    int page_size;              /* 1..65536 */
+    int max_pages;              /* entries of a table row */
+    float scale;                /* on q . c */
+    float k_scale;              /* on E4M3 codes, > 0 (1 for the others) */
+    const int32_t *seq_len;     /* [n_requests]; longer than the table row: cut to it */
+    const int32_t *block_table; /* rows table_stride apart */
+    int64_t table_stride;
+    int64_t n_pages;            /* tokens on other page ids are not seen */
+    const void *q;              /* [n_requests, n_heads, latent_dim + rope_dim], rows on 16 bytes */
+    const void *cache;          /* rows of latent_dim + rope_dim on 16 bytes; strides in [0, 2^31) bytes */
+    void *out;                  /* [n_requests, n_heads, latent_dim] */
+    float *lse;                 /* [n_requests, n_heads] contiguous, or NULL */
+    int64_t q_stride_b, q_stride_h, out_stride_b, out_stride_h;
+    int64_t c_stride_page, c_stride_tok;
+} MoeLatentArgs;
+
+/*
+ * Attention of one new token per request over a paged cache whose rows c_j
+ * (latent part, then rotary part) all heads share:
+ *   s_j = scale * k_scale * (q . c_j) over the request's tokens j < seq_len
+ *   out = k_scale * sum softmax(s)_j c_j[0 .. latent_dim);  lse = ln sum exp(s_j)
+ * q holds each head's query with the key expansion absorbed (latent part) and
+ * its rotary part; the value expansion is applied to out by the caller.
+ * A request that sees no token gets out = 0 and lse = -inf.
+ * Logits, statistics and sums are held in fp32; weights enter the second
+ * product rounded to act_type.  The result does not depend on which block
+ * finishes first.  May be captured in a CUDA graph.  Queries and rows that are
+ * read hold finite numbers.  max_pages * page_size stays below 2^31 - 64,
+ * n_requests * max_pages * page_size below 2^36.
+ * Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+int moe_latent_decode(void *handle, const MoeLatentArgs *args, cudaStream_t stream);
+
+/* Arguments of moe_latent_prompt (host struct; pointers are device pointers). */
+typedef struct {
+    int n_requests, n_heads;         /* 0..MOE_MAX_REQUESTS, 1..1024 */
+    int n_queries, n_keys;           /* rows of q and out, rows of k, k_rope and v; each below 2^31 - 256 */
+    int nope_dim, rope_dim, v_dim;   /* multiples of 16: 16..256, 0..64 (together <= 256), 16..256 */
+    int act_type;                    /* MOE_F16 / BF16 */
+    int causal;
+    float scale;
+    const int32_t *q_start, *kv_start; /* [n_requests + 1]: request b holds queries [q_start[b], q_start[b + 1])
+                                        * and keys [kv_start[b], kv_start[b + 1]); neither falls */
+    const void *q;                   /* [n_queries, n_heads, nope_dim + rope_dim] */
+    const void *k;                   /* [n_keys, n_heads, nope_dim] */
+    const void *k_rope;              /* [n_keys, rope_dim], shared by the heads; rope_dim 0: unused */
+    const void *v;                   /* [n_keys, n_heads, v_dim] */
+    void *out;                       /* [n_queries, n_heads, v_dim] */
+    float *lse;                      /* [n_queries, n_heads] contiguous, or NULL */
+    int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h, kr_stride_t, v_stride_t, v_stride_h;
+    int64_t out_stride_t, out_stride_h;
+} MoePromptArgs;
+
+/*
+ * Attention of the new tokens of ragged prompts over expanded keys and values:
+ *   s_ij = scale * (q_i[0 .. nope_dim) . k_j + q_i[nope_dim ..) . k_rope_j)
+ *   out_i = sum over seen j of softmax(s_i)_j v_j;  lse_i = ln sum exp(s_ij)
+ * A request's queries are its last tokens: with causal, query i of nq over nk
+ * keys sees the keys j <= nk - nq + i, else all of them.  A query that sees
+ * none gets out = 0 and lse = -inf.  Rows outside every request are neither
+ * written nor do their values count.  Bounds beyond the rows given are cut.
+ * Logits, statistics and sums are held in fp32; weights enter the second
+ * product rounded to act_type.  Rows of q, k, k_rope and v start on 16 bytes
+ * with strides in [0, 2^38) bytes.  May be captured in a CUDA graph.  The
+ * queries, keys and values of a request are finite.  out overlaps no input.
+ * Errors: INVALID_ARG, SHAPE, CUDA.
+ */
+int moe_latent_prompt(const MoePromptArgs *args, cudaStream_t stream);
+
+/*
+ * Error flags of the four calls above on the current device.  Synchronises
+ * `stream`, reads and clears them.  *status_out (host) receives 0 or 16 (a
+ * bounded wait inside a kernel ran out of time: its results are not valid).
+ * Returns MOE_OK, MOE_ERR_DEVICE when a flag was set, or INVALID_ARG / CUDA.
+ */
+int moe_dense_status(cudaStream_t stream, int *status_out);
+
 #ifdef __cplusplus
 }
 #endif

@@ -351,3 +351,4 @@ def static_status(stream=None) -> int:
 
 from ._paged import (MOE_PLAN_NEGATIVE, MOE_PLAN_NO_PAGES, MOE_PLAN_NO_ROOM, MOE_PLAN_ROW_FULL,  # noqa: E402,F401
                      KvPlan, PagedAttention, Rope, block_norm)
+from ._latent import LatentAttention, dense_status, fp8_linear, latent_prompt, quant_act_fp8  # noqa: E402,F401

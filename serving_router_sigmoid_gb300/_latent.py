@@ -1,0 +1,234 @@
+"""Binding of the FP8 products and the latent attention of libmoe_int4.so:
+moe_quant_act_fp8, moe_fp8_linear, moe_latent_decode and moe_latent_prompt
+(include/moe_int4.h).  Argument checks and marshalling only."""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import _check, _destroy, _lib, _stream
+from ._paged import (_ACT, _UNPACKABLE, MOE_BF16, MOE_E4M3, MOE_F16, _device, _empty, _here, _ints, _raw, _refuse,
+                     _table)
+
+_HALF = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
+_E4M3 = torch.float8_e4m3fn
+
+_vp, _ci, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+
+
+class MoeLatentDesc(ctypes.Structure):
+    _fields_ = [(n, _ci) for n in ("max_requests", "n_heads", "latent_dim", "rope_dim")]
+
+
+# the host structs of the header, field by field ("@": the C compiler's alignment)
+_LINEAR_ARGS = struct.Struct("@4i5P3q")
+_LATENT_ARGS = struct.Struct("@5i2f2P2q4P6q")
+_PROMPT_ARGS = struct.Struct("@9if8P9q")
+
+for _name, _args in {
+        "moe_quant_act_fp8": [_vp, _ci, _i64, _ci, _ci, _vp, _i64, _vp, _vp],
+        "moe_fp8_linear": [_vp, _vp],
+        "moe_latent_create": [ctypes.POINTER(MoeLatentDesc), ctypes.POINTER(_vp)],
+        "moe_latent_destroy": [_vp],
+        "moe_latent_decode": [_vp, _vp, _vp],
+        "moe_latent_prompt": [_vp, _vp],
+        "moe_dense_status": [_vp, ctypes.POINTER(_ci)],
+}.items():
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = _ci
+
+
+def _codes(name, t, rows=None):
+    """A matrix of E4M3 codes with contiguous rows -> its shape and row stride."""
+    if t.dtype not in (_E4M3, torch.uint8) or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (
+            rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name}: expected float8_e4m3fn (or uint8 codes) [{'rows' if rows is None else rows}, dim] with "
+                         f"contiguous rows, got {t.dtype} {tuple(t.shape)}")
+    return t.shape[0], t.shape[1], t.stride(0)
+
+
+def quant_act_fp8(x, x8=None, scale=None, stream=None):
+    """moe_quant_act_fp8: x [n, dim] (float32, float16 or bfloat16, contiguous
+    rows) as E4M3 codes and one scale for each 128 of a row -> (x8 [n, dim]
+    float8_e4m3fn, scale [n, ceil(dim / 128)] float32).  dim is a multiple of 16."""
+    dev = x.get_device()
+    _here(dev, x, x8, scale)
+    act = _ACT.get(x.dtype)
+    if act is None or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"x: expected float32, float16 or bfloat16 [n, dim] with contiguous rows, got {x.dtype} "
+                         f"{tuple(x.shape)}")
+    n, dim = x.shape
+    groups = (dim + 127) // 128
+    if x8 is None:
+        x8 = _empty((n, dim), None, _E4M3, dev, stream)
+    elif x8.shape != (n, dim):
+        raise ValueError(f"x8: expected {(n, dim)}, got {tuple(x8.shape)}")
+    row = _codes("x8", x8)[2]
+    if scale is None:
+        scale = _empty((n, groups), None, torch.float32, dev, stream)
+    else:
+        _ints("scale", scale, (n, groups), torch.float32)
+    try:
+        _check(_lib.moe_quant_act_fp8(x.data_ptr(), act, x.stride(0), n, dim, x8.data_ptr(), row, scale.data_ptr(),
+                                      _raw(stream, dev)))
+    except ctypes.ArgumentError as e:
+        _refuse(e)
+    return x8, scale
+
+
+def fp8_linear(x8, x_scale, w8, scale_inv, out=None, dtype=torch.bfloat16, stream=None):
+    """moe_fp8_linear: the product of activations as quant_act_fp8 gives them,
+    x8 [n, I] and x_scale [n, ceil(I / 128)], with a checkpoint's matrix w8 [O, I]
+    (float8_e4m3fn or its codes) and scale_inv [ceil(O / 128), ceil(I / 128)] ->
+    out [n, O] of `dtype` (float32, float16 or bfloat16; that of `out` if given)."""
+    dev = x8.get_device()
+    _here(dev, x8, x_scale, w8, scale_inv, out)
+    n, inner, xs = _codes("x8", x8)
+    outer, w_inner, ws = _codes("w8", w8)
+    if w_inner != inner:
+        raise ValueError(f"x8 has rows of {inner}, w8 of {w_inner}")
+    blocks = (inner + 127) // 128
+    _ints("x_scale", x_scale, (n, blocks), torch.float32)
+    _ints("scale_inv", scale_inv, ((outer + 127) // 128, blocks), torch.float32)
+    if out is None:
+        out = _empty((n, outer), None, dtype, dev, stream)
+    elif out.shape != (n, outer) or (outer > 1 and out.stride(1) != 1):
+        raise ValueError(f"out: expected {(n, outer)} with contiguous rows, got {tuple(out.shape)}")
+    kind = _ACT.get(out.dtype)
+    if kind is None:
+        raise ValueError(f"out: expected float32, float16 or bfloat16, got {out.dtype}")
+    try:
+        args = _LINEAR_ARGS.pack(n, inner, outer, kind, x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(),
+                                 scale_inv.data_ptr(), out.data_ptr(), xs, ws, out.stride(0))
+    except _UNPACKABLE as e:
+        _refuse(e)
+    _check(_lib.moe_fp8_linear(args, _raw(stream, dev)))
+    return out
+
+
+class LatentAttention:
+    """Attention of one new token per request over a paged cache of latent rows
+    (latent part, then rotary part) that all heads share: an owned handle of
+    moe_latent_create, one stream at a time.  Keep it as long as a CUDA graph that
+    captured its calls."""
+
+    def __init__(self, max_requests, n_heads, latent_dim=512, rope_dim=64, device="cuda"):
+        self.n_heads, self.latent_dim, self.rope_dim = int(n_heads), int(latent_dim), int(rope_dim)
+        self.dim, self._dev = self.latent_dim + self.rope_dim, _device(device)
+        desc = MoeLatentDesc(int(max_requests), self.n_heads, self.latent_dim, self.rope_dim)
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self._dev):
+            _check(_lib.moe_latent_create(ctypes.byref(desc), ctypes.byref(h)))
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            handle, self.handle = self.handle, None
+            _destroy(_lib.moe_latent_destroy, handle)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def decode(self, q, cache, block_table, seq_len, scale, k_scale=1.0, out=None, lse=None, stream=None):
+        """q [n, heads, latent + rope] float16 or bfloat16: each head's query with
+        the key expansion absorbed, then its rotary part; cache [pages, page_size,
+        1, latent + rope] (or without the 1) of q's type or float8_e4m3fn, as
+        Rope.append writes it; block_table int32 [>= n, pages]; seq_len int32 [>= n],
+        the new token's own row included; scale: on q . row (1 / sqrt of the
+        expanded head's size).  Returns (out [n, heads, latent], lse [n, heads] fp32);
+        the value expansion is the caller's.  A request that sees no token gets 0
+        and -inf."""
+        dev, heads, dim, dt = self._dev, self.n_heads, self.dim, q.dtype
+        _here(dev, q, cache, block_table, seq_len, out, lse)
+        act, shape = _HALF.get(dt), q.shape
+        n = shape[0] if shape else 0
+        if act is None or shape != (n, heads, dim) or q.stride(2) != 1:
+            raise ValueError(f"q: expected float16 or bfloat16 [n, {heads}, {dim}] with contiguous rows, got {dt} "
+                             f"{tuple(shape)}")
+        cs, ct = cache.shape, cache.stride()
+        if cache.dtype not in (dt, _E4M3) or len(cs) not in (3, 4) or cs[-1] != dim or ct[-1] != 1 or (
+                len(cs) == 4 and cs[2] != 1):
+            raise ValueError(f"cache: expected {dt} or float8_e4m3fn [pages, page_size, 1, {dim}] with contiguous rows, got "
+                             f"{cache.dtype} {tuple(cs)}")
+        cols, row = _table(block_table, n)
+        if seq_len.dtype is not torch.int32 or seq_len.dim() != 1 or seq_len.shape[0] < n or \
+                not seq_len.is_contiguous():
+            raise ValueError(f"seq_len: expected a contiguous int32 tensor of at least {n} entries")
+        if out is None:
+            out = _empty((n, heads, self.latent_dim), None, dt, dev, stream)
+        elif out.dtype is not dt or out.shape != (n, heads, self.latent_dim) or out.stride(2) != 1:
+            raise ValueError(f"out: expected {dt} {(n, heads, self.latent_dim)} with contiguous rows")
+        if lse is None:
+            lse = _empty((n, heads), None, torch.float32, dev, stream)
+        else:
+            _ints("lse", lse, (n, heads), torch.float32)
+        try:
+            args = _LATENT_ARGS.pack(
+                n, act, act if cache.dtype is dt else MOE_E4M3, cs[1], cols, scale, k_scale, seq_len.data_ptr(),
+                block_table.data_ptr(), row, cs[0], q.data_ptr(), cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                q.stride(0), q.stride(1), out.stride(0), out.stride(1), ct[0], ct[1])
+        except _UNPACKABLE as e:
+            _refuse(e)
+        _check(_lib.moe_latent_decode(self.handle, args, _raw(stream, dev)))
+        return out, lse
+
+
+def latent_prompt(q, k, k_rope, v, q_start, kv_start, scale, causal=True, out=None, lse=None, stream=None):
+    """moe_latent_prompt: attention of the new tokens of ragged prompts over keys
+    and values expanded a head, the rotary part of the keys shared by the heads.
+
+    q [queries, heads, nope + rope], k [keys, heads, nope], k_rope [keys, rope]
+    (None: no rotary part), v [keys, heads, v_dim], all float16 or all bfloat16 with
+    contiguous rows and free strides (k and v may be views of one projection);
+    q_start, kv_start int32 [requests + 1] as KvPlan.q_start: request b holds queries
+    q_start[b] .. q_start[b + 1] and keys kv_start[b] .. kv_start[b + 1].  causal: a
+    request's queries are its last tokens, each sees the keys up to its own.
+    Returns (out [queries, heads, v_dim], lse [queries, heads] fp32); rows behind
+    the last request are left as they were, a query that sees no key gets 0 and -inf."""
+    dev = q.get_device()
+    _here(dev, q, k, k_rope, v, q_start, kv_start, out, lse)
+    dt, act = q.dtype, _HALF.get(q.dtype)
+    if act is None or q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or (k_rope is not None and k_rope.dim() != 2):
+        raise ValueError(f"expected float16 or bfloat16 q, k and v [tokens, heads, dim] and k_rope [tokens, dim], got {dt} "
+                         f"{[None if t is None else tuple(t.shape) for t in (q, k, k_rope, v)]}")
+    (nq, heads, dim), (nk, _, nope), v_dim = q.shape, k.shape, v.shape[2]
+    rope = 0 if k_rope is None else k_rope.shape[1]
+    if out is None:
+        out = _empty((nq, heads, v_dim), None, dt, dev, stream)
+    if lse is None:
+        lse = _empty((nq, heads), None, torch.float32, dev, stream)
+    else:
+        _ints("lse", lse, (nq, heads), torch.float32)
+    for name, t, want in (("q", q, (nq, heads, nope + rope)), ("k", k, (nk, heads, nope)), ("k_rope", k_rope, (nk, rope)),
+                          ("v", v, (nk, heads, v_dim)), ("out", out, (nq, heads, v_dim))):
+        if t is not None and (t.dtype is not dt or t.shape != want or (want[-1] > 1 and t.stride(-1) != 1)):
+            raise ValueError(f"{name}: expected {dt} {want} with contiguous rows, got {t.dtype} {tuple(t.shape)}")
+    n = q_start.shape[0] - 1 if q_start.dim() == 1 else -1
+    _ints("q_start", q_start, (max(n, 0) + 1,))
+    _ints("kv_start", kv_start, (max(n, 0) + 1,))
+    rs = 0 if k_rope is None else k_rope.stride(0)
+    try:
+        args = _PROMPT_ARGS.pack(
+            n, heads, nq, nk, nope, rope, v_dim, act, bool(causal), scale, q_start.data_ptr(), kv_start.data_ptr(),
+            q.data_ptr(), k.data_ptr(), 0 if k_rope is None else k_rope.data_ptr(), v.data_ptr(), out.data_ptr(),
+            lse.data_ptr(), q.stride(0), q.stride(1), k.stride(0), k.stride(1), rs, v.stride(0), v.stride(1),
+            out.stride(0), out.stride(1))
+    except _UNPACKABLE as e:
+        _refuse(e)
+    _check(_lib.moe_latent_prompt(args, _raw(stream, dev)))
+    return out, lse
+
+
+def dense_status(stream=None) -> int:
+    """Reads and clears the error flags that the calls of this module left on the
+    current device (0 when none); synchronises the stream."""
+    v = _ci(0)
+    rc = _lib.moe_dense_status(_stream(stream), ctypes.byref(v))
+    if rc != -5:  # MOE_ERR_DEVICE: the flags are the answer
+        _check(rc)
+    return int(v.value)
