@@ -54,9 +54,4 @@ cudaError_t launch_latent_prompt(const MoePromptArgs &a, cudaStream_t s) {
     return launch_after(fn, (int)(((int64_t)a.n_queries * a.n_heads + 7) / 8), 256, 0, s, args);
 }
 
-cudaError_t dense_status(cudaStream_t s, int *out) {
-    *out = 0;
-    return cudaStreamSynchronize(s);
-}
-
 }  // namespace moe

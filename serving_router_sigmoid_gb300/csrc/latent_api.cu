@@ -71,9 +71,9 @@ int moe_fp8_linear(const MoeFp8LinearArgs *p, cudaStream_t stream) {
     if (!is_act(a.out_type)) return fail(MOE_ERR_INVALID_ARG, "out_type=%d", a.out_type);
     if (a.n_tokens == 0) return MOE_OK;
     const int64_t most = 1ll << 38, oe = (int64_t)moe::dtype_bytes(a.out_type);
-    if ((a.n_tokens > 1 && (a.x_stride < 0 || a.x_stride >= most || a.out_stride < a.n_out || a.out_stride >= most)) ||
-        (a.n_out > 1 && (a.w_stride < 0 || a.w_stride >= most)))
-        return fail(MOE_ERR_SHAPE, "strides must lie in [0, 2^38), out_stride at least n_out");
+    if ((a.n_tokens > 1 && (a.x_stride < a.n_in || a.x_stride >= most || a.out_stride < a.n_out || a.out_stride >= most)) ||
+        (a.n_out > 1 && (a.w_stride < a.n_in || a.w_stride >= most)))
+        return fail(MOE_ERR_SHAPE, "rows may not overlap, strides must stay below 2^38");
     if (!a.x8 || !a.x_scale || !a.w8 || !a.w_scale || !a.out) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
     if (!aligned(a.x8, 16) || !aligned(a.w8, 16) || (a.n_tokens > 1 && a.x_stride % 16) ||
         (a.n_out > 1 && a.w_stride % 16))
@@ -230,7 +230,13 @@ int moe_latent_prompt(const MoePromptArgs *p, cudaStream_t stream) {
 
 int moe_dense_status(cudaStream_t stream, int *status_out) {
     if (!status_out) return fail(MOE_ERR_INVALID_ARG, "status_out is NULL");
-    const cudaError_t e = moe::dense_status(stream, status_out);
+    *status_out = 0;
+    cudaError_t e = cudaStreamSynchronize(stream);
+    for (const auto flags : {moe::fp8_linear_flags}) {
+        int32_t v = 0;
+        if (e == cudaSuccess) e = flags(&v);
+        *status_out |= v;
+    }
     if (e != cudaSuccess) return cuda_fail(e, "dense_status");
     return *status_out ? fail(MOE_ERR_DEVICE, "device flags %d", *status_out) : MOE_OK;
 }

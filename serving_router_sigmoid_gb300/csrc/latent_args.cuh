@@ -22,7 +22,7 @@ cudaError_t launch_fp8_linear(const MoeFp8LinearArgs &a, cudaStream_t s);
 cudaError_t latent_prepare(const MoeLatentDesc &d, int num_sms, size_t *bytes);
 cudaError_t launch_latent_decode(const LatentHandle &h, const MoeLatentArgs &a, cudaStream_t s);
 cudaError_t launch_latent_prompt(const MoePromptArgs &a, cudaStream_t s);
-// Reads and clears the current device's error word; synchronises s.
-cudaError_t dense_status(cudaStream_t s, int *out);
+// The flags that a file's kernels left on the current device, read and cleared.
+cudaError_t fp8_linear_flags(int32_t *out);
 
 }  // namespace moe
