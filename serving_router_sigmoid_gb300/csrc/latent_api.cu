@@ -232,7 +232,7 @@ int moe_dense_status(cudaStream_t stream, int *status_out) {
     if (!status_out) return fail(MOE_ERR_INVALID_ARG, "status_out is NULL");
     *status_out = 0;
     cudaError_t e = cudaStreamSynchronize(stream);
-    for (const auto flags : {moe::fp8_linear_flags}) {
+    for (const auto flags : {moe::fp8_linear_flags, moe::latent_decode_flags}) {
         int32_t v = 0;
         if (e == cudaSuccess) e = flags(&v);
         *status_out |= v;

@@ -46,7 +46,7 @@ __device__ __forceinline__ bool mb_try(uint64_t *b, uint32_t parity) {
 // Bounded wait (one second) for the phase with this parity; false on time-out or
 // once another thread of the block has given up.  The block then ends with its
 // results undefined and `err` set.
-__device__ __noinline__ bool mb_wait_slow(uint64_t *b, uint32_t parity, volatile int *abort, int32_t *err) {
+static __device__ __noinline__ bool mb_wait_slow(uint64_t *b, uint32_t parity, volatile int *abort, int32_t *err) {
     const unsigned long long t0 = global_ns();
     for (;;) {
         if (mb_try(b, parity)) return true;
