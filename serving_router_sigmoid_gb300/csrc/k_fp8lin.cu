@@ -164,41 +164,40 @@ __global__ void __launch_bounds__(Cfg<TOKM, BN>::kThreads, TOKM ? 1 : 2)
                 }
             }
             if (*abort) {  // copies in flight land before the block ends
-                const unsigned long long t = global_ns();
+                const long long t = clock64();
                 for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
-                    while (!mb_try(&sm.full[i % C::kStages], (uint32_t)((i / C::kStages) & 1)) && global_ns() - t < kWaitNs) {}
+                    while (!mb_try(&sm.full[i % C::kStages], (uint32_t)((i / C::kStages) & 1)) && clock64() - t < kWaitClk) {}
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------- MMA
         const uint32_t id = idesc(0, 0, 0, 128, BN);
-        const uint64_t da = desc(sbase, 16, 1024), db = desc(sbase + C::kA, 16, 1024);
-        if (elect()) {
-            Ring r, acc;
-            bool ok = true;
-            for (int i = first; i < n_tiles && ok; i += step)
-                for (int k = k0; k < k1; ++k) {
-                    if (!mb_wait(&sm.acc_empty[acc.slot], acc.phase ^ 1, abort, &g_err) ||
-                        !mb_wait(&sm.full[r.slot], r.phase, abort, &g_err)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_after_sync();
-                    const uint64_t off = (uint64_t)((uint32_t)r.slot * (C::kStage >> 4));
-                    const uint32_t d = tmem + (uint32_t)(acc.slot * C::kAcc);
+        const uint32_t da = desc(sbase, 16), db = desc(sbase + C::kA, 16);
+        const bool lead = elect();
+        Ring r, acc;
+        bool ok = true;
+        for (int i = first; i < n_tiles && ok; i += step)
+            for (int k = k0; k < k1; ++k) {
+                ok = __all_sync(0xffffffffu, mb_wait(&sm.acc_empty[acc.slot], acc.phase ^ 1, abort, &g_err) &&
+                                                 mb_wait(&sm.full[r.slot], r.phase, abort, &g_err));
+                if (!ok) break;
+                tc_after_sync();
+                const uint32_t off = (uint32_t)(r.slot * (int)(C::kStage >> 4)), d = tmem + (uint32_t)(acc.slot * C::kAcc);
+                if (lead) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) mma_f8(d, da + off + 2 * j, db + off + 2 * j, id, j != 0);
                     mma_commit(&sm.empty[r.slot]);
                     mma_commit(&sm.acc_full[acc.slot]);
-                    r.next(C::kStages);
-                    acc.next(2);
                 }
-            if (!ok) {  // what was issued ends before the tensor memory is freed
-                mma_commit(&sm.drain);
-                const unsigned long long t = global_ns();
-                while (!mb_try(&sm.drain, 0) && global_ns() - t < kWaitNs) {}
+                __syncwarp();
+                r.next(C::kStages);
+                acc.next(2);
             }
+        if (!ok) {  // what was issued ends before the tensor memory is freed
+            if (lead) mma_commit(&sm.drain);
+            const long long t = clock64();
+            while (!mb_try(&sm.drain, 0) && clock64() - t < kWaitClk) {}
         }
         __syncwarp();
     } else if (warp >= 4) {

@@ -31,6 +31,8 @@
 // - A request that several blocks share leaves its pieces (O, m, l) in the handle's
 //   workspace; a second small launch joins them in order, so results do not depend
 //   on timing.
+#include <type_traits>
+
 #include "tc_dev.cuh"
 
 namespace moe {
@@ -46,6 +48,7 @@ constexpr int kChunks = 9;            // of 64 dimensions: 512 + 64
 constexpr uint32_t kChunk = kTile * 128;
 constexpr uint32_t kStageB = kChunks * kChunk;
 constexpr int kStages = 2;
+constexpr int kParts = 5;             // of a stage: two chunks, what one step of the second product frees
 constexpr int kProd = 8;              // producer warps
 constexpr int kThreads = 32 * (4 + 1 + kProd);
 constexpr uint32_t kOffQ = 0, kOffK = kStageB, kOffP = kOffK + kStages * kStageB;
@@ -63,6 +66,8 @@ struct Params {
     int runs;
     float factor;                     // scale * k_scale * log2(e)
     FastDiv by_page;
+    int box;                          // rows of a TMA box: the largest of 8 .. 64 that divides a page
+    int out32;                        // rows of out start on 32 bytes
     int64_t c_page, c_tok;            // bytes
     uint32_t n_pages;
     float *part;                      // [2 * blocks] pieces
@@ -72,7 +77,7 @@ struct Params {
 __host__ __device__ inline int64_t piece_floats(int latent) { return (int64_t)kHeads * latent + 2 * kHeads; }
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], valid_full[kStages], q_full, q_empty, s_full[2], p_ready, pv_done, o_full, o_empty, drain;
+    uint64_t full[kStages][kParts], empty[kStages][kParts], valid_full[kStages], q_full, q_empty, s_full[2], p_ready, pv_done, o_full, o_empty, drain;
     uint32_t valid[kStages][2];
     uint32_t tmem;
     int abort;
@@ -156,6 +161,8 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t at, uint32_t (&v)[32]) {
                    "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
                  : "r"(at));
 }
+__device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void prod_bar() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
 __device__ __forceinline__ bool soft_or(bool p) {
     uint32_t r;
     asm volatile("{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.or.pred po, 1, 128, pi;\n selp.u32 %0, 1, 0, po;\n}"
@@ -163,8 +170,13 @@ __device__ __forceinline__ bool soft_or(bool p) {
     return r != 0;
 }
 
-template <bool BF, bool E4>
-__global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid_constant__ Params p) {
+// How rows come: by TMA (pages of whole runs of 8 tokens; a request's last, ragged
+// tile row by row), row by row (any page size and stride), or as E4M3 codes.
+constexpr int kByRow = 0, kByTma = 1, kByCode = 2;
+
+template <bool BF, int LOAD>
+__global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ Params p) {
+    constexpr bool E4 = LOAD == kByCode;
     using T = typename Elem<BF ? MOE_BF16 : MOE_F16>::type;
     extern __shared__ uint8_t raw[];
     __shared__ Shared sm;
@@ -176,9 +188,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mb_init(&sm.full[i], E4 ? kProd : 32 * kProd);
-            mb_init(&sm.valid_full[i], kProd);
-            mb_init(&sm.empty[i], 1);
+            for (int j = 0; j < kParts; ++j) {
+                mb_init(&sm.full[i][j], LOAD == kByRow ? 32 * kProd : LOAD == kByCode ? kProd : 1);
+                mb_init(&sm.empty[i][j], 1);
+            }
+            mb_init(&sm.valid_full[i], LOAD == kByTma ? 1 : kProd);
             mb_init(&sm.s_full[i], 1);
         }
         mb_init(&sm.q_full, 32 * kProd);
@@ -244,127 +258,222 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         const int row = 8 * pw + (lane >> 3);                  // and row + 4
         const uint8_t *cache = static_cast<const uint8_t *>(a.cache);
         const int pieces = p.dim / (E4 ? 16 : 8);              // of 16 bytes
-        const uint8_t *src[2];
-        const auto find = [&](int i) -> const uint8_t * {      // row i of the tile at w, or none
-            const int t = w.t * kTile + row + 4 * i;
-            if (t >= w.len) return nullptr;
-            const uint32_t col = p.by_page.div((uint32_t)t);
-            const uint32_t id = (uint32_t)ld_in(a.block_table + w.b * a.table_stride + col);
-            if (id >= p.n_pages) return nullptr;
-            return cache + (int64_t)id * p.c_page + (int64_t)(t - col * a.page_size) * p.c_tok;
+        struct Next {                                          // a tile to bring
+            const uint8_t *row[2];                             // this thread's rows, or none
+            int b, page, off;                                  // by TMA: page and row of the group `lane`
+            bool first, have, whole;
         };
-        constexpr int kLoads = E4 ? 5 : 9;
-        if (more) {
-            src[0] = find(0);
-            src[1] = find(1);
-        }
-        bool first = true;
-        Ring r;
-        uint32_t q_phase = 0;
-        while (more) {
-            if (first) {
-                // the queries of another request, once the products with the last ones are done
-                if (__any_sync(0xffffffffu, !mb_wait(&sm.q_empty, q_phase ^ 1, abort, &g_err))) break;
-                q_phase ^= 1;
-                const T *q = static_cast<const T *>(a.q) + w.b * a.q_stride_b;
-                const int qp = p.dim / 8;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int h = row + 4 * i;
-                    const bool has = h < nh;
-                    const T *qr = q + (has ? (int64_t)(h0 + h) * a.q_stride_h : 0);
-#pragma unroll
-                    for (int j = 0; j < kChunks; ++j)
-                        if (8 * j + sub < qp)
-                            cp16(sbase + kOffQ + (uint32_t)j * kChunk + sw_off(h, sub), qr + 8 * (8 * j + sub), has);
+        const int gshift = LOAD == kByTma ? 31 - __clz(p.box) : 3;  // log2 of the rows of a group
+        bool opens = true;
+        const auto fetch = [&]() {
+            Next x;
+            x.have = more;
+            if (!more) return x;
+            x.whole = LOAD == kByTma && (w.t + 1) * kTile <= w.len;
+            if (x.whole) {
+                const int t = w.t * kTile + (lane << gshift);
+                x.page = -1;
+                if (lane << gshift < kTile) {
+                    const uint32_t col = p.by_page.div((uint32_t)t);
+                    x.page = ld_in(a.block_table + w.b * a.table_stride + col);
+                    x.off = t - (int)(col * a.page_size);
                 }
-                cp_arrive(&sm.q_full);
-            }
-            uint4 code[2][E4 ? kLoads : 1];
-            if constexpr (E4) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < kLoads; ++j) {
-                        code[i][j] = make_uint4(0, 0, 0, 0);
-                        if (src[i] && 8 * j + sub < pieces) code[i][j] = ld_once16(src[i] + 16 * (8 * j + sub));
-                    }
-            }
-            const uint8_t *now[2] = {src[0], src[1]};
-            more = w.next(a, first);
-            if (more) {  // table entries of the next tile, under this one's copies
-                src[0] = find(0);
-                src[1] = find(1);
-            }
-            if (__any_sync(0xffffffffu, !mb_wait(&sm.empty[r.slot], r.phase ^ 1, abort, &g_err))) break;
-            const uint32_t at = sbase + kOffK + (uint32_t)r.slot * kStageB;
-            if constexpr (E4) {
-                uint8_t *tile = dyn + kOffK + (uint32_t)r.slot * kStageB;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < kLoads; ++j) {
-                        const int c = 8 * j + sub;
-                        if (c >= pieces) continue;
-                        uint8_t *d = tile + (uint32_t)(c >> 2) * kChunk;
-                        *reinterpret_cast<uint4 *>(d + sw_off(row + 4 * i, 2 * (c & 3))) = widen8<BF>(code[i][j].x, code[i][j].y);
-                        *reinterpret_cast<uint4 *>(d + sw_off(row + 4 * i, 2 * (c & 3) + 1)) = widen8<BF>(code[i][j].z, code[i][j].w);
-                    }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mb_arrive(&sm.full[r.slot]);
             } else {
 #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = w.t * kTile + row + 4 * i;
+                    const uint32_t col = p.by_page.div((uint32_t)t);
+                    const uint32_t id = t < w.len ? (uint32_t)ld_in(a.block_table + w.b * a.table_stride + col) : ~0u;
+                    x.row[i] = id < p.n_pages ? cache + (int64_t)id * p.c_page + (int64_t)(t - col * a.page_size) * p.c_tok : nullptr;
+                }
+            }
+            x.b = w.b;
+            x.first = opens;
+            more = w.next(a, opens);
+            return x;
+        };
+        const int parts = (p.dim + 127) / 128, pieces16 = p.dim / 16;
+        Next now = fetch(), nxt = fetch();
+        Ring r;
+        uint32_t q_phase = 0;
+        uint4 code[2][E4 ? kParts : 1];
+        const auto load = [&](const Next &x, int j) {          // codes of a part, 8 pieces of 16 bytes a row
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                code[i][j] = make_uint4(0, 0, 0, 0);
+                if (x.have && x.row[i] && 8 * j + sub < pieces) code[i][j] = ld_once16(x.row[i] + 16 * (8 * j + sub));
+            }
+        };
+        if constexpr (E4)
+#pragma unroll
+            for (int j = 0; j < kParts; ++j) load(now, j);
+        const auto queries = [&](int b) {                      // of another request
+            const T *q = static_cast<const T *>(a.q) + b * a.q_stride_b;
+            const int qp = p.dim / 8;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int h = row + 4 * i;
+                const bool has = h < nh;
+                const T *qr = q + (has ? (int64_t)(h0 + h) * a.q_stride_h : 0);
+#pragma unroll
+                for (int j = 0; j < kChunks; ++j)
+                    if (8 * j + sub < qp)
+                        cp16(sbase + kOffQ + (uint32_t)j * kChunk + sw_off(h, sub), qr + 8 * (8 * j + sub), has);
+            }
+            cp_arrive(&sm.q_full);
+        };
+        const auto copy_part = [&](uint32_t at, int j) {       // this thread's pieces of two chunks
+#pragma unroll
+            for (int c = 2 * j; c < 2 * j + 2; ++c)
+#pragma unroll
                 for (int i = 0; i < 2; ++i)
+                    if (8 * c + sub < pieces)
+                        cp16(sbase + at + (uint32_t)c * kChunk + sw_off(row + 4 * i, sub),
+                             now.row[i] ? now.row[i] + 16 * (8 * c + sub) : cache, now.row[i] != nullptr);
+        };
+        const auto seen = [&]() {                              // which of the warp's 8 tokens are
+            const uint32_t b0 = __ballot_sync(0xffffffffu, sub == 0 && now.row[0]), b1 = __ballot_sync(0xffffffffu, sub == 0 && now.row[1]);
+            uint32_t m = 0;
 #pragma unroll
-                    for (int j = 0; j < kLoads; ++j)
+            for (int k = 0; k < 4; ++k) m |= (b0 >> (8 * k) & 1) << k | (b1 >> (8 * k) & 1) << (4 + k);
+            if (lane == 0) reinterpret_cast<volatile uint8_t *>(sm.valid[r.slot])[pw] = (uint8_t)m;
+        };
+        const auto part_of = [&](int k) { return parts < kParts ? k : (k + kParts - 1) % kParts; };  // what only S reads is free first
+        bool ok = true;
+        if constexpr (LOAD == kByTma) {
+            // one warp waits and issues; the others join it where rows are copied.  Nobody leaves early: all
+            // warps meet at every barrier, whatever was given up
+            int issued[kStages] = {-1, -1};
+            for (; now.have; now = nxt, nxt = fetch()) {
+                if (now.first) {
+                    if (pw == 0) ok = mb_wait(&sm.q_empty, q_phase ^ 1, abort, &g_err) && ok;
+                    q_phase ^= 1;
+                    prod_bar();
+                    queries(now.b);
+                }
+                const uint32_t at = kOffK + (uint32_t)r.slot * kStageB;
+                if (now.whole) {
+                    if (pw == 0) {
+                        const int groups = kTile >> gshift;
+                        uint32_t lives = 0;
+                        for (int g = 0; g < groups; ++g)
+                            if ((uint32_t)__shfl_sync(0xffffffffu, now.page, g) < p.n_pages) lives |= 1u << g;
+                        for (int k = 0; k < parts; ++k) {
+                            const int j = part_of(k), chunks = 8 * j + 4 < pieces16 ? 2 : 1;
+                            ok = __all_sync(0xffffffffu, mb_wait(&sm.empty[r.slot][j], r.phase ^ 1, abort, &g_err) && ok);
+                            if (!ok) continue;
+                            // lane: a group of rows of a chunk; a page that is none reads as zeros
+                            const int g = lane & (groups - 1), c = 2 * j + lane / groups;
+                            const int id = __shfl_sync(0xffffffffu, now.page, g), off = __shfl_sync(0xffffffffu, now.off, g);
+                            if (lane == 0) mb_expect_tx(&sm.full[r.slot][j], (uint32_t)chunks * kChunk);
+                            __syncwarp();
+                            if (lane < chunks * groups)
+                                tma_3d(sbase + at + (uint32_t)c * kChunk + (uint32_t)(g << gshift) * 128u, &cmap, 64 * c,
+                                       lives >> g & 1 ? off : 0, lives >> g & 1 ? id : (int)p.n_pages, &sm.full[r.slot][j]);
+                            __syncwarp();
+                        }
+                        if (ok) issued[r.slot] = (int)r.phase;
+                        if (lane < 8) reinterpret_cast<volatile uint8_t *>(sm.valid[r.slot])[lane] = lives >> (8 * lane >> gshift) & 1 ? 0xff : 0;
+                        __syncwarp();
+                        if (lane == 0) mb_arrive(&sm.valid_full[r.slot]);
+                    }
+                } else {
+                    // the last tile of a request, row by row
+                    if (pw == 0)
+                        for (int j = 0; j < parts; ++j) ok = mb_wait(&sm.empty[r.slot][j], r.phase ^ 1, abort, &g_err) && ok;
+                    prod_bar();
+#pragma unroll
+                    for (int j = 0; j < kParts; ++j) copy_part(at, j);
+                    seen();
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_async_smem();
+                    prod_bar();
+                    if (pw == 0 && lane < parts) mb_arrive(&sm.full[r.slot][lane]);
+                    if (pw == 0 && lane == 0) mb_arrive(&sm.valid_full[r.slot]);
+                }
+                r.next(kStages);
+            }
+            if (pw == 0 && *abort) {  // copies in flight land before the block ends
+                const long long t = clock64();
+                for (int i = 0; i < kStages; ++i)
+                    for (int j = 0; j < parts && issued[i] >= 0; ++j)
+                        while (!mb_test(&sm.full[i][j], (uint32_t)issued[i]) && clock64() - t < kWaitClk) {}
+            }
+        } else {
+            for (; now.have && ok; now = nxt, nxt = fetch()) {
+                if (now.first) {  // once the products with the last queries are done
+                    ok = __all_sync(0xffffffffu, mb_wait(&sm.q_empty, q_phase ^ 1, abort, &g_err));
+                    q_phase ^= 1;
+                    if (ok) queries(now.b);
+                }
+                const uint32_t at = kOffK + (uint32_t)r.slot * kStageB;
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) {
+                    const int j = (k + kParts - 1) % kParts;
+                    if (j >= parts) continue;
+                    ok = __all_sync(0xffffffffu, ok && mb_wait(&sm.empty[r.slot][j], r.phase ^ 1, abort, &g_err));
+                    if constexpr (E4) {
+                        uint8_t *tile = dyn + at + (uint32_t)(2 * j + (sub >> 2)) * kChunk;
                         if (8 * j + sub < pieces)
-                            cp16(at + (uint32_t)j * kChunk + sw_off(row + 4 * i, sub), now[i] ? now[i] + 16 * (8 * j + sub) : cache,
-                                 now[i] != nullptr);
-                cp_arrive(&sm.full[r.slot]);
-            }
-            // which of the warp's 8 tokens are seen
-            const uint32_t b0 = __ballot_sync(0xffffffffu, sub == 0 && now[0]), b1 = __ballot_sync(0xffffffffu, sub == 0 && now[1]);
-            if (lane == 0) {
-                uint32_t m = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) m |= (b0 >> (8 * k) & 1) << k | (b1 >> (8 * k) & 1) << (4 + k);
-                reinterpret_cast<volatile uint8_t *>(sm.valid[r.slot])[pw] = (uint8_t)m;
-                mb_arrive(&sm.valid_full[r.slot]);
+                            for (int i = 0; i < 2; ++i) {
+                                // lanes of both chunks store to different banks
+                                const uint4 lo8 = widen8<BF>(code[i][j].x, code[i][j].y), hi8 = widen8<BF>(code[i][j].z, code[i][j].w);
+                                const int c = 2 * (sub & 3), f = sub >> 2;
+                                *reinterpret_cast<uint4 *>(tile + sw_off(row + 4 * i, c + f)) = f ? hi8 : lo8;
+                                *reinterpret_cast<uint4 *>(tile + sw_off(row + 4 * i, c + (f ^ 1))) = f ? lo8 : hi8;
+                            }
+                    } else {
+                        copy_part(at, j);
+                        cp_arrive(&sm.full[r.slot][j]);
+                    }
+                }
+                if constexpr (E4) {
+                    // one fence a tile: it waits for the loads in flight too, so the next codes are asked for behind it
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane < parts) mb_arrive(&sm.full[r.slot][lane]);
+#pragma unroll
+                    for (int j = 0; j < kParts; ++j) load(nxt, j);
+                }
+                seen();  // read by the softmax before the second product, which frees the stage
+                if (lane == 0) mb_arrive(&sm.valid_full[r.slot]);
+                r.next(kStages);
             }
-            r.next(kStages);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 4) {
         // -------------------------------------------------------------- MMA
         const uint32_t fmt = BF ? 1 : 0;
         const uint32_t id_s = idesc(fmt, 0, 0, 64, kTile), id_o = idesc(fmt, 1, 0, 128, p.n);
-        const uint64_t dq = desc(sbase + kOffQ, 16, 1024), dk = desc(sbase + kOffK, 16, 1024);
-        const uint64_t dv = desc(sbase + kOffK, kChunk, 1024), dp = desc(sbase + kOffP, 16, 1024);
-        const int full_chunks = p.dim / 64, rest = p.dim % 64 / 16, mts = (p.latent + 127) / 128;
+        const uint32_t dq = desc(sbase + kOffQ, 16), dk = desc(sbase + kOffK, 16);
+        const uint32_t dv = desc(sbase + kOffK, kChunk), dp = desc(sbase + kOffP, 16);
+        const int steps = p.dim / 16, parts = (steps + 7) / 8, mts = (p.latent + 127) / 128;
         const bool lead = elect();
-        Ring r;                           // stage of the tile whose S comes next
-        Ring ro;                          // stage of the tile whose O comes next
+        Ring r, ro;                       // stages of the tiles whose S, whose O comes next
         uint32_t qf = 0, pr = 0, oe = 0, i = 0;
         bool first = true, ok = more;
-        bool pend = false, pend_first = false;
-        const auto second = [&]() -> bool {  // O += V^T P^T of the pending tile
-            if (!mb_wait(&sm.p_ready, pr, abort, &g_err)) return false;
+        bool pend = false, pend_first = false, pend_last = false;
+        const auto ready = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_test(bar, phase)); };
+        const auto wait = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_wait(bar, phase, abort, &g_err)); };
+        const auto second = [&]() -> bool {  // O += V^T P^T of the pending tile, whose weights are there
             pr ^= 1;
             if (pend_first) {
-                if (!mb_wait(&sm.o_empty, oe ^ 1, abort, &g_err)) return false;
+                if (!wait(&sm.o_empty, oe ^ 1)) return false;
                 oe ^= 1;
             }
             tc_after_sync();
             if (lead) {
-                const uint64_t v = dv + (uint64_t)(ro.slot * (kStageB >> 4));
-                for (int m = 0; m < mts; ++m)
+                const uint32_t v = dv + (uint32_t)(ro.slot * (int)(kStageB >> 4));
+                for (int m = 0; m < mts; ++m) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_f16(tmem + 64 * m, v + (uint64_t)(m * (2 * kChunk >> 4) + k * (2048 >> 4)), dp + 2 * k, id_o,
+                        mma_f16(tmem + 64 * m, v + (uint32_t)(m * (int)(2 * kChunk >> 4) + k * (2048 >> 4)), dp + 2 * k, id_o,
                                 !(pend_first && k == 0));
-                mma_commit(&sm.empty[ro.slot]);
+                    mma_commit(&sm.empty[ro.slot][m]);
+                }
                 mma_commit(&sm.pv_done);
+                if (pend_last) mma_commit(&sm.o_full);
             }
             __syncwarp();
             ro.next(kStages);
@@ -372,50 +481,65 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             return true;
         };
         while (ok && more) {
-            if (first) {
-                if (pend) {
-                    if (!(ok = second())) break;
-                    if (lead) mma_commit(&sm.o_full);
-                    __syncwarp();
-                }
-                if (!(ok = mb_wait(&sm.q_full, qf, abort, &g_err))) break;
+            if (first) {  // the last request ends before the queries of the next are there
+                if (pend) ok = wait(&sm.p_ready, pr) && second();
+                if (!(ok = ok && wait(&sm.q_full, qf))) break;
                 qf ^= 1;
+                fence_async_smem();  // copied by the generic proxy
             }
-            if (!(ok = mb_wait(&sm.full[r.slot], r.phase, abort, &g_err))) break;
-            fence_async_smem();  // the copies landed by the generic proxy
-            tc_after_sync();
             const bool last = w.t + 1 == w.te;
+            const uint32_t k = dk + (uint32_t)(r.slot * (int)(kStageB >> 4));
+            const uint32_t d = tmem + kColS + (i & 1) * kTile;
+            // until the tile is there: the second product of the one before, if its weights are
+            const auto whole = [&]() {
+                bool all = true;
+#pragma unroll
+                for (int x = 0; x < kParts; ++x)
+                    if (x < parts) all = mb_test(&sm.full[r.slot][x], r.phase) && all;
+                return __all_sync(0xffffffffu, all);
+            };
+            long long t0 = 0;
+            while (ok && !whole()) {
+                if (pend && ready(&sm.p_ready, pr)) ok = second();
+                else if (*abort) ok = false;
+                else if (!t0) t0 = clock64();
+                else if (clock64() - t0 > kWaitClk) {
+                    *abort = 1;
+                    atomicOr(&g_err, kErrSyncTimeout);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (!ok) break;
+            if (LOAD == kByRow) fence_async_smem();  // the copies landed by the generic proxy
+            tc_after_sync();
             if (lead) {
-                const uint64_t k = dk + (uint64_t)(r.slot * (kStageB >> 4));
-                const uint32_t d = tmem + kColS + (i & 1) * kTile;
-                for (int c = 0; c < full_chunks; ++c)
+                for (int c = 0; c < steps / 4; ++c)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mma_f16(d, dq + (uint64_t)(c * (kChunk >> 4) + 2 * j), k + (uint64_t)(c * (kChunk >> 4) + 2 * j), id_s,
+                        mma_f16(d, dq + (uint32_t)(c * (int)(kChunk >> 4) + 2 * j), k + (uint32_t)(c * (int)(kChunk >> 4) + 2 * j), id_s,
                                 c + j != 0);
-                for (int j = 0; j < rest; ++j)
-                    mma_f16(d, dq + (uint64_t)(full_chunks * (kChunk >> 4) + 2 * j),
-                            k + (uint64_t)(full_chunks * (kChunk >> 4) + 2 * j), id_s, 1);
+                for (int j = 0; j < steps % 4; ++j)
+                    mma_f16(d, dq + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * j),
+                            k + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * j), id_s, 1);
                 mma_commit(&sm.s_full[i & 1]);
                 if (last) mma_commit(&sm.q_empty);
+                for (int e = mts; e < parts; ++e) mma_commit(&sm.empty[r.slot][e]);
             }
             __syncwarp();
+            if (!ok) break;
             r.next(kStages);
             ++i;
-            if (pend && !(ok = second())) break;
+            if (pend) ok = wait(&sm.p_ready, pr) && second();
             pend = true;
             pend_first = first;
+            pend_last = last;
             more = w.next(a, first);
         }
-        if (ok && pend) {
-            ok = second();
-            if (ok && lead) mma_commit(&sm.o_full);
-            __syncwarp();
-        }
-        if (*abort && lead) {  // what was issued ends before the tensor memory is freed
-            mma_commit(&sm.drain);
-            const unsigned long long t = global_ns();
-            while (!mb_try(&sm.drain, 0) && global_ns() - t < kWaitNs) {}
+        if (ok && pend) ok = wait(&sm.p_ready, pr) && second();
+        if (*abort) {  // what was issued ends before the tensor memory is freed
+            if (lead) mma_commit(&sm.drain);
+            const long long t = clock64();
+            while (!mb_try(&sm.drain, 0) && clock64() - t < kWaitClk) {}
         }
         __syncwarp();
     } else {
@@ -439,16 +563,16 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 
         Ring r;
         uint32_t i = 0, pv = 0, of = 0;
-        bool first = true, ok = true;
+        bool first = true;
         float m[2], l[2];
-        while (more && ok) {
+        // (a wait that was given up changes nothing here: every thread takes every barrier)
+        while (more) {
             if (first) {
                 m[0] = m[1] = kFloor;
                 l[0] = l[1] = 0.f;
             }
-            ok = mb_wait(&sm.valid_full[r.slot], r.phase, abort, &g_err) &&
-                 mb_wait(&sm.s_full[i & 1], (i >> 1) & 1, abort, &g_err);
-            if (soft_or(!ok)) { ok = false; break; }
+            mb_wait(&sm.valid_full[r.slot], r.phase, abort, &g_err);
+            mb_wait(&sm.s_full[i & 1], (i >> 1) & 1, abort, &g_err);
             tc_after_sync();
             uint32_t v[32];
             tmem_ld_rows(tmem + quad + kColS + (i & 1) * kTile, v);
@@ -482,9 +606,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                     l[k] *= f;
                     if ((lane & 3) == 0) sm.factor[hr + 8 * k] = f;
                 }
-                ok = mb_wait(&sm.pv_done, pv, abort, &g_err);
+                mb_wait(&sm.pv_done, pv, abort, &g_err);
                 waited = true;
-                if (soft_or(!ok)) { ok = false; break; }
+                soft_bar();
                 tc_after_sync();
                 for (int c = 0; c < (p.latent + 127) / 128 * 64; c += 16) {
                     if ((c & 63) >= p.n) continue;
@@ -505,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                 l[k] += x + y;
                 w2[j] = pack_pair(x, y, T());
             }
-            if (!waited) ok = mb_wait(&sm.pv_done, pv, abort, &g_err);  // the weights' place is free
+            if (!waited) mb_wait(&sm.pv_done, pv, abort, &g_err);  // the weights' place is free
             if (i) pv ^= 1;
             uint8_t *pt = dyn + kOffP;
 #pragma unroll
@@ -526,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
                 }
-                ok = mb_wait(&sm.o_full, of, abort, &g_err) && ok;
+                mb_wait(&sm.o_full, of, abort, &g_err);
                 of ^= 1;
                 if (from0 && ends) {
                     if ((lane & 3) == 0)
@@ -537,19 +661,37 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                                 a.lse[(int64_t)b * p.heads + h0 + hr + 8 * k] =
                                     l[k] > 0.f ? (m[k] - kOff) / kLog2e + logf(l[k]) : -INFINITY;
                         }
-                    if (soft_or(!ok)) { ok = false; break; }
+                    soft_bar();
                     tc_after_sync();
                     for (int c = 0; c < (p.latent + 127) / 128 * 64; c += 16) {
                         if ((c & 63) >= p.n) continue;
                         uint32_t o[16];
                         tmem_ld(tmem + quad + c, o);
                         tmem_wait_ld();
-                        const int d = (c >> 6) * 128 + 32 * warp + lane;
-                        if (d >= p.latent) continue;
-                        T *to = out + b * a.out_stride_b + (h0 + (c & 63)) * a.out_stride_h + d;
+                        // 16 heads by 32 dimensions, turned in the weights' place: a lane takes half a head's row
+                        float *turn = reinterpret_cast<float *>(dyn + kOffP) + 512 * warp;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if ((c & 63) + j < nh) from_f32(__uint_as_float(o[j]) * sm.factor[(c & 63) + j], to[j * a.out_stride_h]);
+                            turn[32 * j + (lane ^ 4 * (j & 7))] = __uint_as_float(o[j]) * sm.factor[(c & 63) + j];
+                        __syncwarp();
+                        const int h = (c & 63) + (lane >> 1), d = (c >> 6) * 128 + 32 * warp + 16 * (lane & 1);
+                        float x[16];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<float4 *>(x + 4 * k) = *reinterpret_cast<const float4 *>(
+                                turn + 32 * (lane >> 1) + ((16 * (lane & 1) + 4 * k) ^ 4 * (lane >> 1 & 7)));
+                        __syncwarp();
+                        if (h >= nh || d >= p.latent) continue;
+                        T *to = out + b * a.out_stride_b + (h0 + h) * a.out_stride_h + d;
+                        if (p.out32) {
+                            uint32_t y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) y[k] = pack_pair(x[2 * k], x[2 * k + 1], T());
+                            st32(to, y);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) from_f32(x[k], to[k]);
+                        }
                     }
                 } else {
                     float *piece = p.part + (2 * (int64_t)blockIdx.x + (from0 ? 1 : 0)) * piece_floats(p.latent);
@@ -564,7 +706,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                         const int64_t end = s + kSegCost + tiles;
                         p.rec[blockIdx.x] = make_int4(b, run, (int)((end * p.runs - 1) / total), total);
                     }
-                    if (soft_or(!ok)) { ok = false; break; }
                     tc_after_sync();
                     for (int c = 0; c < (p.latent + 127) / 128 * 64; c += 16) {
                         if ((c & 63) >= p.n) continue;
@@ -573,8 +714,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                         tmem_wait_ld();
                         const int d = (c >> 6) * 128 + 32 * warp + lane;
                         if (d >= p.latent) continue;
+                        uint32_t *to = reinterpret_cast<uint32_t *>(piece) + d * kHeads + (c & 63);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) piece[(int64_t)((c & 63) + j) * p.latent + d] = __uint_as_float(o[j]);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t y[8] = {o[8 * k], o[8 * k + 1], o[8 * k + 2], o[8 * k + 3], o[8 * k + 4], o[8 * k + 5], o[8 * k + 6], o[8 * k + 7]};
+                            st32(to + 8 * k, y);
+                        }
                     }
                 }
                 tc_before_sync();
@@ -591,90 +736,148 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     if (warp == 4) tmem_free(tmem, 512);
 }
 
-// Joins the pieces of the requests that several runs share: a block a (record,
-// head), four groups of 128 threads over the runs, then over the groups.
+// Joins the pieces of the requests that several runs share.  A block takes 32
+// latent dimensions of the k-th such request of a head group, a lane one of them
+// for 8 heads (32 contiguous bytes a piece); its 8 warps take 8 heads each, or
+// (many: few requests over many runs) a part of the runs for the same 8 heads.
+constexpr int kMaxRuns = 152;
 template <typename T>
-__global__ void __launch_bounds__(512) latent_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ Params p, int many) {
     after_previous();
-    __shared__ float wt[512];
-    __shared__ float4 sums[4][128];
-    __shared__ float red[2];
+    __shared__ __align__(16) float wt[8][kMaxRuns][8];
+    __shared__ float sums[8][8][32];
+    __shared__ int4 rec;
     const MoeLatentArgs &a = p.a;
-    const int block = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-    const int4 rec = p.rec[block];
+    const int group = blockIdx.x % p.groups, k = blockIdx.x / p.groups, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) rec.x = -1;
+    __syncthreads();
+    if (warp == 0) {  // the k-th request that begins in a run and ends in another
+        int seen = 0;
+        for (int r = 0; r < p.runs; r += 32) {
+            const int4 x = r + lane < p.runs ? p.rec[(r + lane) * p.groups + group] : make_int4(-1, 0, 0, 0);
+            const uint32_t has = __ballot_sync(0xffffffffu, x.x >= 0);
+            if (x.x >= 0 && seen + __popc(has & ((1u << lane) - 1)) == k) rec = x;
+            seen += __popc(has);
+        }
+    }
+    __syncthreads();
     if (rec.x < 0) return;
-    const int group = block % p.groups, h0 = group * p.per_group;
-    if (h >= min(p.per_group, p.heads - h0)) return;
-    const int n = rec.z - rec.y + 1;
+    const int h0 = group * p.per_group, nh = min(p.per_group, p.heads - h0);
+    const int oct = many ? (int)blockIdx.z : warp, n = rec.z - rec.y + 1;
     const int64_t floats = piece_floats(p.latent);
-    const auto piece = [&](int i) { return p.part + (2 * ((int64_t)(rec.y + i) * p.groups + group) + (i == 0)) * floats; };
-    const auto holds = [&](int i) {  // a run may be empty
-        const int r = rec.y + i;
-        return (int)((int64_t)rec.w * r / p.runs) < (int)((int64_t)rec.w * (r + 1) / p.runs);
-    };
-    const int64_t at = (int64_t)kHeads * p.latent + h;
-    if (tid < 32) {
-        float m = kFloor, l = 0.f;
-        for (int i = tid; i < n; i += 32)
-            if (holds(i)) m = fmaxf(m, piece(i)[at]);
+    const float *pieces = p.part + (2 * ((int64_t)rec.y * p.groups + group)) * floats;  // of run i: 2 i groups further; the first is a second piece
+    const auto piece = [&](int i) { return pieces + (2 * (int64_t)i * p.groups + (i == 0)) * floats; };
+    float top = kFloor, l = 0.f;
+    float (*const w)[8] = wt[many ? 0 : warp];
+    // maxima and sums of the pieces, (run, head) pairs over the 8 heads' threads: all of them (many) or a warp
+    const int team = many ? 256 : 32, me = many ? tid : lane, pairs = 8 * oct < nh ? 8 * n : 0;
+    const int64_t at = (int64_t)kHeads * p.latent + 8 * oct + (lane & 7);
+    for (int i0 = me; i0 < pairs; i0 += 5 * team) {
+        float m[5];
 #pragma unroll
-        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        for (int i = tid; i < n; i += 32) {
-            const float f = holds(i) ? ex2(piece(i)[at] - m) : 0.f;
-            wt[i] = f;
-            l += f > 0.f ? f * piece(i)[at + kHeads] : 0.f;
+        for (int k = 0; k < 5; ++k) {
+            const int i = (i0 + k * team) >> 3;
+            // a run may be empty: no weight
+            const bool holds = i < n && (int)((int64_t)rec.w * (rec.y + i) / p.runs) < (int)((int64_t)rec.w * (rec.y + i + 1) / p.runs);
+            m[k] = holds ? piece(i)[at] : -INFINITY;
         }
 #pragma unroll
-        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (tid == 0) {
-            red[0] = l;
-            red[1] = m;
+        for (int k = 0; k < 5; ++k) {
+            if (i0 + k * team < pairs) w[(i0 + k * team) >> 3][lane & 7] = m[k];
+            top = fmaxf(top, m[k]);
         }
     }
-    __syncthreads();
-    const int part = tid >> 7, d = (tid & 127) * 4;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (d < p.latent) {
-#pragma unroll 4
-        for (int i = part; i < n; i += 4) {
-            const float f = wt[i];
-            if (f == 0.f) continue;
-            const float4 v = *reinterpret_cast<const float4 *>(piece(i) + (int64_t)h * p.latent + d);
-            s.x += f * v.x; s.y += f * v.y; s.z += f * v.z; s.w += f * v.w;
-        }
-    }
-    sums[part][tid & 127] = s;
-    __syncthreads();
-    if (part || d >= p.latent) return;
-    const float l = red[0], f = l > 0.f ? a.k_scale / l : 0.f;
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    if (many) {
+        if (lane < 8) sums[0][warp][lane] = top;
+        __syncthreads();
 #pragma unroll
-    for (int k = 1; k < 4; ++k) {
-        const float4 v = sums[k][tid & 127];
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        for (int q = 0; q < 8; ++q) top = fmaxf(top, sums[0][q][lane & 7]);
     }
-    T *out = static_cast<T *>(a.out) + rec.x * a.out_stride_b + (h0 + h) * a.out_stride_h + d;
-    from_f32(s.x * f, out[0]);
-    from_f32(s.y * f, out[1]);
-    from_f32(s.z * f, out[2]);
-    from_f32(s.w * f, out[3]);
-    constexpr float kOff = sizeof(T) == 2 && std::is_same<T, __half>::value ? 7.f : 0.f;
-    if (tid == 0 && a.lse)
-        a.lse[(int64_t)rec.x * p.heads + h0 + h] = l > 0.f ? (red[1] - kOff) / kLog2e + logf(l) : -INFINITY;
+    for (int i0 = me; i0 < pairs; i0 += 5 * team) {
+        float v[5];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+            const int i = (i0 + k * team) >> 3;
+            v[k] = i < n ? piece(i)[at + kHeads] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+            const int i = (i0 + k * team) >> 3;
+            if (i >= n) continue;
+            const float m = w[i][lane & 7], f = m == -INFINITY ? -1.f : ex2(m - top);
+            w[i][lane & 7] = f;
+            if (f > 0.f) l += f * v[k];
+        }
+    }
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    if (many) {
+        if (lane < 8) sums[1][warp][lane] = l;
+        __syncthreads();
+        l = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) l += sums[1][q][lane & 7];
+        __syncthreads();
+    } else {
+        __syncwarp();
+    }
+    const int d = 32 * blockIdx.y + lane;
+    float s[8] = {};
+    if (8 * oct < nh)
+#pragma unroll 5
+        for (int i = many ? warp : 0; i < n; i += many ? 8 : 1) {
+            const float4 f0 = *reinterpret_cast<const float4 *>(w[i]), f1 = *reinterpret_cast<const float4 *>(w[i] + 4);
+            if (f0.x < 0.f) continue;
+            const float4 *v = reinterpret_cast<const float4 *>(piece(i) + d * kHeads + 8 * oct);
+            const float4 v0 = v[0], v1 = v[1];
+            s[0] += f0.x * v0.x; s[1] += f0.y * v0.y; s[2] += f0.z * v0.z; s[3] += f0.w * v0.w;
+            s[4] += f1.x * v1.x; s[5] += f1.y * v1.y; s[6] += f1.z * v1.z; s[7] += f1.w * v1.w;
+        }
+    if (many) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[warp][j][lane] = s[j];
+        __syncthreads();
+        if (warp) return;
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] += sums[q][j][lane];
+    }
+    constexpr float kOff = std::is_same<T, __half>::value ? 7.f : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float lj = __shfl_sync(0xffffffffu, l, j), mj = __shfl_sync(0xffffffffu, top, j);
+        const int h = 8 * oct + j;
+        if (h >= nh) continue;
+        from_f32(lj > 0.f ? s[j] * (a.k_scale / lj) : 0.f,
+                 static_cast<T *>(a.out)[rec.x * a.out_stride_b + (h0 + h) * a.out_stride_h + d]);
+        if (a.lse && blockIdx.y == 0 && lane == 0)
+            a.lse[(int64_t)rec.x * p.heads + h0 + h] = lj > 0.f ? (mj - kOff) / kLog2e + logf(lj) : -INFINITY;
+    }
 }
 
 int groups_of(int heads) { return (heads + kHeads - 1) / kHeads; }
-int runs_of(int heads, int sms) { return sms / groups_of(heads) > 0 ? sms / groups_of(heads) : 1; }
+int runs_of(int heads, int sms) {
+    const int n = sms / groups_of(heads);
+    return n < 1 ? 1 : n > kMaxRuns ? kMaxRuns : n;
+}
 
-template <bool BF, bool E4>
-const void *kernel() { return reinterpret_cast<const void *>(latent_decode_kernel<BF, E4>); }
+template <int LOAD>
+const void *kernel(bool bf) {
+    return bf ? reinterpret_cast<const void *>(latent_decode_kernel<true, LOAD>)
+              : reinterpret_cast<const void *>(latent_decode_kernel<false, LOAD>);
+}
 
 }  // namespace
 
 cudaError_t latent_prepare(const MoeLatentDesc &d, int num_sms, size_t *bytes) {
-    for (const void *fn : {kernel<false, false>(), kernel<false, true>(), kernel<true, false>(), kernel<true, true>()}) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-        if (e != cudaSuccess) return e;
-    }
+    for (const bool bf : {false, true})
+        for (const void *fn : {kernel<kByRow>(bf), kernel<kByTma>(bf), kernel<kByCode>(bf)}) {
+            const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+            if (e != cudaSuccess) return e;
+        }
     const int64_t blocks = (int64_t)groups_of(d.n_heads) * runs_of(d.n_heads, num_sms);
     *bytes = (size_t)blocks * (2 * (size_t)piece_floats(d.latent_dim) * 4 + sizeof(int4));
     return cudaSuccess;
@@ -696,25 +899,41 @@ cudaError_t launch_latent_decode(const LatentHandle &h, const MoeLatentArgs &a, 
     p.c_page = a.c_stride_page * ce;
     p.c_tok = a.c_stride_tok * ce;
     p.n_pages = (uint32_t)a.n_pages;
+    p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride_b % 16 == 0 && a.out_stride_h % 16 == 0;
     p.part = h.part;
     const int blocks = p.groups * p.runs;
     p.rec = reinterpret_cast<int4 *>(h.part + 2 * blocks * piece_floats(p.latent));
-    const bool bf = a.act_type == MOE_BF16, e4 = a.cache_type == MOE_E4M3;
-    const void *fn = bf ? (e4 ? kernel<true, true>() : kernel<true, false>()) : (e4 ? kernel<false, true>() : kernel<false, false>());
-    void *args[] = {&p};
+    const bool bf = a.act_type == MOE_BF16;
+    for (p.box = kTile; p.box > 1 && a.page_size % p.box;) p.box /= 2;
+    CUtensorMap cmap = {};
+    const void *fn;
+    if (a.cache_type == MOE_E4M3) {
+        fn = kernel<kByCode>(bf);
+    } else {
+        // boxes of 8 rows and more keep the swizzle's atoms; rows and pages that overlap have no map
+        const int64_t dims[3] = {p.dim, a.page_size, a.n_pages}, str[2] = {p.c_tok, a.n_pages > 1 ? p.c_page : p.c_tok * a.page_size};
+        const bool tma = p.box >= 8 && a.n_pages > 0 && p.c_tok >= 2 * p.dim && str[1] >= 2 * p.dim &&
+                         encode_map(&cmap, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.cache, 3, dims,
+                                    str, p.box) == cudaSuccess;
+        fn = tma ? kernel<kByTma>(bf) : kernel<kByRow>(bf);
+    }
+    void *args[] = {&cmap, &p};
     cudaError_t e = launch_after(fn, blocks, kThreads, kSmem, s, args);
     if (e != cudaSuccess) return e;
+    const int split = a.n_requests < p.runs ? a.n_requests : p.runs;  // requests over several runs, at most
+    int many = 8 * split <= p.runs;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)blocks, (unsigned)p.per_group);
-    c.blockDim = dim3(512);
+    c.gridDim = dim3((unsigned)(split * p.groups), (unsigned)(p.latent / 32), many ? (unsigned)(p.per_group + 7) / 8 : 1u);
+    c.blockDim = dim3(256);
     c.stream = s;
     c.attrs = at;
     c.numAttrs = 1;
-    return cudaLaunchKernelExC(&c, reinterpret_cast<const void *>(bf ? latent_join_kernel<__nv_bfloat16> : latent_join_kernel<__half>),
-                               args);
+    void *jargs[] = {&p, &many};
+    return cudaLaunchKernelExC(&c, bf ? reinterpret_cast<const void *>(latent_join_kernel<__nv_bfloat16>)
+                                      : reinterpret_cast<const void *>(latent_join_kernel<__half>), jargs);
 }
 
 cudaError_t latent_decode_flags(int32_t *out) {

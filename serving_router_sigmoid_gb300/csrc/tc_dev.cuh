@@ -2,12 +2,12 @@
 // latent attention: thin wrappers of the PTX, bounded waits, descriptors.
 //
 // A tcgen05.mma costs the tensor core N/2 cycles (M = 128, 32 bytes of K a row),
-// at least what its operands take from shared memory at 128 bytes a cycle, if
-// its issuer keeps up.  Measured: M = 128: N = 256 128 cycles, 128 64, 64 48, 16
-// 39; M = 64: N = 64 32; A in tensor memory, N = 64: 32.  An issuer that forms
-// 64-bit descriptors for each instruction, or that the compiler does not see as
-// one thread of a converged warp (elect), takes 70 to 90 whatever the shape: the
-// loops here add constants to descriptors formed once.
+// at least what its operands take from shared memory at 128 bytes a cycle, if its
+// issuer keeps up.  Measured: M = 128: N = 256 128 cycles, 128 64, 64 48, 16 39; M
+// = 64: N = 64 32; A in tensor memory, N = 64: 32.  An issuer takes 60 to 90 cycles
+// an instruction inside a branch that one lane takes, 26 without a branch: the
+// whole warp runs along and a predicate picks the lane, the upper half of the
+// descriptors is a constant.  A test of a barrier and a fence take some 160.
 #pragma once
 
 #include <cuda.h>
@@ -43,15 +43,32 @@ __device__ __forceinline__ bool mb_try(uint64_t *b, uint32_t parity) {
                  : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
     return ok != 0;
 }
-// Bounded wait (one second) for the phase with this parity; false on time-out or
-// once another thread of the block has given up.  The block then ends with its
-// results undefined and `err` set.
+__device__ __forceinline__ bool mb_test(uint64_t *b, uint32_t parity) {  // without waiting
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// The same with a hint to sleep in the barrier unit (up to 0.1 ms): a dozen warps
+// that spin slow down the one that issues MMAs.
+__device__ __forceinline__ bool mb_try_sleep(uint64_t *b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(su32(b)), "r"(parity), "r"(100000u) : "memory");
+    return ok != 0;
+}
+// Waits are bounded: a second or more, in cycles (%globaltimer costs about a
+// microsecond to read).
+constexpr long long kWaitClk = 2'100'000'000ll;
+// Bounded wait for the phase with this parity; false on time-out or once another
+// thread of the block has given up.  The block then ends with its results
+// undefined and `err` set.
 static __device__ __noinline__ bool mb_wait_slow(uint64_t *b, uint32_t parity, volatile int *abort, int32_t *err) {
-    const unsigned long long t0 = global_ns();
+    const long long t0 = clock64();
     for (;;) {
-        if (mb_try(b, parity)) return true;
+        if (mb_try_sleep(b, parity)) return true;
         if (*abort) return false;
-        if (global_ns() - t0 > kWaitNs) {
+        if (clock64() - t0 > kWaitClk) {
             *abort = 1;
             atomicOr(err, kErrSyncTimeout);
             return false;
@@ -59,7 +76,7 @@ static __device__ __noinline__ bool mb_wait_slow(uint64_t *b, uint32_t parity, v
     }
 }
 __device__ __forceinline__ bool mb_wait(uint64_t *b, uint32_t parity, volatile int *abort, int32_t *err) {
-    return mb_try(b, parity) || mb_wait_slow(b, parity, abort, err);
+    return mb_test(b, parity) || mb_wait_slow(b, parity, abort, err);
 }
 // Slot and parity of a ring.
 struct Ring {
@@ -125,13 +142,12 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // -------------------------------------------------------------------- MMAs
 // Shared-memory descriptor with the 128-byte swizzle (atoms of 8 rows of 128
 // bytes, 1024-byte aligned).  K-major operands: sbo = distance of 8-row groups,
-// lbo unused, and 32 bytes of K step the address by 32.  MN-major operands (a row
+// lbo unused, and 32 bytes of K step the address by 32 (the descriptor by 2).  MN-major operands (a row
 // of the tile holds 64 elements of M or N at one K): lbo = distance of the blocks
-// of 64 elements, sbo = distance of groups of 8 K, and 16 K step the address by 2048.
-__device__ __forceinline__ uint64_t desc(uint32_t at, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((at & 0x3FFFF) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// of 64 elements, sbo = distance of groups of 8 K, and 16 K step the address by 2048.  Here sbo is 1024.
+// Only the address and lbo vary: the lower half, without carries into the upper.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // sbo 1024, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc(uint32_t at, uint32_t lbo) { return ((at & 0x3FFFF) >> 4) | ((lbo >> 4) << 16); }
 // Byte offset of 16-byte piece c of row r in such a tile.
 __device__ __forceinline__ uint32_t sw_off(int r, int c) {
     return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
@@ -141,18 +157,17 @@ __host__ __device__ constexpr uint32_t idesc(int fmt, int a_mn, int b_mn, int m,
     return (1u << 4) | ((uint32_t)fmt << 7) | ((uint32_t)fmt << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(id), "r"(acc));
-}
-__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(id), "r"(acc));
-}
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(id), "r"(acc));
-}
+// D (+)= A B^T.  One thread issues: inside `if (lead)`, lead from elect().
+#define MOE_TC_MMA(NAME, KIND, A, AREG)                                                                       \
+    __device__ __forceinline__ void NAME(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {     \
+        asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n" AREG                    \
+                     " mov.b64 y, {%2, %4};\n tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A ", y, %3, p;\n}" ::"r"(d), \
+                     "r"(a), "r"(b), "r"(id), "n"(kDescHi), "r"(acc));                                        \
+    }
+MOE_TC_MMA(mma_f16, "f16", "x", " mov.b64 x, {%1, %4};\n")
+MOE_TC_MMA(mma_f16_ta, "f16", "[%1]", "")  // A in tensor memory
+MOE_TC_MMA(mma_f8, "f8f6f4", "x", " mov.b64 x, {%1, %4};\n")
+#undef MOE_TC_MMA
 // The barrier's arrival once all MMAs of this thread so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t *b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(b)) : "memory");
