@@ -46,7 +46,12 @@ def _codes(name, t, rows=None):
             rows is not None and t.shape[0] != rows):
         raise ValueError(f"{name}: expected float8_e4m3fn (or uint8 codes) [{'rows' if rows is None else rows}, dim] with "
                          f"contiguous rows, got {t.dtype} {tuple(t.shape)}")
-    return t.shape[0], t.shape[1], t.stride(0)
+    return t.shape[0], t.shape[1], _st(t, 0)[0]
+
+
+def _st(t, *dims):
+    """Strides, 0 where there is nothing to step to."""
+    return [t.stride(d) if t.shape[d] > 1 else 0 for d in dims]
 
 
 def quant_act_fp8(x, x8=None, scale=None, stream=None):
@@ -71,7 +76,7 @@ def quant_act_fp8(x, x8=None, scale=None, stream=None):
     else:
         _ints("scale", scale, (n, groups), torch.float32)
     try:
-        _check(_lib.moe_quant_act_fp8(x.data_ptr(), act, x.stride(0), n, dim, x8.data_ptr(), row, scale.data_ptr(),
+        _check(_lib.moe_quant_act_fp8(x.data_ptr(), act, *_st(x, 0), n, dim, x8.data_ptr(), row, scale.data_ptr(),
                                       _raw(stream, dev)))
     except ctypes.ArgumentError as e:
         _refuse(e)
@@ -101,7 +106,7 @@ def fp8_linear(x8, x_scale, w8, scale_inv, out=None, dtype=torch.bfloat16, strea
         raise ValueError(f"out: expected float32, float16 or bfloat16, got {out.dtype}")
     try:
         args = _LINEAR_ARGS.pack(n, inner, outer, kind, x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(),
-                                 scale_inv.data_ptr(), out.data_ptr(), xs, ws, out.stride(0))
+                                 scale_inv.data_ptr(), out.data_ptr(), xs, ws, *_st(out, 0))
     except _UNPACKABLE as e:
         _refuse(e)
     _check(_lib.moe_fp8_linear(args, _raw(stream, dev)))
@@ -171,7 +176,7 @@ class LatentAttention:
             args = _LATENT_ARGS.pack(
                 n, act, act if cache.dtype is dt else MOE_E4M3, cs[1], cols, scale, k_scale, seq_len.data_ptr(),
                 block_table.data_ptr(), row, cs[0], q.data_ptr(), cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                q.stride(0), q.stride(1), out.stride(0), out.stride(1), ct[0], ct[1])
+                *_st(q, 0, 1), *_st(out, 0, 1), *_st(cache, 0, 1))
         except _UNPACKABLE as e:
             _refuse(e)
         _check(_lib.moe_latent_decode(self.handle, args, _raw(stream, dev)))
@@ -211,13 +216,12 @@ def latent_prompt(q, k, k_rope, v, q_start, kv_start, scale, causal=True, out=No
     n = q_start.shape[0] - 1 if q_start.dim() == 1 else -1
     _ints("q_start", q_start, (max(n, 0) + 1,))
     _ints("kv_start", kv_start, (max(n, 0) + 1,))
-    rs = 0 if k_rope is None else k_rope.stride(0)
     try:
         args = _PROMPT_ARGS.pack(
             n, heads, nq, nk, nope, rope, v_dim, act, bool(causal), scale, q_start.data_ptr(), kv_start.data_ptr(),
             q.data_ptr(), k.data_ptr(), 0 if k_rope is None else k_rope.data_ptr(), v.data_ptr(), out.data_ptr(),
-            lse.data_ptr(), q.stride(0), q.stride(1), k.stride(0), k.stride(1), rs, v.stride(0), v.stride(1),
-            out.stride(0), out.stride(1))
+            lse.data_ptr(), *_st(q, 0, 1), *_st(k, 0, 1), *((0,) if k_rope is None else _st(k_rope, 0)), *_st(v, 0, 1),
+            *_st(out, 0, 1))
     except _UNPACKABLE as e:
         _refuse(e)
     _check(_lib.moe_latent_prompt(args, _raw(stream, dev)))

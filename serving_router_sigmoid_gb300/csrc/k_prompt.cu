@@ -1,57 +1,593 @@
-// k_prompt.cu -- attention of ragged prompts over expanded keys and values
-// (moe_latent_prompt): one warp a (query, head).
-#include "latent_args.cuh"
+// k_prompt.cu -- attention of ragged prompts over keys and values expanded a
+// head, the keys' rotary part shared by the heads (moe_latent_prompt):
+//   s_ij = scale (qn_i . kn_j + qr_i . kr_j),  out_i = sum_j e^(s_ij) v_j / sum_j e^(s_ij)
+//
+// Both products run on tcgen05 with fp32 accumulators in tensor memory: S = Q K^T
+// (128 queries by 128 keys) from shared memory, O += P V with the weights P in
+// tensor memory (where S stood) and V an MN-major operand.  At 128 + 64 / 128
+// dimensions a tile of keys is 768 + 512 cycles of the tensor core.
+//
+// - Narrow heads (values up to 128, keys up to 192 dimensions): a block holds 256
+//   queries as two streams that share the keys; while one stream's softmax runs,
+//   the tensor core works for the other (512 columns: S and O of both).  Wide heads
+//   (to 256): 128 queries, S of two tiles in turn, one O of 256 columns; both
+//   groups of softmax warps work on one tile, half the columns each.
+//   In both the order is S(0), S(1), PV(0), S(2), PV(1), ... over the steps, where
+//   step k + 2 reuses the S buffer of step k.
+// - A softmax thread holds a row (narrow) or half a row of logits in registers: no
+//   shuffles.  The maximum moves only when a logit passes it by 2^kLazy; then the
+//   row of O is scaled in tensor memory.  Weights are rounded to the operand type
+//   (their sum is not), for f16 times 2^7, so that its subnormals begin at 2^-31.
+// - One warp brings tiles by TMA into a ring of 16 KB slots: 128 keys by 64
+//   dimensions, or as many rows of V as fit.  What lies outside a tensor reads as
+//   zeros; rows of V behind a request's last key, which belong to others, are set
+//   to zero (a weight of 0 does not hide a NaN).
+// - Blocks are persistent; work items (request, 256 or 128 queries, head) go to them
+//   in turn and back, a request's last queries first: the longest come first where
+//   the mask is causal.
+#include <type_traits>
+
+#include "tc_dev.cuh"
 
 namespace moe {
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(256) latent_prompt_simple(MoePromptArgs a) {
-    after_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int i = (int)(w / a.n_heads), h = (int)(w % a.n_heads);
-    if (i >= a.n_queries) return;
-    int b = 0;
-    while (b < a.n_requests && a.q_start[b + 1] <= i) ++b;
-    if (b == a.n_requests || i < a.q_start[b]) return;
-    const int q1 = min(a.q_start[b + 1], a.n_queries), k0 = max(a.kv_start[b], 0), k1 = min(a.kv_start[b + 1], a.n_keys);
-    const int end = a.causal ? min(k1, k1 - (q1 - i) + 1) : k1;
-    const T *q = static_cast<const T *>(a.q) + i * a.q_stride_t + h * a.q_stride_h;
-    double acc[8] = {}, l = 0;
-    float m = -INFINITY;
-    for (int j = k0; j < end; ++j) {
-        const T *k = static_cast<const T *>(a.k) + j * a.k_stride_t + h * a.k_stride_h;
-        const T *v = static_cast<const T *>(a.v) + j * a.v_stride_t + h * a.v_stride_h;
-        float s = 0.f;
-        for (int d = lane; d < a.nope_dim; d += 32) s += to_f32(q[d]) * to_f32(k[d]);
-        for (int d = lane; d < a.rope_dim; d += 32)
-            s += to_f32(q[a.nope_dim + d]) * to_f32(static_cast<const T *>(a.k_rope)[j * a.kr_stride_t + d]);
+using namespace tc;
+
+__device__ int32_t g_err;  // flags since the last read
+
+constexpr uint32_t kSlot = 16384;
+constexpr int kMaxSlots = 11;
+constexpr int kThreads = 320;     // 8 softmax warps, the MMA and the TMA warp
+constexpr float kLazy = 8.f;
+constexpr float kFloor = -3.4028235e38f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kColO = 256;   // tensor memory: S twice 128 columns, then O
+
+struct Params {
+    MoePromptArgs a;
+    float factor;                 // |scale| * log2(e)
+    int negate;                   // scale < 0
+    int nope_chunks, rope, chunks; // of 64 dimensions; chunks: with the rotary one
+    int v_rows, v_boxes, v_slots; // rows of V in a slot, boxes of 64 dimensions, slots of 128 rows
+    int slots;                    // of the ring
+    int q_heads, k_heads, v_heads; // 0: one row for all heads
+    int out32;
+};
+
+struct Shared {
+    uint64_t full[kMaxSlots], empty[kMaxSlots], q_full, q_empty, v_fixed[2], s_full[2], p_ready[2], pv_done[2], o_full[2], o_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+    float top[2][2][128];         // wide heads: the halves' row maxima, by the step's parity
+};
+
+// A work item: queries [q0, q0 + nq) of a request, its keys [k0, k0 + nk), and for
+// each stream the tiles of 128 keys that its rows see.
+struct Item {
+    int head, q0, nq, k0, nk, last;   // last: the request's queries end `last` rows behind q0
+    int tiles[2], n;
+};
+
+template <int NQ>
+struct Cursor {
+    int group = 0;                    // 32 requests from here on
+    long long before = 0;             // blocks of queries before them
+    // the it-th item of this block; the whole warp calls
+    __device__ __forceinline__ bool item(const Params &p, int it, Item &x) {
+        const MoePromptArgs &a = p.a;
+        const int G = gridDim.x, lane = threadIdx.x & 31;
+        const long long idx = (long long)it * G + (it & 1 ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        const long long unit = idx / a.n_heads;
+        x.head = (int)(idx - unit * a.n_heads);
+        for (; group < a.n_requests; group += 32) {
+            const int b = group + lane;
+            int q0 = 0, q1 = 0;
+            if (b < a.n_requests) {
+                q0 = max(ld_in(a.q_start + b), 0);
+                q1 = min(ld_in(a.q_start + b + 1), a.n_queries);
+            }
+            const int blocks = q1 > q0 ? (q1 - q0 + 128 * NQ - 1) / (128 * NQ) : 0;
+            int sum = blocks;
 #pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale;
-        const float top = fmaxf(m, s), f = __expf(m - top), p = __expf(s - top);
-        m = top;
-        l = l * f + p;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += v;
+            }
+            const int all = __shfl_sync(0xffffffffu, sum, 31);
+            if (unit < before + all) {
+                const int at = (int)(unit - before);
+                const int from = __ffs(__ballot_sync(0xffffffffu, at < sum)) - 1;  // the lane of its request
+                const int first = __shfl_sync(0xffffffffu, sum - blocks, from), nb = __shfl_sync(0xffffffffu, blocks, from);
+                q0 = __shfl_sync(0xffffffffu, q0, from);
+                q1 = __shfl_sync(0xffffffffu, q1, from);
+                const int r = group + from;
+                x.k0 = min(max(ld_in(a.kv_start + r), 0), a.n_keys);
+                x.nk = max(min(ld_in(a.kv_start + r + 1), a.n_keys) - x.k0, 0);
+                x.q0 = q0 + (nb - 1 - (at - first)) * 128 * NQ;
+                x.last = q1 - x.q0;
+                x.nq = min(x.last, 128 * NQ);
+                x.n = 0;
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-            if (lane + 32 * x < a.v_dim) acc[x] = acc[x] * f + p * to_f32(v[lane + 32 * x]);
+                for (int g = 0; g < 2; ++g) {
+                    const int rows = min(max(x.nq - 128 * g, 0), 128);
+                    const int sees = rows && (g < NQ) ? seen(a, x, 128 * g + rows - 1) : 0;
+                    x.tiles[g] = (sees + 127) / 128;
+                    x.n = max(x.n, x.tiles[g]);
+                }
+                return true;
+            }
+            before += all;
+        }
+        return false;
     }
+    // keys that row r of the item sees
+    static __device__ __forceinline__ int seen(const MoePromptArgs &a, const Item &x, int r) {
+        return a.causal ? max(min(x.nk - (x.last - r) + 1, x.nk), 0) : x.nk;
+    }
+};
+
+// The ring's positions of the tiles' keys and values, in the order of their first use.
+template <int NQ>
+struct Places {
+    int nk, nv;
+    __device__ __forceinline__ int keys(int j) const { return NQ == 2 ? j * (nk + nv) : j == 0 ? 0 : nk + (j - 1) * (nk + nv); }
+    __device__ __forceinline__ int values(int j, int n) const {
+        return NQ == 2 ? j * (nk + nv) + nk : j + 1 < n ? nk + j * (nk + nv) + nk : nk + (n - 1) * (nk + nv);
+    }
+    __device__ __forceinline__ int all(int n) const { return n * (nk + nv); }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <typename T, int NQ>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
+    constexpr bool BF = sizeof(T) == 2 && !std::is_same<T, __half>::value;
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared sm;
+    uint8_t *dyn = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const MoePromptArgs &a = p.a;
+    const uint32_t ring = su32(dyn), qbase = ring + (uint32_t)p.slots * kSlot;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int *abort = &sm.abort;
+
+    if (tid == 0) {
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mb_init(&sm.full[i], 1);
+            mb_init(&sm.empty[i], 1);
+        }
+        mb_init(&sm.q_full, 1);
+        mb_init(&sm.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mb_init(&sm.v_fixed[i], 1);  // in turn: the copies are an item ahead at most
+            mb_init(&sm.s_full[i], 1);
+            mb_init(&sm.p_ready[i], NQ == 2 ? 4 : 8);
+            mb_init(&sm.pv_done[i], 1);
+            mb_init(&sm.o_full[i], 1);
+            mb_init(&sm.o_empty[i], NQ == 2 ? 4 : 8);
+        }
+        mb_init(&sm.drain, 1);
+        sm.abort = 0;
+        mb_init_done();
+        tma_prefetch(&qmap);
+        tma_prefetch(&kmap);
+        tma_prefetch(&vmap);
+    }
+    if (warp == 8) tmem_alloc(&sm.tmem, 512);
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = sm.tmem;
+    after_previous();
+
+    Cursor<NQ> cur;
+    Item x;
+    const Places<NQ> place = {p.chunks, p.v_slots};
+
+    if (warp == 9) {
+        // ------------------------------------------------------------- TMA
+        int pos = 0, slot = 0;             // slots taken so far
+        uint32_t phase = 0, qp = 0, fixes = 0;
+        bool ok = true;
+        const auto take = [&]() {          // the next slot, free
+            ok = __all_sync(0xffffffffu, ok && mb_wait(&sm.empty[slot], phase ^ 1, abort, &g_err));
+        };
+        const auto next = [&]() {
+            ++pos;
+            if (++slot == p.slots) { slot = 0; phase ^= 1; }
+        };
+        for (int it = 0; ok && cur.item(p, it, x); ++it) {
+            if (!x.n) continue;
+            ok = __all_sync(0xffffffffu, mb_wait(&sm.q_empty, qp ^ 1, abort, &g_err));
+            qp ^= 1;
+            if (!ok) break;
+            if (lane == 0) {
+                mb_expect_tx(&sm.q_full, (uint32_t)(NQ * p.chunks) * kSlot);
+                for (int g = 0; g < NQ; ++g)
+                    for (int c = 0; c < p.chunks; ++c)
+                        tma_3d(qbase + (uint32_t)(g * p.chunks + c) * kSlot, &qmap, c < p.nope_chunks ? 64 * c : a.nope_dim, x.q0 + 128 * g,
+                               p.q_heads * x.head, &sm.q_full);
+            }
+            __syncwarp();
+            const auto keys = [&](int j) {
+                for (int c = 0; c < p.chunks; ++c, next()) {
+                    take();
+                    if (ok && lane == 0) {
+                        const uint32_t at = ring + (uint32_t)slot * kSlot;
+                        mb_expect_tx(&sm.full[slot], kSlot);
+                        if (c < p.nope_chunks) tma_3d(at, &kmap, 64 * c, x.k0 + 128 * j, p.k_heads * x.head, &sm.full[slot]);
+                        else tma_2d(at, &rmap, 0, x.k0 + 128 * j, &sm.full[slot]);
+                    }
+                    __syncwarp();
+                }
+            };
+            const auto values = [&](int j) {
+                const int live = x.nk - 128 * j;   // rows of this request
+                for (int s = 0; s < p.v_slots; ++s, next()) {
+                    take();
+                    const uint32_t box = (uint32_t)p.v_rows * 128u;
+                    if (ok && lane == 0) {
+                        const uint32_t at = ring + (uint32_t)slot * kSlot;
+                        mb_expect_tx(&sm.full[slot], (uint32_t)p.v_boxes * box);
+                        for (int c = 0; c < p.v_boxes; ++c)
+                            tma_3d(at + (uint32_t)c * box, &vmap, 64 * c, x.k0 + 128 * j + s * p.v_rows, p.v_heads * x.head, &sm.full[slot]);
+                    }
+                    __syncwarp();
+                    if (ok && live < 128) {
+                        // rows behind the last key, as far as the last step of 16 goes
+                        const int r0 = max(live - s * p.v_rows, 0), r1 = min((live + 15) / 16 * 16 - s * p.v_rows, p.v_rows);
+                        if (r0 < r1) {
+                            ok = __all_sync(0xffffffffu, mb_wait(&sm.full[slot], phase, abort, &g_err));
+                            for (int i = lane; i < (r1 - r0) * 8 * p.v_boxes; i += 32) {
+                                const int c = i / (8 * (r1 - r0)), r = r0 + i / 8 % (r1 - r0);
+                                *reinterpret_cast<uint4 *>(dyn + (uint32_t)slot * kSlot + (uint32_t)c * box + sw_off(r, i & 7)) = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                    }
+                }
+                if (live < 128) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(&sm.v_fixed[fixes & 1]);
+                    ++fixes;
+                }
+            };
+            for (int j = 0; j < x.n && ok; ++j) {
+                keys(j);
+                if (NQ == 2) values(j);
+                else if (j) values(j - 1);
+            }
+            if (NQ == 1 && ok) values(x.n - 1);
+        }
+        if (*abort) {  // copies in flight land before the block ends
+            const long long t = clock64();
+            for (int i = pos > p.slots ? pos - p.slots : 0; i < pos; ++i)
+                while (!mb_test(&sm.full[i % p.slots], (uint32_t)(i / p.slots & 1)) && clock64() - t < kWaitClk / 16) {}
+        }
+    } else if (warp == 8) {
+        // -------------------------------------------------------------- MMA
+        const uint32_t fmt = BF ? 1 : 0;
+        const uint32_t id_s = idesc(fmt, 0, 0, 128, 128), id_o = idesc(fmt, 0, 1, 128, a.v_dim);
+        const uint32_t dq = desc(qbase, 16), dk = desc(ring, 16), dv = desc(ring, (uint32_t)p.v_rows * 128u);
+        const int rest = (a.nope_dim % 64) / 16, rope_steps = a.rope_dim / 16;
+        const bool lead = elect();
+        const auto wait = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_wait(bar, phase, abort, &g_err)); };
+        long long base = 0;                // ring position of the item
+        uint32_t qf = 0, fixes = 0, pr[2] = {0, 0}, oe[2] = {0, 0}, step = 0;
+        bool ok = true;
+        for (int it = 0; ok && cur.item(p, it, x); ++it) {
+            if (!x.n) continue;
+            if (!(ok = wait(&sm.q_full, qf))) break;
+            qf ^= 1;
+            const auto slot_of = [&](int at, uint32_t &phase) {
+                const long long q = base + at;
+                const int s = (int)(q % p.slots);
+                phase = (uint32_t)(q / p.slots & 1);
+                return s;
+            };
+            // S of tile j into buffer b (narrow: of stream b)
+            const auto first = [&](int b, int j) -> bool {
+                for (int c = 0; c < p.chunks; ++c) {
+                    uint32_t phase;
+                    const int s = slot_of(place.keys(j) + c, phase);
+                    if (!wait(&sm.full[s], phase)) return false;
+                    tc_after_sync();
+                    if (lead) {
+                        const uint32_t q = dq + (uint32_t)(((NQ == 2 ? b * p.chunks : 0) + c) * (int)(kSlot >> 4)), k = dk + (uint32_t)(s * (int)(kSlot >> 4));
+                        const uint32_t d = tmem + 128 * b;
+                        const int n = c >= p.nope_chunks ? rope_steps : c + 1 == p.nope_chunks && rest ? rest : 4;
+                        if (n == 4) {
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
-        if (lane + 32 * x < a.v_dim)
-            from_f32(l > 0 ? (float)(acc[x] / l) : 0.f, static_cast<T *>(a.out)[i * a.out_stride_t + h * a.out_stride_h + lane + 32 * x]);
-    if (!lane && a.lse) a.lse[(int64_t)i * a.n_heads + h] = m + logf((float)l);
+                            for (int e = 0; e < 4; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id_s, c + e != 0);
+                        } else {
+                            for (int e = 0; e < n; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id_s, c + e != 0);
+                        }
+                        // the last stream that sees this tile
+                        if (NQ == 1 || b == 1 || j >= x.tiles[1]) mma_commit(&sm.empty[s]);
+                    }
+                    __syncwarp();
+                }
+                if (lead) mma_commit(&sm.s_full[b]);
+                __syncwarp();
+                return true;
+            };
+            // O += P V of tile j, step buffer b
+            const auto second = [&](int b, int j) -> bool {
+                const int o = NQ == 2 ? b : 0;
+                if (!wait(&sm.p_ready[b], pr[b])) return false;
+                pr[b] ^= 1;
+                if (j == 0) {
+                    if (!wait(&sm.o_empty[o], oe[o] ^ 1)) return false;
+                    oe[o] ^= 1;
+                }
+                const int live = x.nk - 128 * j, steps = (min(live, 128) + 15) / 16, per = p.v_rows / 16;
+                const bool frees = NQ == 1 || b == 1 || j >= x.tiles[1];
+                if (live < 128 && (NQ == 1 || b == 0 || j >= x.tiles[0])) {  // once a tile
+                    if (!wait(&sm.v_fixed[fixes & 1], fixes >> 1 & 1)) return false;
+                    ++fixes;
+                }
+                for (int i = 0; i < p.v_slots; ++i) {
+                    uint32_t phase;
+                    const int s = slot_of(place.values(j, x.n) + i, phase);
+                    if (!wait(&sm.full[s], phase)) return false;
+                    tc_after_sync();
+                    if (lead) {
+                        const uint32_t v = dv + (uint32_t)(s * (int)(kSlot >> 4)), d = tmem + kColO + 128 * o, w = tmem + 128 * b;
+                        for (int e = 0; e < per; ++e)
+                            if (i * per + e < steps)
+                                mma_f16_ta(d, w + 8 * (i * per + e), v + e * (2048 >> 4), id_o, !(j == 0 && i + e == 0));
+                        if (frees) mma_commit(&sm.empty[s]);
+                    }
+                    __syncwarp();
+                }
+                if (lead) {
+                    mma_commit(&sm.pv_done[b]);
+                    if (j + 1 == x.tiles[o]) mma_commit(&sm.o_full[o]);
+                }
+                __syncwarp();
+                return true;
+            };
+            int pb = -1, pj = 0;           // the step whose second product is due
+            for (int j = 0; j < x.n && ok; ++j)
+                for (int g = 0; g < NQ && ok; ++g) {
+                    if (j >= x.tiles[g]) continue;
+                    const int b = NQ == 2 ? g : (int)(step++ & 1);
+                    if (NQ == 2 && pb == b) {  // the other stream is done: P of this one stands where S goes
+                        ok = second(pb, pj);
+                        pb = -1;
+                    }
+                    ok = ok && first(b, j);
+                    if (ok && pb >= 0) ok = second(pb, pj);
+                    pb = b;
+                    pj = j;
+                }
+            if (ok && lead) mma_commit(&sm.q_empty);
+            __syncwarp();
+            if (ok && pb >= 0) ok = second(pb, pj);
+            base += place.all(x.n);
+        }
+        if (*abort) {  // what was issued ends before the tensor memory is freed
+            if (lead) mma_commit(&sm.drain);
+            const long long t = clock64();
+            while (!mb_test(&sm.drain, 0) && clock64() - t < kWaitClk) {}
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- softmax
+        constexpr float kOff = BF ? 0.f : 7.f;
+        constexpr int kCols = NQ == 2 ? 128 : 64;      // logits of a thread
+        const int g = warp >> 2, row = tid & 127;      // stream (narrow) or half of the columns (wide)
+        const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
+        T *out = static_cast<T *>(a.out);
+        uint32_t sf[2] = {0, 0}, pd[2] = {0, 0}, of = 0, step = 0;
+        const int o = NQ == 2 ? g : 0;
+        for (int it = 0; cur.item(p, it, x); ++it) {
+            const int q = NQ == 2 ? 128 * g + row : row;   // of the item
+            const bool mine = q < x.nq;
+            const int tiles = x.tiles[o];
+            const int sees = mine ? Cursor<NQ>::seen(a, x, q) : 0;
+            // tiles that every row of this warp sees whole need no mask
+            const int lead_row = NQ == 2 ? 128 * g + (row & ~31) : (row & ~31);
+            const int whole = lead_row + 31 < x.nq ? Cursor<NQ>::seen(a, x, lead_row) / 128 : 0;
+            float m = kFloor, l = 0.f;                 // the maximum in units of the logits
+            for (int j = 0; j < tiles; ++j) {
+                const int b = NQ == 2 ? g : (int)(step & 1);
+                mb_wait(&sm.s_full[b], sf[b], abort, &g_err);
+                sf[b] ^= 1;
+                tc_after_sync();
+                uint32_t s[kCols / 32][32];
+                const uint32_t at = tmem + quad + 128 * b;
+#pragma unroll
+                for (int c = 0; c < kCols / 32; ++c) tmem_ld(at + (NQ == 2 ? 0 : 64 * g) + 32 * c, s[c]);
+                tmem_wait_ld();
+                if (p.negate) {
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) s[c >> 5][c & 31] ^= 0x80000000u;
+                }
+                const int sees_here = sees - 128 * j - (NQ == 2 ? 0 : 64 * g);  // columns of this thread that count
+                const bool masked = j >= whole;
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c)
+                        if (c >= sees_here) s[c >> 5][c & 31] = 0xff800000u;
+                }
+                float t4[4] = {kFloor, kFloor, kFloor, kFloor};
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) t4[c & 3] = fmaxf(t4[c & 3], __uint_as_float(s[c >> 5][c & 31]));
+                float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                if (NQ == 1) {                         // the row's other half
+                    sm.top[step & 1][g][row] = top;
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    top = fmaxf(top, sm.top[step & 1][g ^ 1][row]);
+                }
+                if (j == 0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, top * p.factor > m * p.factor + kLazy)) {
+                    const float to = fmaxf(m, top), f = ex2((m - to) * p.factor);
+                    m = to;
+                    l *= f;
+                    // O of the tiles before is complete, then its rows are scaled
+                    const int pb = NQ == 2 ? b : b ^ 1;
+                    mb_wait(&sm.pv_done[pb], pd[pb] ^ 1, abort, &g_err);
+                    tc_after_sync();
+                    const int c0 = NQ == 2 ? 0 : 16 * g, c1 = a.v_dim, dc = NQ == 2 ? 16 : 32;
+                    for (int c = c0; c < c1; c += dc) {
+                        uint32_t v[16];
+                        tmem_ld(tmem + quad + kColO + 128 * o + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                        tmem_st(tmem + quad + kColO + 128 * o + c, v);
+                    }
+                }
+                pd[b] ^= 1;
+                const float mf = kOff - m * p.factor;
+                float l2[2] = {0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kCols; c += 2) {
+                    float x0 = ex2(fmaf(__uint_as_float(s[c >> 5][c & 31]), p.factor, mf)), x1 = ex2(fmaf(__uint_as_float(s[c >> 5][(c & 31) + 1]), p.factor, mf));
+                    if (masked) {                      // not by the logit: nothing is known of factor and m
+                        x0 = c < sees_here ? x0 : 0.f;
+                        x1 = c + 1 < sees_here ? x1 : 0.f;
+                    }
+                    l2[0] += x0;
+                    l2[1] += x1;
+                    s[c >> 6][(c & 63) >> 1] = pack_pair(x0, x1, T());  // pairs behind what is still to be read
+                }
+                l += l2[0] + l2[1];
+#pragma unroll
+                for (int c = 0; c < kCols / 64; ++c) {
+                    uint32_t w[2][16];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) w[k >> 4][k & 15] = s[c][k];
+                    tmem_st(at + (NQ == 2 ? 0 : 32 * g) + 32 * c, w[0]);
+                    tmem_st(at + (NQ == 2 ? 0 : 32 * g) + 32 * c + 16, w[1]);
+                }
+                tmem_wait_st();
+                tc_before_sync();
+                __syncwarp();
+                if (lane == 0) mb_arrive(&sm.p_ready[b]);
+                ++step;
+            }
+            if (NQ == 1) {                             // the row's whole sum
+                sm.top[step & 1][g][row] = l;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                l += sm.top[step & 1][g ^ 1][row];
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            T *to = out + (int64_t)(x.q0 + q) * a.out_stride_t + (int64_t)x.head * a.out_stride_h;
+            if (tiles) {
+                mb_wait(&sm.o_full[o], of, abort, &g_err);
+                of ^= 1;
+                tc_after_sync();
+            }
+            const int c0 = NQ == 2 ? 0 : 16 * g, dc = NQ == 2 ? 16 : 32;
+            for (int c = c0; c < a.v_dim; c += dc) {
+                uint32_t v[16], y[8];
+                if (tiles) {
+                    tmem_ld(tmem + quad + kColO + 128 * o + c, v);
+                    tmem_wait_ld();
+                }
+                if (!mine) continue;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    y[k] = tiles ? pack_pair(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv, T()) : 0u;
+                if (l == 0.f)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = 0u;
+                if (p.out32) {
+                    st32(to + c, y);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) reinterpret_cast<uint16_t *>(to)[c + k] = (uint16_t)(y[k >> 1] >> (16 * (k & 1)));
+                }
+            }
+            if (mine && a.lse && (NQ == 2 || g == 0))
+                a.lse[(int64_t)(x.q0 + q) * a.n_heads + x.head] = l > 0.f ? (m * p.factor - kOff) / kLog2e + logf(l) : -INFINITY;
+            if (tiles) {
+                tc_before_sync();
+                __syncwarp();
+                if (lane == 0) mb_arrive(&sm.o_empty[o]);
+            }
+        }
+    }
+
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    if (warp == 8) tmem_free(tmem, 512);
+}
+
+template <typename T, int NQ>
+cudaError_t launch(const MoePromptArgs &a, Params &p, int sms, cudaStream_t s) {
+    const int v_pad = (a.v_dim + 63) / 64;
+    p.v_boxes = v_pad;
+    p.v_rows = v_pad == 1 ? 128 : v_pad == 2 ? 64 : 32;
+    p.v_slots = 128 / p.v_rows;
+    p.slots = (int)((227 * 1024 - 1024 - sizeof(Shared) - 64) / kSlot) - NQ * p.chunks;
+    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+    const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap maps[4] = {};
+    const auto map = [&](int i, const void *base, int dim, int rows, int64_t st, int64_t sh, int &heads, int box) {
+        const bool one = a.n_heads == 1 || sh == 0;
+        heads = one ? 0 : 1;
+        const int64_t row = (2 * dim + 15) / 16 * 16;
+        const int64_t d[3] = {dim, rows, one ? 1 : a.n_heads}, str[2] = {rows > 1 ? 2 * st : row, one ? row : 2 * sh};
+        return encode_map(&maps[i], type, 2, base, 3, d, str, box);
+    };
+    int unused;
+    cudaError_t e = map(0, a.q, a.nope_dim + a.rope_dim, a.n_queries, a.q_stride_t, a.q_stride_h, p.q_heads, 128);
+    // without keys nothing is loaded: any valid map will do
+    if (e == cudaSuccess) e = a.n_keys ? map(1, a.k, a.nope_dim, a.n_keys, a.k_stride_t, a.k_stride_h, p.k_heads, 128) : (maps[1] = maps[0], cudaSuccess);
+    if (e == cudaSuccess) e = a.n_keys ? map(3, a.v, a.v_dim, a.n_keys, a.v_stride_t, a.v_stride_h, p.v_heads, p.v_rows) : (maps[3] = maps[0], cudaSuccess);
+    if (e == cudaSuccess && a.rope_dim && a.n_keys) {
+        const int64_t d[3] = {a.rope_dim, a.n_keys, 1}, str[2] = {a.n_keys > 1 ? 2 * a.kr_stride_t : 128, 0};
+        e = encode_map(&maps[2], type, 2, a.k_rope, 2, d, str, 128);
+    } else {
+        maps[2] = maps[0];
+    }
+    (void)unused;
+    if (e != cudaSuccess) return e;
+    const size_t smem = (size_t)(p.slots + NQ * p.chunks) * kSlot + 1024;
+    auto fn = prompt_kernel<T, NQ>;
+    if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    // no more blocks than there can be items
+    const int64_t most = ((int64_t)a.n_queries / (128 * NQ) + a.n_requests) * a.n_heads;
+    void *args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
+    return launch_after(reinterpret_cast<const void *>(fn), (int)(most < sms ? most : sms), kThreads, smem, s, args);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_prompt(const MoePromptArgs &a, cudaStream_t s) {
-    MoePromptArgs p = a;
-    void *args[] = {&p};
-    const void *fn = a.act_type == MOE_F16 ? (const void *)latent_prompt_simple<__half>
-                                           : (const void *)latent_prompt_simple<__nv_bfloat16>;
-    return launch_after(fn, (int)(((int64_t)a.n_queries * a.n_heads + 7) / 8), 256, 0, s, args);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    Params p = {};
+    p.a = a;
+    p.factor = (a.scale < 0 ? -a.scale : a.scale) * kLog2e;
+    p.negate = a.scale < 0;
+    p.nope_chunks = (a.nope_dim + 63) / 64;
+    p.chunks = p.nope_chunks + (a.rope_dim > 0);
+    p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride_t % 16 == 0 && a.out_stride_h % 16 == 0;
+    const bool narrow = a.v_dim <= 128 && p.chunks <= 3;
+    if (a.act_type == MOE_F16) return narrow ? launch<__half, 2>(a, p, sms, s) : launch<__half, 1>(a, p, sms, s);
+    return narrow ? launch<__nv_bfloat16, 2>(a, p, sms, s) : launch<__nv_bfloat16, 1>(a, p, sms, s);
+}
+
+cudaError_t latent_prompt_flags(int32_t *out) {
+    const int32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_err, 4);
+    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_err, &zero, 4);
+    return e;
 }
 
 }  // namespace moe

@@ -206,6 +206,9 @@ int moe_latent_prompt(const MoePromptArgs *p, cudaStream_t stream) {
     for (int64_t st : {a.q_stride_t, a.q_stride_h, a.k_stride_t, a.k_stride_h, a.kr_stride_t, a.v_stride_t, a.v_stride_h})
         if (st < 0 || st >= 1ll << 37 || st % 8)
             return fail(MOE_ERR_INVALID_ARG, "rows of q, k, k_rope and v must start on 16 bytes, strides below 2^38 bytes");
+    if ((a.n_queries > 1 && a.q_stride_t == 0) ||
+        (a.n_keys > 1 && (a.k_stride_t == 0 || a.v_stride_t == 0 || (a.rope_dim > 0 && a.kr_stride_t == 0))))
+        return fail(MOE_ERR_INVALID_ARG, "tokens of q, k, k_rope and v have rows of their own");
     for (int64_t st : {a.out_stride_t, a.out_stride_h})
         if (st < 0 || st >= 1ll << 37) return fail(MOE_ERR_INVALID_ARG, "out strides must lie in [0, 2^38) bytes");
     if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || (a.rope_dim > 0 && !aligned(a.k_rope, 16)))
@@ -232,7 +235,7 @@ int moe_dense_status(cudaStream_t stream, int *status_out) {
     if (!status_out) return fail(MOE_ERR_INVALID_ARG, "status_out is NULL");
     *status_out = 0;
     cudaError_t e = cudaStreamSynchronize(stream);
-    for (const auto flags : {moe::fp8_linear_flags, moe::latent_decode_flags}) {
+    for (const auto flags : {moe::fp8_linear_flags, moe::latent_decode_flags, moe::latent_prompt_flags}) {
         int32_t v = 0;
         if (e == cudaSuccess) e = flags(&v);
         *status_out |= v;

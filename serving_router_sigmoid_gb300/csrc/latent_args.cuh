@@ -25,5 +25,6 @@ cudaError_t launch_latent_prompt(const MoePromptArgs &a, cudaStream_t s);
 // The flags that a file's kernels left on the current device, read and cleared.
 cudaError_t fp8_linear_flags(int32_t *out);
 cudaError_t latent_decode_flags(int32_t *out);
+cudaError_t latent_prompt_flags(int32_t *out);
 
 }  // namespace moe
