@@ -127,15 +127,16 @@ struct Cursor {
     }
 };
 
-// The ring's positions of the tiles' keys and values, in the order of their first use.
-template <int NQ>
-struct Places {
-    int nk, nv;
-    __device__ __forceinline__ int keys(int j) const { return NQ == 2 ? j * (nk + nv) : j == 0 ? 0 : nk + (j - 1) * (nk + nv); }
-    __device__ __forceinline__ int values(int j, int n) const {
-        return NQ == 2 ? j * (nk + nv) + nk : j + 1 < n ? nk + j * (nk + nv) + nk : nk + (n - 1) * (nk + nv);
+// A position in the ring of slots.
+struct Place {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step(int n, int slots) {  // n <= slots
+        if ((slot += n) >= slots) {
+            slot -= slots;
+            phase ^= 1;
+        }
     }
-    __device__ __forceinline__ int all(int n) const { return n * (nk + nv); }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -188,7 +189,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     Cursor<NQ> cur;
     Item x;
-    const Places<NQ> place = {p.chunks, p.v_slots};
 
     if (warp == 9) {
         // ------------------------------------------------------------- TMA
@@ -278,29 +278,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rest = (a.nope_dim % 64) / 16, rope_steps = a.rope_dim / 16;
         const bool lead = elect();
         const auto wait = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_wait(bar, phase, abort, &g_err)); };
-        long long base = 0;                // ring position of the item
+        const int nk = p.chunks, nv = p.v_slots, slots = p.slots;
+        Place kp, vp;                      // the keys of the next first product's tile, the values of the next second's
         uint32_t qf = 0, fixes = 0, pr[2] = {0, 0}, oe[2] = {0, 0}, step = 0;
         bool ok = true;
         for (int it = 0; ok && cur.item(p, it, x); ++it) {
             if (!x.n) continue;
             if (!(ok = wait(&sm.q_full, qf))) break;
             qf ^= 1;
-            const auto slot_of = [&](int at, uint32_t &phase) {
-                const long long q = base + at;
-                const int s = (int)(q % p.slots);
-                phase = (uint32_t)(q / p.slots & 1);
-                return s;
+            // The ring holds, narrow: K0 V0 K1 V1 ..., wide: K0 K1 V0 K2 V1 ..., as they are first used.
+            const Place begin = kp;
+            vp = begin;
+            vp.step(nk, slots);
+            if (NQ == 1 && x.n > 1) vp.step(nk, slots);
+            const auto landed = [&](Place at, int n) {
+                bool all = true;
+                for (int i = 0; i < n && all; ++i, at.step(1, slots)) all = wait(&sm.full[at.slot], at.phase);
+                return all;
             };
             // S of tile j into buffer b (narrow: of stream b)
             const auto first = [&](int b, int j) -> bool {
-                for (int c = 0; c < p.chunks; ++c) {
-                    uint32_t phase;
-                    const int s = slot_of(place.keys(j) + c, phase);
-                    if (!wait(&sm.full[s], phase)) return false;
-                    tc_after_sync();
-                    if (lead) {
-                        const uint32_t q = dq + (uint32_t)(((NQ == 2 ? b * p.chunks : 0) + c) * (int)(kSlot >> 4)), k = dk + (uint32_t)(s * (int)(kSlot >> 4));
-                        const uint32_t d = tmem + 128 * b;
+                if (!landed(kp, nk)) return false;
+                tc_after_sync();
+                const bool frees = NQ == 1 || b == 1 || j >= x.tiles[1];  // the last stream that sees this tile
+                if (lead) {
+                    uint32_t q = dq + (uint32_t)((NQ == 2 ? b * p.chunks : 0) * (int)(kSlot >> 4));
+                    const uint32_t d = tmem + 128 * b;
+                    Place at = kp;
+                    for (int c = 0; c < nk; ++c, q += kSlot >> 4, at.step(1, slots)) {
+                        const uint32_t k = dk + (uint32_t)(at.slot * (int)(kSlot >> 4));
                         const int n = c >= p.nope_chunks ? rope_steps : c + 1 == p.nope_chunks && rest ? rest : 4;
                         if (n == 4) {
 #pragma unroll
@@ -308,13 +314,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             for (int e = 0; e < n; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id_s, c + e != 0);
                         }
-                        // the last stream that sees this tile
-                        if (NQ == 1 || b == 1 || j >= x.tiles[1]) mma_commit(&sm.empty[s]);
+                        if (frees) mma_commit(&sm.empty[at.slot]);
                     }
-                    __syncwarp();
+                    mma_commit(&sm.s_full[b]);
                 }
-                if (lead) mma_commit(&sm.s_full[b]);
                 __syncwarp();
+                if (frees) {
+                    kp.step(nk, slots);
+                    if (NQ == 2 || j) kp.step(nv, slots);
+                }
                 return true;
             };
             // O += P V of tile j, step buffer b
@@ -332,25 +340,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!wait(&sm.v_fixed[fixes & 1], fixes >> 1 & 1)) return false;
                     ++fixes;
                 }
-                for (int i = 0; i < p.v_slots; ++i) {
-                    uint32_t phase;
-                    const int s = slot_of(place.values(j, x.n) + i, phase);
-                    if (!wait(&sm.full[s], phase)) return false;
-                    tc_after_sync();
-                    if (lead) {
-                        const uint32_t v = dv + (uint32_t)(s * (int)(kSlot >> 4)), d = tmem + kColO + 128 * o, w = tmem + 128 * b;
-                        for (int e = 0; e < per; ++e)
-                            if (i * per + e < steps)
-                                mma_f16_ta(d, w + 8 * (i * per + e), v + e * (2048 >> 4), id_o, !(j == 0 && i + e == 0));
-                        if (frees) mma_commit(&sm.empty[s]);
-                    }
-                    __syncwarp();
-                }
+                if (!landed(vp, nv)) return false;
+                tc_after_sync();
                 if (lead) {
+                    const uint32_t d = tmem + kColO + 128 * o;
+                    uint32_t w = tmem + 128 * b;
+                    Place at = vp;
+                    int left = steps;
+                    for (int i = 0; i < nv; ++i, at.step(1, slots)) {
+                        uint32_t v = dv + (uint32_t)(at.slot * (int)(kSlot >> 4));
+                        for (int e = 0; e < per && left > 0; e += 2, left -= 2, w += 16, v += 2 * (2048 >> 4)) {
+                            mma_f16_ta(d, w, v, id_o, !(j == 0 && i + e == 0));
+                            if (left > 1) mma_f16_ta(d, w + 8, v + (2048 >> 4), id_o, 1);
+                        }
+                        if (frees) mma_commit(&sm.empty[at.slot]);
+                    }
                     mma_commit(&sm.pv_done[b]);
                     if (j + 1 == x.tiles[o]) mma_commit(&sm.o_full[o]);
                 }
                 __syncwarp();
+                if (frees) {
+                    vp.step(nv, slots);
+                    if (NQ == 2 || j + 2 < x.n) vp.step(nk, slots);
+                }
                 return true;
             };
             int pb = -1, pj = 0;           // the step whose second product is due
@@ -370,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && lead) mma_commit(&sm.q_empty);
             __syncwarp();
             if (ok && pb >= 0) ok = second(pb, pj);
-            base += place.all(x.n);
+            if (NQ == 1) kp = vp;          // behind the last values, where the next item's keys begin
         }
         if (*abort) {  // what was issued ends before the tensor memory is freed
             if (lead) mma_commit(&sm.drain);
