@@ -37,8 +37,8 @@ using namespace tc;
 __device__ int32_t g_err;  // flags since the last read
 
 constexpr uint32_t kSlot = 16384;
-constexpr int kMaxSlots = 11;
-constexpr int kThreads = 320;     // 8 softmax warps, the MMA and the TMA warp
+constexpr int kTiles = 8;         // tiles of keys or values in flight, at most (a tile has two slots or more)
+constexpr int kThreads = 352;     // 8 softmax warps, two that issue MMAs, one TMA warp
 constexpr float kLazy = 8.f;
 constexpr float kFloor = -3.4028235e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -56,7 +56,7 @@ struct Params {
 };
 
 struct Shared {
-    uint64_t full[kMaxSlots], empty[kMaxSlots], q_full, q_empty, v_fixed[2], s_full[2], p_ready[2], pv_done[2], o_full[2], o_empty[2], drain;
+    uint64_t full[kTiles], empty[kTiles], q_full, q_empty, v_fixed[2], s_full[2], p_ready[2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem;
     int abort;
     float top[2][2][128];         // wide heads: the halves' row maxima, by the step's parity
@@ -127,18 +127,6 @@ struct Cursor {
     }
 };
 
-// A position in the ring of slots.
-struct Place {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void step(int n, int slots) {  // n <= slots
-        if ((slot += n) >= slots) {
-            slot -= slots;
-            phase ^= 1;
-        }
-    }
-};
-
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -159,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort = &sm.abort;
 
     if (tid == 0) {
-        for (int i = 0; i < kMaxSlots; ++i) {
+        for (int i = 0; i < kTiles; ++i) {
             mb_init(&sm.full[i], 1);
             mb_init(&sm.empty[i], 1);
         }
@@ -170,10 +158,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mb_init(&sm.s_full[i], 1);
             mb_init(&sm.p_ready[i], NQ == 2 ? 4 : 8);
             mb_init(&sm.pv_done[i], 1);
+            mb_init(&sm.drain[i], 1);
             mb_init(&sm.o_full[i], 1);
             mb_init(&sm.o_empty[i], NQ == 2 ? 4 : 8);
         }
-        mb_init(&sm.drain, 1);
         sm.abort = 0;
         mb_init_done();
         tma_prefetch(&qmap);
@@ -190,17 +178,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor<NQ> cur;
     Item x;
 
-    if (warp == 9) {
+    if (warp == 10) {
         // ------------------------------------------------------------- TMA
-        int pos = 0, slot = 0;             // slots taken so far
-        uint32_t phase = 0, qp = 0, fixes = 0;
+        // Tiles take their slots in ring order and give them back in that order.
+        const int nk = p.chunks, nv = p.v_slots;
+        int slot = 0, room = p.slots;      // next slot, free ones
+        uint32_t put = 0, got = 0;         // tiles brought, tiles whose slots are back
+        uint32_t sizes = 0;                // of the tiles in flight, 4 bits each, the oldest lowest
+        uint32_t qp = 0, fixes = 0;
         bool ok = true;
-        const auto take = [&]() {          // the next slot, free
-            ok = __all_sync(0xffffffffu, ok && mb_wait(&sm.empty[slot], phase ^ 1, abort, &g_err));
+        const auto take = [&](int n) {     // n free slots and a free pair of barriers
+            while (ok && (room < n || put - got == kTiles)) {
+                ok = __all_sync(0xffffffffu, mb_wait(&sm.empty[got % kTiles], got / kTiles & 1, abort, &g_err));
+                room += (int)(sizes & 15);
+                sizes >>= 4;
+                ++got;
+            }
+            sizes |= (uint32_t)n << (4 * (put - got));
+            room -= n;
         };
         const auto next = [&]() {
-            ++pos;
-            if (++slot == p.slots) { slot = 0; phase ^= 1; }
+            const int at = slot;
+            if (++slot == p.slots) slot = 0;
+            return ring + (uint32_t)at * kSlot;
         };
         for (int it = 0; ok && cur.item(p, it, x); ++it) {
             if (!x.n) continue;
@@ -216,47 +216,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             const auto keys = [&](int j) {
-                for (int c = 0; c < p.chunks; ++c, next()) {
-                    take();
-                    if (ok && lane == 0) {
-                        const uint32_t at = ring + (uint32_t)slot * kSlot;
-                        mb_expect_tx(&sm.full[slot], kSlot);
-                        if (c < p.nope_chunks) tma_3d(at, &kmap, 64 * c, x.k0 + 128 * j, p.k_heads * x.head, &sm.full[slot]);
-                        else tma_2d(at, &rmap, 0, x.k0 + 128 * j, &sm.full[slot]);
-                    }
-                    __syncwarp();
+                take(nk);
+                if (!ok) return;
+                uint64_t *const full = &sm.full[put % kTiles];
+                if (lane == 0) mb_expect_tx(full, (uint32_t)nk * kSlot);
+                for (int c = 0; c < nk; ++c) {
+                    const uint32_t at = next();
+                    if (lane) continue;
+                    if (c < p.nope_chunks) tma_3d(at, &kmap, 64 * c, x.k0 + 128 * j, p.k_heads * x.head, full);
+                    else tma_2d(at, &rmap, 0, x.k0 + 128 * j, full);
                 }
+                __syncwarp();
+                ++put;
             };
             const auto values = [&](int j) {
                 const int live = x.nk - 128 * j;   // rows of this request
-                for (int s = 0; s < p.v_slots; ++s, next()) {
-                    take();
-                    const uint32_t box = (uint32_t)p.v_rows * 128u;
-                    if (ok && lane == 0) {
-                        const uint32_t at = ring + (uint32_t)slot * kSlot;
-                        mb_expect_tx(&sm.full[slot], (uint32_t)p.v_boxes * box);
-                        for (int c = 0; c < p.v_boxes; ++c)
-                            tma_3d(at + (uint32_t)c * box, &vmap, 64 * c, x.k0 + 128 * j + s * p.v_rows, p.v_heads * x.head, &sm.full[slot]);
-                    }
-                    __syncwarp();
-                    if (ok && live < 128) {
-                        // rows behind the last key, as far as the last step of 16 goes
-                        const int r0 = max(live - s * p.v_rows, 0), r1 = min((live + 15) / 16 * 16 - s * p.v_rows, p.v_rows);
-                        if (r0 < r1) {
-                            ok = __all_sync(0xffffffffu, mb_wait(&sm.full[slot], phase, abort, &g_err));
-                            for (int i = lane; i < (r1 - r0) * 8 * p.v_boxes; i += 32) {
-                                const int c = i / (8 * (r1 - r0)), r = r0 + i / 8 % (r1 - r0);
-                                *reinterpret_cast<uint4 *>(dyn + (uint32_t)slot * kSlot + (uint32_t)c * box + sw_off(r, i & 7)) = make_uint4(0, 0, 0, 0);
-                            }
-                        }
-                    }
+                const uint32_t box = (uint32_t)p.v_rows * 128u;
+                take(nv);
+                if (!ok) return;
+                uint64_t *const full = &sm.full[put % kTiles];
+                const int begin = slot;
+                if (lane == 0) mb_expect_tx(full, (uint32_t)(nv * p.v_boxes) * box);
+                for (int i = 0; i < nv; ++i) {
+                    const uint32_t at = next();
+                    if (lane) continue;
+                    for (int c = 0; c < p.v_boxes; ++c)
+                        tma_3d(at + (uint32_t)c * box, &vmap, 64 * c, x.k0 + 128 * j + i * p.v_rows, p.v_heads * x.head, full);
                 }
+                __syncwarp();
                 if (live < 128) {
+                    // rows behind the last key, as far as the last step of 16 goes
+                    ok = __all_sync(0xffffffffu, mb_wait(full, put / kTiles & 1, abort, &g_err));
+                    const int r0 = live, n = (live + 15) / 16 * 16 - live;
+                    for (int i = lane; i < n * 8 * p.v_boxes; i += 32) {
+                        const int c = i / (8 * n), r = r0 + i / 8 % n, part = r / p.v_rows;
+                        const int at = begin + part < p.slots ? begin + part : begin + part - p.slots;
+                        *reinterpret_cast<uint4 *>(dyn + (uint32_t)at * kSlot + (uint32_t)c * box + sw_off(r % p.v_rows, i & 7)) =
+                            make_uint4(0, 0, 0, 0);
+                    }
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0) mb_arrive(&sm.v_fixed[fixes & 1]);
                     ++fixes;
                 }
+                ++put;
             };
             for (int j = 0; j < x.n && ok; ++j) {
                 keys(j);
@@ -267,127 +270,139 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (*abort) {  // copies in flight land before the block ends
             const long long t = clock64();
-            for (int i = pos > p.slots ? pos - p.slots : 0; i < pos; ++i)
-                while (!mb_test(&sm.full[i % p.slots], (uint32_t)(i / p.slots & 1)) && clock64() - t < kWaitClk / 16) {}
+            for (uint32_t i = put > kTiles ? put - kTiles : 0; i < put; ++i)
+                while (!mb_test(&sm.full[i % kTiles], i / kTiles & 1) && clock64() - t < kWaitClk) {}
         }
-    } else if (warp == 8) {
+    } else if (warp >= 8) {
         // -------------------------------------------------------------- MMA
+        // One warp issues the first products, another the second ones: an issue takes
+        // 40 to 100 cycles, more than a short MMA.
+        const bool firsts = warp == 8;
         const uint32_t fmt = BF ? 1 : 0;
-        const uint32_t id_s = idesc(fmt, 0, 0, 128, 128), id_o = idesc(fmt, 0, 1, 128, a.v_dim);
-        const uint32_t dq = desc(qbase, 16), dk = desc(ring, 16), dv = desc(ring, (uint32_t)p.v_rows * 128u);
-        const int rest = (a.nope_dim % 64) / 16, rope_steps = a.rope_dim / 16;
         const bool lead = elect();
-        const auto wait = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_wait(bar, phase, abort, &g_err)); };
         const int nk = p.chunks, nv = p.v_slots, slots = p.slots;
-        Place kp, vp;                      // the keys of the next first product's tile, the values of the next second's
-        uint32_t qf = 0, fixes = 0, pr[2] = {0, 0}, oe[2] = {0, 0}, step = 0;
+        const auto wait = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_wait(bar, phase, abort, &g_err)); };
+        const auto ahead = [&](int slot, int n) { return slot + n < slots ? slot + n : slot + n - slots; };
+        // Tiles come, narrow: K0 V0 K1 V1 ..., wide: K0 K1 V0 K2 V1 ..., as they are first used.
+        int slot = 0;                      // of the next item's first keys
+        uint32_t tile = 0;                 // the same as a tile, counted as they come
+        uint32_t uses[2] = {0, 0};         // of the S buffers, the last bit
+        uint32_t step = 0;
         bool ok = true;
-        for (int it = 0; ok && cur.item(p, it, x); ++it) {
-            if (!x.n) continue;
-            if (!(ok = wait(&sm.q_full, qf))) break;
-            qf ^= 1;
-            // The ring holds, narrow: K0 V0 K1 V1 ..., wide: K0 K1 V0 K2 V1 ..., as they are first used.
-            const Place begin = kp;
-            vp = begin;
-            vp.step(nk, slots);
-            if (NQ == 1 && x.n > 1) vp.step(nk, slots);
-            const auto landed = [&](Place at, int n) {
-                bool all = true;
-                for (int i = 0; i < n && all; ++i, at.step(1, slots)) all = wait(&sm.full[at.slot], at.phase);
-                return all;
-            };
-            // S of tile j into buffer b (narrow: of stream b)
-            const auto first = [&](int b, int j) -> bool {
-                if (!landed(kp, nk)) return false;
-                tc_after_sync();
-                const bool frees = NQ == 1 || b == 1 || j >= x.tiles[1];  // the last stream that sees this tile
-                if (lead) {
-                    uint32_t q = dq + (uint32_t)((NQ == 2 ? b * p.chunks : 0) * (int)(kSlot >> 4));
-                    const uint32_t d = tmem + 128 * b;
-                    Place at = kp;
-                    for (int c = 0; c < nk; ++c, q += kSlot >> 4, at.step(1, slots)) {
-                        const uint32_t k = dk + (uint32_t)(at.slot * (int)(kSlot >> 4));
-                        const int n = c >= p.nope_chunks ? rope_steps : c + 1 == p.nope_chunks && rest ? rest : 4;
-                        if (n == 4) {
+        if (firsts) {
+            // ---- S = Q K^T
+            const uint32_t id = idesc(fmt, 0, 0, 128, 128), dq = desc(qbase, 16), dk = desc(ring, 16);
+            const int rest = (a.nope_dim % 64) / 16, rope_steps = a.rope_dim / 16;
+            uint32_t qf = 0, began = 0;
+            for (int it = 0; ok && cur.item(p, it, x); ++it) {
+                if (!x.n) continue;
+                if (!(ok = wait(&sm.q_full, qf))) break;
+                qf ^= 1;
+                for (int j = 0; j < x.n && ok; ++j) {
+                    if (!(ok = wait(&sm.full[tile % kTiles], tile / kTiles & 1))) break;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id_s, c + e != 0);
-                        } else {
-                            for (int e = 0; e < n; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id_s, c + e != 0);
+                    for (int g = 0; g < NQ; ++g) {
+                        if (j >= x.tiles[g]) continue;
+                        const int b = NQ == 2 ? g : (int)(step++ & 1);
+                        // the weights of the step before in this buffer have been read
+                        if (began >> b & 1 && !(ok = wait(&sm.pv_done[b], uses[b] ^ 1))) break;
+                        began |= 1u << b;
+                        uses[b] ^= 1;
+                        tc_after_sync();
+                        if (lead) {
+                            const uint32_t d = tmem + 128 * b;
+                            uint32_t q = dq + (uint32_t)(NQ == 2 && g ? nk * (int)(kSlot >> 4) : 0);
+                            int at = slot;
+#pragma unroll 1
+                            for (int c = 0; c < nk; ++c, q += kSlot >> 4) {
+                                const uint32_t k = dk + (uint32_t)(at * (int)(kSlot >> 4));
+                                const int n = c >= p.nope_chunks ? rope_steps : c + 1 == p.nope_chunks && rest ? rest : 4;
+                                if (n == 4) {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id, c + e != 0);
+                                } else {
+#pragma unroll 1
+                                    for (int e = 0; e < n; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id, c + e != 0);
+                                }
+                                if (++at == slots) at = 0;
+                            }
+                            mma_commit(&sm.s_full[b]);
+                            // the last stream that sees this tile
+                            if (NQ == 1 || g == 1 || j >= x.tiles[1]) mma_commit(&sm.empty[tile % kTiles]);
                         }
-                        if (frees) mma_commit(&sm.empty[at.slot]);
+                        __syncwarp();
                     }
-                    mma_commit(&sm.s_full[b]);
+                    const bool v_next = NQ == 2 || j;
+                    slot = ahead(slot, nk + (v_next ? nv : 0));
+                    tile += v_next ? 2 : 1;
                 }
+                if (ok && lead) mma_commit(&sm.q_empty);
                 __syncwarp();
-                if (frees) {
-                    kp.step(nk, slots);
-                    if (NQ == 2 || j) kp.step(nv, slots);
+                if (NQ == 1) {             // the last values stand before the next keys
+                    slot = ahead(slot, nv);
+                    ++tile;
                 }
-                return true;
-            };
-            // O += P V of tile j, step buffer b
-            const auto second = [&](int b, int j) -> bool {
-                const int o = NQ == 2 ? b : 0;
-                if (!wait(&sm.p_ready[b], pr[b])) return false;
-                pr[b] ^= 1;
-                if (j == 0) {
-                    if (!wait(&sm.o_empty[o], oe[o] ^ 1)) return false;
-                    oe[o] ^= 1;
-                }
-                const int live = x.nk - 128 * j, steps = (min(live, 128) + 15) / 16, per = p.v_rows / 16;
-                const bool frees = NQ == 1 || b == 1 || j >= x.tiles[1];
-                if (live < 128 && (NQ == 1 || b == 0 || j >= x.tiles[0])) {  // once a tile
-                    if (!wait(&sm.v_fixed[fixes & 1], fixes >> 1 & 1)) return false;
-                    ++fixes;
-                }
-                if (!landed(vp, nv)) return false;
-                tc_after_sync();
-                if (lead) {
-                    const uint32_t d = tmem + kColO + 128 * o;
-                    uint32_t w = tmem + 128 * b;
-                    Place at = vp;
-                    int left = steps;
-                    for (int i = 0; i < nv; ++i, at.step(1, slots)) {
-                        uint32_t v = dv + (uint32_t)(at.slot * (int)(kSlot >> 4));
-                        for (int e = 0; e < per && left > 0; e += 2, left -= 2, w += 16, v += 2 * (2048 >> 4)) {
-                            mma_f16_ta(d, w, v, id_o, !(j == 0 && i + e == 0));
-                            if (left > 1) mma_f16_ta(d, w + 8, v + (2048 >> 4), id_o, 1);
+            }
+        } else {
+            // ---- O += P V
+            const uint32_t id = idesc(fmt, 0, 1, 128, a.v_dim), dv = desc(ring, (uint32_t)p.v_rows * 128u);
+            const int per = p.v_rows / 16;
+            uint32_t fixes = 0, oe[2] = {0, 0};
+            for (int it = 0; ok && cur.item(p, it, x); ++it) {
+                if (!x.n) continue;
+                const bool two = NQ == 1 && x.n > 1;
+                slot = ahead(two ? ahead(slot, nk) : slot, nk);
+                tile += two ? 2 : 1;
+                for (int j = 0; j < x.n && ok; ++j) {
+                    const int live = x.nk - 128 * j, steps = (min(live, 128) + 15) / 16;
+                    if (live < 128) {
+                        if (!(ok = wait(&sm.v_fixed[fixes & 1], fixes >> 1 & 1))) break;
+                        ++fixes;
+                    }
+                    if (!(ok = wait(&sm.full[tile % kTiles], tile / kTiles & 1))) break;
+#pragma unroll
+                    for (int g = 0; g < NQ; ++g) {
+                        if (j >= x.tiles[g]) continue;
+                        const int b = NQ == 2 ? g : (int)(step++ & 1);
+                        if (!(ok = wait(&sm.p_ready[b], uses[b]))) break;
+                        uses[b] ^= 1;
+                        if (j == 0) {
+                            if (!(ok = wait(&sm.o_empty[g], oe[g] ^ 1))) break;
+                            oe[g] ^= 1;
                         }
-                        if (frees) mma_commit(&sm.empty[at.slot]);
+                        tc_after_sync();
+                        if (lead) {
+                            const uint32_t d = tmem + kColO + 128 * g;
+                            uint32_t w = tmem + 128 * b;
+                            int at = slot;
+#pragma unroll 1
+                            for (int e = 0; e < steps; e += per) {
+                                const uint32_t v = dv + (uint32_t)(at * (int)(kSlot >> 4));
+#pragma unroll 1
+                                for (int f = 0; f < per && e + f < steps; f += 2) {
+                                    mma_f16_ta(d, w, v + f * (2048 >> 4), id, j + e + f != 0);
+                                    if (e + f + 1 < steps) mma_f16_ta(d, w + 8, v + (f + 1) * (2048 >> 4), id, 1);
+                                    w += NQ == 1 && e + f == 2 ? 48 : 16;  // wide: the second half of the weights is at column 64
+                                }
+                                if (++at == slots) at = 0;
+                            }
+                            mma_commit(&sm.pv_done[b]);
+                            if (j + 1 == x.tiles[g]) mma_commit(&sm.o_full[g]);
+                            if (NQ == 1 || g == 1 || j >= x.tiles[1]) mma_commit(&sm.empty[tile % kTiles]);
+                        }
+                        __syncwarp();
                     }
-                    mma_commit(&sm.pv_done[b]);
-                    if (j + 1 == x.tiles[o]) mma_commit(&sm.o_full[o]);
+                    const bool k_next = NQ == 2 || j + 2 < x.n;
+                    // narrow: behind the last values the next item's keys begin
+                    slot = ahead(slot, nv + (k_next && !(NQ == 2 && j + 1 == x.n) ? nk : 0));
+                    tile += k_next && !(NQ == 2 && j + 1 == x.n) ? 2 : 1;
                 }
-                __syncwarp();
-                if (frees) {
-                    vp.step(nv, slots);
-                    if (NQ == 2 || j + 2 < x.n) vp.step(nk, slots);
-                }
-                return true;
-            };
-            int pb = -1, pj = 0;           // the step whose second product is due
-            for (int j = 0; j < x.n && ok; ++j)
-                for (int g = 0; g < NQ && ok; ++g) {
-                    if (j >= x.tiles[g]) continue;
-                    const int b = NQ == 2 ? g : (int)(step++ & 1);
-                    if (NQ == 2 && pb == b) {  // the other stream is done: P of this one stands where S goes
-                        ok = second(pb, pj);
-                        pb = -1;
-                    }
-                    ok = ok && first(b, j);
-                    if (ok && pb >= 0) ok = second(pb, pj);
-                    pb = b;
-                    pj = j;
-                }
-            if (ok && lead) mma_commit(&sm.q_empty);
-            __syncwarp();
-            if (ok && pb >= 0) ok = second(pb, pj);
-            if (NQ == 1) kp = vp;          // behind the last values, where the next item's keys begin
+            }
         }
         if (*abort) {  // what was issued ends before the tensor memory is freed
-            if (lead) mma_commit(&sm.drain);
+            if (lead) mma_commit(&sm.drain[warp - 8]);
             const long long t = clock64();
-            while (!mb_test(&sm.drain, 0) && clock64() - t < kWaitClk) {}
+            while (!mb_test(&sm.drain[warp - 8], 0) && clock64() - t < kWaitClk) {}
         }
         __syncwarp();
     } else {
@@ -413,26 +428,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mb_wait(&sm.s_full[b], sf[b], abort, &g_err);
                 sf[b] ^= 1;
                 tc_after_sync();
-                uint32_t s[kCols / 32][32];
-                const uint32_t at = tmem + quad + 128 * b;
-#pragma unroll
-                for (int c = 0; c < kCols / 32; ++c) tmem_ld(at + (NQ == 2 ? 0 : 64 * g) + 32 * c, s[c]);
-                tmem_wait_ld();
-                if (p.negate) {
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) s[c >> 5][c & 31] ^= 0x80000000u;
-                }
-                const int sees_here = sees - 128 * j - (NQ == 2 ? 0 : 64 * g);  // columns of this thread that count
+                const uint32_t at = tmem + quad + 128 * b + (NQ == 2 ? 0 : 64 * g);  // this thread's columns
+                const int sees_here = sees - 128 * j - (NQ == 2 ? 0 : 64 * g);       // those that count
                 const bool masked = j >= whole;
-                if (masked) {
+                // 64 logits; read twice (tensor memory is fast, and the code stays small)
+                const auto logits = [&](int c0, uint32_t (&s)[2][32]) {
+                    tmem_ld(at + c0, s[0]);
+                    tmem_ld(at + c0 + 32, s[1]);
+                    tmem_wait_ld();
+                    if (p.negate) {
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c)
-                        if (c >= sees_here) s[c >> 5][c & 31] = 0xff800000u;
+                        for (int c = 0; c < 64; ++c) s[c >> 5][c & 31] ^= 0x80000000u;
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (c0 + c >= sees_here) s[c >> 5][c & 31] = 0xff800000u;
+                    }
+                };
+                float top = kFloor;
+#pragma unroll 1
+                for (int c0 = 0; c0 < kCols; c0 += 64) {
+                    uint32_t s[2][32];
+                    logits(c0, s);
+                    float t4[4] = {top, kFloor, kFloor, kFloor};
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) t4[c & 3] = fmaxf(t4[c & 3], __uint_as_float(s[c >> 5][c & 31]));
+                    top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 }
-                float t4[4] = {kFloor, kFloor, kFloor, kFloor};
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) t4[c & 3] = fmaxf(t4[c & 3], __uint_as_float(s[c >> 5][c & 31]));
-                float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 if (NQ == 1) {                         // the row's other half
                     sm.top[step & 1][g][row] = top;
                     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -461,26 +484,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pd[b] ^= 1;
                 const float mf = kOff - m * p.factor;
                 float l2[2] = {0.f, 0.f};
+#pragma unroll 1
+                for (int c0 = 0; c0 < kCols; c0 += 64) {
+                    uint32_t s[2][32];
+                    logits(c0, s);
 #pragma unroll
-                for (int c = 0; c < kCols; c += 2) {
-                    float x0 = ex2(fmaf(__uint_as_float(s[c >> 5][c & 31]), p.factor, mf)), x1 = ex2(fmaf(__uint_as_float(s[c >> 5][(c & 31) + 1]), p.factor, mf));
-                    if (masked) {                      // not by the logit: nothing is known of factor and m
-                        x0 = c < sees_here ? x0 : 0.f;
-                        x1 = c + 1 < sees_here ? x1 : 0.f;
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            float x0 = ex2(fmaf(__uint_as_float(s[h][c]), p.factor, mf)), x1 = ex2(fmaf(__uint_as_float(s[h][c + 1]), p.factor, mf));
+                            if (masked) {              // not by the logit: nothing is known of factor and m
+                                x0 = c0 + 32 * h + c < sees_here ? x0 : 0.f;
+                                x1 = c0 + 32 * h + c + 1 < sees_here ? x1 : 0.f;
+                            }
+                            l2[0] += x0;
+                            l2[1] += x1;
+                            w[c >> 1] = pack_pair(x0, x1, T());
+                        }
+                        tmem_st(at + c0 / 2 + 16 * h, w);  // over logits that were read
                     }
-                    l2[0] += x0;
-                    l2[1] += x1;
-                    s[c >> 6][(c & 63) >> 1] = pack_pair(x0, x1, T());  // pairs behind what is still to be read
                 }
                 l += l2[0] + l2[1];
-#pragma unroll
-                for (int c = 0; c < kCols / 64; ++c) {
-                    uint32_t w[2][16];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) w[k >> 4][k & 15] = s[c][k];
-                    tmem_st(at + (NQ == 2 ? 0 : 32 * g) + 32 * c, w[0]);
-                    tmem_st(at + (NQ == 2 ? 0 : 32 * g) + 32 * c + 16, w[1]);
-                }
                 tmem_wait_st();
                 tc_before_sync();
                 __syncwarp();
@@ -544,7 +569,6 @@ cudaError_t launch(const MoePromptArgs &a, Params &p, int sms, cudaStream_t s) {
     p.v_rows = v_pad == 1 ? 128 : v_pad == 2 ? 64 : 32;
     p.v_slots = 128 / p.v_rows;
     p.slots = (int)((227 * 1024 - 1024 - sizeof(Shared) - 64) / kSlot) - NQ * p.chunks;
-    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
     const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap maps[4] = {};
     const auto map = [&](int i, const void *base, int dim, int rows, int64_t st, int64_t sh, int &heads, int box) {

@@ -114,6 +114,16 @@ def test_many_requests(moe):
     check(out, lse, *a, 0.1, True)
 
 
+@pytest.mark.parametrize("nope,rope,v", [(128, 64, 128), (192, 64, 256), (64, 64, 192)])
+def test_many_work_items_a_block(moe, nope, rope, v):
+    """More (request, queries, head) items than SMs, of one and of several tiles."""
+    a = setup([600, 90, 300, 1, 0, 257], [900, 90, 700, 400, 5, 257], 48, nope, rope, v, torch.bfloat16, seed=nope)
+    for causal in (True, False):
+        out, lse = moe.latent_prompt(*a, 0.07, causal=causal)
+        check(out, lse, *a, 0.07, causal)
+        assert moe.dense_status() == 0
+
+
 def test_rows_of_no_request_stay(moe):
     q, k, kr, v, qs, ks = setup([40, 30], [60, 45], 4, 128, 64, 128, torch.bfloat16, seed=5, spare=20)
     out = torch.full((90, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
