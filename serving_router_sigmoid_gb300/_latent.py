@@ -40,18 +40,44 @@ for _name, _args in {
     getattr(_lib, _name).restype = _ci
 
 
-def _codes(name, t, rows=None):
-    """A matrix of E4M3 codes with contiguous rows -> its shape and row stride."""
-    if t.dtype not in (_E4M3, torch.uint8) or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (
-            rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: expected float8_e4m3fn (or uint8 codes) [{'rows' if rows is None else rows}, dim] with "
-                         f"contiguous rows, got {t.dtype} {tuple(t.shape)}")
-    return t.shape[0], t.shape[1], _st(t, 0)[0]
-
-
 def _st(t, *dims):
     """Strides, 0 where there is nothing to step to."""
-    return [t.stride(d) if t.shape[d] > 1 else 0 for d in dims]
+    shape, stride = t.shape, t.stride()
+    return [stride[d] if shape[d] > 1 else 0 for d in dims]
+
+
+_templates = {}  # (shape, type, device) -> a tensor of that shape over one element
+
+
+def _out(shape, dtype, dev, stream):
+    """A new contiguous tensor that belongs to the stream the call runs on.
+
+    torch.empty_like is the cheapest way to one (2 us next to a launch, torch.empty 3
+    to 4), so shapes that were asked for before stand by as expanded single elements."""
+    if stream is not None:
+        return _empty(shape, None, dtype, dev, stream)
+    like = _templates.get((shape, dtype, dev))
+    if like is None:
+        if torch.cuda.is_current_stream_capturing():  # nothing of a graph's memory stays here
+            return torch.empty(shape, dtype=dtype, device=dev)
+        if len(_templates) >= 256:
+            _templates.clear()
+        like = _templates[shape, dtype, dev] = torch.empty(1, dtype=dtype, device=dev).expand(shape)
+    return torch.empty_like(like)
+
+
+def _rows(name, t, dtypes):
+    """A matrix with contiguous rows -> its shape and row stride (0: one row)."""
+    shape = t.shape
+    if t.dtype in dtypes and len(shape) == 2:
+        rs, cs = t.stride()
+        if cs == 1 or shape[1] <= 1:
+            return shape[0], shape[1], rs if shape[0] > 1 else 0
+    raise ValueError(f"{name}: expected a matrix of {' or '.join(str(d) for d in dtypes)} with contiguous rows, got "
+                     f"{t.dtype} {tuple(shape)}")
+
+
+_CODES = (_E4M3, torch.uint8)
 
 
 def quant_act_fp8(x, x8=None, scale=None, stream=None):
@@ -60,26 +86,20 @@ def quant_act_fp8(x, x8=None, scale=None, stream=None):
     float8_e4m3fn, scale [n, ceil(dim / 128)] float32).  dim is a multiple of 16."""
     dev = x.get_device()
     _here(dev, x, x8, scale)
-    act = _ACT.get(x.dtype)
-    if act is None or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"x: expected float32, float16 or bfloat16 [n, dim] with contiguous rows, got {x.dtype} "
-                         f"{tuple(x.shape)}")
-    n, dim = x.shape
+    n, dim, xs = _rows("x", x, _ACT)
     groups = (dim + 127) // 128
     if x8 is None:
-        x8 = _empty((n, dim), None, _E4M3, dev, stream)
-    elif x8.shape != (n, dim):
-        raise ValueError(f"x8: expected {(n, dim)}, got {tuple(x8.shape)}")
-    row = _codes("x8", x8)[2]
+        x8, row = _out((n, dim), _E4M3, dev, stream), dim
+    else:
+        row = _rows("x8", x8, _CODES)[2]
+        if x8.shape != (n, dim):
+            raise ValueError(f"x8: expected {(n, dim)}, got {tuple(x8.shape)}")
     if scale is None:
-        scale = _empty((n, groups), None, torch.float32, dev, stream)
+        scale = _out((n, groups), torch.float32, dev, stream)
     else:
         _ints("scale", scale, (n, groups), torch.float32)
-    try:
-        _check(_lib.moe_quant_act_fp8(x.data_ptr(), act, *_st(x, 0), n, dim, x8.data_ptr(), row, scale.data_ptr(),
-                                      _raw(stream, dev)))
-    except ctypes.ArgumentError as e:
-        _refuse(e)
+    _check(_lib.moe_quant_act_fp8(x.data_ptr(), _ACT[x.dtype], xs, n, dim, x8.data_ptr(), row, scale.data_ptr(),
+                                  _raw(stream, dev)))
     return x8, scale
 
 
@@ -90,23 +110,24 @@ def fp8_linear(x8, x_scale, w8, scale_inv, out=None, dtype=torch.bfloat16, strea
     out [n, O] of `dtype` (float32, float16 or bfloat16; that of `out` if given)."""
     dev = x8.get_device()
     _here(dev, x8, x_scale, w8, scale_inv, out)
-    n, inner, xs = _codes("x8", x8)
-    outer, w_inner, ws = _codes("w8", w8)
+    n, inner, xs = _rows("x8", x8, _CODES)
+    outer, w_inner, ws = _rows("w8", w8, _CODES)
     if w_inner != inner:
         raise ValueError(f"x8 has rows of {inner}, w8 of {w_inner}")
     blocks = (inner + 127) // 128
     _ints("x_scale", x_scale, (n, blocks), torch.float32)
     _ints("scale_inv", scale_inv, ((outer + 127) // 128, blocks), torch.float32)
     if out is None:
-        out = _empty((n, outer), None, dtype, dev, stream)
-    elif out.shape != (n, outer) or (outer > 1 and out.stride(1) != 1):
-        raise ValueError(f"out: expected {(n, outer)} with contiguous rows, got {tuple(out.shape)}")
-    kind = _ACT.get(out.dtype)
-    if kind is None:
-        raise ValueError(f"out: expected float32, float16 or bfloat16, got {out.dtype}")
+        if dtype not in _ACT:
+            raise ValueError(f"dtype: expected float32, float16 or bfloat16, got {dtype}")
+        out, os = _out((n, outer), dtype, dev, stream), outer
+    else:
+        dtype, os = out.dtype, _rows("out", out, _ACT)[2]
+        if out.shape != (n, outer):
+            raise ValueError(f"out: expected {(n, outer)}, got {tuple(out.shape)}")
     try:
-        args = _LINEAR_ARGS.pack(n, inner, outer, kind, x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(),
-                                 scale_inv.data_ptr(), out.data_ptr(), xs, ws, *_st(out, 0))
+        args = _LINEAR_ARGS.pack(n, inner, outer, _ACT[dtype], x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(),
+                                 scale_inv.data_ptr(), out.data_ptr(), xs, ws, os)
     except _UNPACKABLE as e:
         _refuse(e)
     _check(_lib.moe_fp8_linear(args, _raw(stream, dev)))
@@ -165,11 +186,11 @@ class LatentAttention:
                 not seq_len.is_contiguous():
             raise ValueError(f"seq_len: expected a contiguous int32 tensor of at least {n} entries")
         if out is None:
-            out = _empty((n, heads, self.latent_dim), None, dt, dev, stream)
+            out = _out((n, heads, self.latent_dim), dt, dev, stream)
         elif out.dtype is not dt or out.shape != (n, heads, self.latent_dim) or out.stride(2) != 1:
             raise ValueError(f"out: expected {dt} {(n, heads, self.latent_dim)} with contiguous rows")
         if lse is None:
-            lse = _empty((n, heads), None, torch.float32, dev, stream)
+            lse = _out((n, heads), torch.float32, dev, stream)
         else:
             _ints("lse", lse, (n, heads), torch.float32)
         try:
@@ -204,9 +225,9 @@ def latent_prompt(q, k, k_rope, v, q_start, kv_start, scale, causal=True, out=No
     (nq, heads, dim), (nk, _, nope), v_dim = q.shape, k.shape, v.shape[2]
     rope = 0 if k_rope is None else k_rope.shape[1]
     if out is None:
-        out = _empty((nq, heads, v_dim), None, dt, dev, stream)
+        out = _out((nq, heads, v_dim), dt, dev, stream)
     if lse is None:
-        lse = _empty((nq, heads), None, torch.float32, dev, stream)
+        lse = _out((nq, heads), torch.float32, dev, stream)
     else:
         _ints("lse", lse, (nq, heads), torch.float32)
     for name, t, want in (("q", q, (nq, heads, nope + rope)), ("k", k, (nk, heads, nope)), ("k_rope", k_rope, (nk, rope)),

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(Cfg<TOKM, BN>::kThreads, TOKM ? 1 : 2)
 }
 
 template <bool TOKM, int BN, typename T>
-cudaError_t launch(const MoeFp8LinearArgs &a, Params p, int slots, cudaStream_t s) {
+cudaError_t launch(const MoeFp8LinearArgs &a, Params p, int dev, int slots, cudaStream_t s) {
     using C = Cfg<TOKM, BN>;
     p.tiles_t = (a.n_tokens + (TOKM ? 127 : BN - 1)) / (TOKM ? 128 : BN);
     p.tiles_o = (a.n_out + (TOKM ? BN - 1 : 127)) / (TOKM ? BN : 128);
@@ -327,7 +327,8 @@ cudaError_t launch(const MoeFp8LinearArgs &a, Params p, int slots, cudaStream_t 
     if (e == cudaSuccess) e = encode_map(&mat, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.w8, 2, md, ms, TOKM ? BN : 128);
     if (e != cudaSuccess) return e;
     auto fn = fp8_linear_kernel<TOKM, BN, T>;
-    if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem)) != cudaSuccess) return e;
+    static SmemOnce once;
+    if ((e = once.allow(reinterpret_cast<const void *>(fn), dev, C::kSmem)) != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -344,20 +345,19 @@ cudaError_t launch(const MoeFp8LinearArgs &a, Params p, int slots, cudaStream_t 
 }
 
 template <typename T>
-cudaError_t pick(const MoeFp8LinearArgs &a, const Params &p, int sms, cudaStream_t s) {
-    if (a.n_tokens <= 16) return launch<false, 16, T>(a, p, 2 * sms, s);
-    if (a.n_tokens <= 32) return launch<false, 32, T>(a, p, 2 * sms, s);
-    if (a.n_tokens <= 64) return launch<false, 64, T>(a, p, 2 * sms, s);
+cudaError_t pick(const MoeFp8LinearArgs &a, const Params &p, int dev, int sms, cudaStream_t s) {
+    if (a.n_tokens <= 16) return launch<false, 16, T>(a, p, dev, 2 * sms, s);
+    if (a.n_tokens <= 32) return launch<false, 32, T>(a, p, dev, 2 * sms, s);
+    if (a.n_tokens <= 64) return launch<false, 64, T>(a, p, dev, 2 * sms, s);
     const int64_t wide = (int64_t)((a.n_tokens + 127) / 128) * ((a.n_out + 255) / 256);
-    return wide >= sms ? launch<true, 256, T>(a, p, sms, s) : launch<true, 128, T>(a, p, sms, s);
+    return wide >= sms ? launch<true, 256, T>(a, p, dev, sms, s) : launch<true, 128, T>(a, p, dev, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_linear(const MoeFp8LinearArgs &a, cudaStream_t s) {
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t e = current_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
     Params p = {};
     p.n_tokens = a.n_tokens;
@@ -370,9 +370,9 @@ cudaError_t launch_fp8_linear(const MoeFp8LinearArgs &a, cudaStream_t s) {
     p.out_stride = a.out_stride;
     p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride * (int64_t)dtype_bytes(a.out_type) % 32 == 0;
     switch (a.out_type) {
-        case MOE_F32: return pick<float>(a, p, sms, s);
-        case MOE_F16: return pick<__half>(a, p, sms, s);
-        default: return pick<__nv_bfloat16>(a, p, sms, s);
+        case MOE_F32: return pick<float>(a, p, dev, sms, s);
+        case MOE_F16: return pick<__half>(a, p, dev, sms, s);
+        default: return pick<__nv_bfloat16>(a, p, dev, sms, s);
     }
 }
 

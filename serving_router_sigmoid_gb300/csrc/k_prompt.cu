@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename T, int NQ>
-cudaError_t launch(const MoePromptArgs &a, Params &p, int sms, cudaStream_t s) {
+cudaError_t launch(const MoePromptArgs &a, Params &p, int dev, int sms, cudaStream_t s) {
     const int v_pad = (a.v_dim + 63) / 64;
     p.v_boxes = v_pad;
     p.v_rows = v_pad == 1 ? 128 : v_pad == 2 ? 64 : 32;
@@ -593,7 +593,8 @@ cudaError_t launch(const MoePromptArgs &a, Params &p, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const size_t smem = (size_t)(p.slots + NQ * p.chunks) * kSlot + 1024;
     auto fn = prompt_kernel<T, NQ>;
-    if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    static SmemOnce once;
+    if ((e = once.allow(reinterpret_cast<const void *>(fn), dev, 227 * 1024 - sizeof(Shared) - 64)) != cudaSuccess) return e;
     // no more blocks than there can be items
     const int64_t most = ((int64_t)a.n_queries / (128 * NQ) + a.n_requests) * a.n_heads;
     void *args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
@@ -604,8 +605,7 @@ cudaError_t launch(const MoePromptArgs &a, Params &p, int sms, cudaStream_t s) {
 
 cudaError_t launch_latent_prompt(const MoePromptArgs &a, cudaStream_t s) {
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t e = current_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
     Params p = {};
     p.a = a;
@@ -615,8 +615,8 @@ cudaError_t launch_latent_prompt(const MoePromptArgs &a, cudaStream_t s) {
     p.chunks = p.nope_chunks + (a.rope_dim > 0);
     p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride_t % 16 == 0 && a.out_stride_h % 16 == 0;
     const bool narrow = a.v_dim <= 128 && p.chunks <= 3;
-    if (a.act_type == MOE_F16) return narrow ? launch<__half, 2>(a, p, sms, s) : launch<__half, 1>(a, p, sms, s);
-    return narrow ? launch<__nv_bfloat16, 2>(a, p, sms, s) : launch<__nv_bfloat16, 1>(a, p, sms, s);
+    if (a.act_type == MOE_F16) return narrow ? launch<__half, 2>(a, p, dev, sms, s) : launch<__half, 1>(a, p, dev, sms, s);
+    return narrow ? launch<__nv_bfloat16, 2>(a, p, dev, sms, s) : launch<__nv_bfloat16, 1>(a, p, dev, sms, s);
 }
 
 cudaError_t latent_prompt_flags(int32_t *out) {

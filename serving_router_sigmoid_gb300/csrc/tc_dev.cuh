@@ -10,6 +10,7 @@
 // descriptors is a constant.  A test of a barrier and a fence take some 160.
 #pragma once
 
+#include <atomic>
 #include <cuda.h>
 
 #include "latent_args.cuh"
@@ -179,6 +180,30 @@ __device__ __forceinline__ void st32(void *p, const uint32_t (&v)[8]) {  // 32-b
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+
+// ------------------------------------------------- host: devices, kernels
+constexpr int kDevices = 64;
+
+// The current device and its SMs (asked for once a device).
+inline cudaError_t current_sms(int *dev, int *sms) {
+    static std::atomic<int> known[kDevices];
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return e;
+    if (*dev < kDevices && (*sms = known[*dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+    if (e == cudaSuccess && *dev < kDevices) known[*dev].store(*sms, std::memory_order_relaxed);
+    return e;
+}
+// A kernel's dynamic shared memory, allowed once a device.
+struct SmemOnce {
+    std::atomic<bool> done[kDevices] = {};
+    cudaError_t allow(const void *fn, int dev, size_t bytes) {
+        if (dev < kDevices && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess && dev < kDevices) done[dev].store(true, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 // -------------------------------------------------------------- host: maps
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
