@@ -56,7 +56,7 @@ struct Params {
 };
 
 struct Shared {
-    uint64_t full[kTiles], empty[kTiles], q_full, q_empty, v_fixed[2], s_full[2], p_ready[2], pv_done[2], o_full[2], o_empty[2], drain[2];
+    uint64_t full[kTiles], empty[kTiles], q_full[2], q_empty[2], v_fixed[2], s_full[2], p_ready[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem;
     int abort;
     float top[2][2][128];         // wide heads: the halves' row maxima, by the step's parity
@@ -133,6 +133,32 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// two fp32 operations an instruction, each rounded as by itself
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+    unsigned long long x, y, z, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(z) : "f"(c));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long x, y, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+
 template <typename T, int NQ>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -149,14 +175,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kTiles; ++i) {
             mb_init(&sm.full[i], 1);
-            mb_init(&sm.empty[i], 1);
+            mb_init(&sm.empty[i], NQ);
         }
-        mb_init(&sm.q_full, 1);
-        mb_init(&sm.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mb_init(&sm.v_fixed[i], 1);  // in turn: the copies are an item ahead at most
+            mb_init(&sm.q_full[i], 1);
+            mb_init(&sm.q_empty[i], 1);
             mb_init(&sm.s_full[i], 1);
-            mb_init(&sm.p_ready[i], NQ == 2 ? 4 : 8);
+            for (int h = 0; h < 2; ++h) mb_init(&sm.p_ready[i][h], NQ == 2 ? 4 : 8);
             mb_init(&sm.pv_done[i], 1);
             mb_init(&sm.drain[i], 1);
             mb_init(&sm.o_full[i], 1);
@@ -204,17 +230,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (int it = 0; ok && cur.item(p, it, x); ++it) {
             if (!x.n) continue;
-            ok = __all_sync(0xffffffffu, mb_wait(&sm.q_empty, qp ^ 1, abort, &g_err));
-            qp ^= 1;
-            if (!ok) break;
-            if (lane == 0) {
-                mb_expect_tx(&sm.q_full, (uint32_t)(NQ * p.chunks) * kSlot);
-                for (int g = 0; g < NQ; ++g)
-                    for (int c = 0; c < p.chunks; ++c)
-                        tma_3d(qbase + (uint32_t)(g * p.chunks + c) * kSlot, &qmap, c < p.nope_chunks ? 64 * c : a.nope_dim, x.q0 + 128 * g,
-                               p.q_heads * x.head, &sm.q_full);
-            }
-            __syncwarp();
+            // a stream's queries, once its last product with the last ones is done
+            const auto queries = [&](int g) {
+                ok = __all_sync(0xffffffffu, ok && mb_wait(&sm.q_empty[g], qp ^ 1, abort, &g_err));
+                if (ok && lane == 0) {
+                    mb_expect_tx(&sm.q_full[g], (uint32_t)nk * kSlot);
+                    for (int c = 0; c < nk; ++c)
+                        tma_3d(qbase + (uint32_t)(g * nk + c) * kSlot, &qmap, c < p.nope_chunks ? 64 * c : a.nope_dim, x.q0 + 128 * g,
+                               p.q_heads * x.head, &sm.q_full[g]);
+                }
+                __syncwarp();
+            };
             const auto keys = [&](int j) {
                 take(nk);
                 if (!ok) return;
@@ -261,12 +287,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++put;
             };
+            queries(0);
             for (int j = 0; j < x.n && ok; ++j) {
                 keys(j);
+                if (NQ == 2 && j == 0) queries(1);
+                if (!ok) break;
                 if (NQ == 2) values(j);
                 else if (j) values(j - 1);
             }
             if (NQ == 1 && ok) values(x.n - 1);
+            qp ^= 1;
         }
         if (*abort) {  // copies in flight land before the block ends
             const long long t = clock64();
@@ -275,82 +305,165 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 8) {
         // -------------------------------------------------------------- MMA
-        // One warp issues the first products, another the second ones: an issue takes
-        // 40 to 100 cycles, more than a short MMA.
-        const bool firsts = warp == 8;
+        // Two warps issue (an issue takes 40 to 100 cycles, more than a short MMA), narrow:
+        // one a stream, so that its S follows its PV without a word; wide: one the first
+        // products, the other the second ones.
         const uint32_t fmt = BF ? 1 : 0;
+        const uint32_t id_s = idesc(fmt, 0, 0, 128, 128), id_o = idesc(fmt, 0, 1, 128, a.v_dim);
+        const uint32_t dq = desc(qbase, 16), dk = desc(ring, 16), dv = desc(ring, (uint32_t)p.v_rows * 128u);
+        const int rest = (a.nope_dim % 64) / 16, rope_steps = a.rope_dim / 16, per = p.v_rows / 16, lper = 31 - __clz(per);
         const bool lead = elect();
         const int nk = p.chunks, nv = p.v_slots, slots = p.slots;
         const auto wait = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_wait(bar, phase, abort, &g_err)); };
         const auto ahead = [&](int slot, int n) { return slot + n < slots ? slot + n : slot + n - slots; };
+        // S of the keys at a slot, issued by one lane
+        const auto product_s = [&](uint32_t d, uint32_t q, int at) {
+#pragma unroll 1
+            for (int c = 0; c < nk; ++c, q += kSlot >> 4) {
+                const uint32_t k = dk + (uint32_t)(at * (int)(kSlot >> 4));
+                const int n = c >= p.nope_chunks ? rope_steps : c + 1 == p.nope_chunks && rest ? rest : 4;
+                if (n == 4) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id_s, c + e != 0);
+                } else {
+#pragma unroll 1
+                    for (int e = 0; e < n; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id_s, c + e != 0);
+                }
+                if (++at == slots) at = 0;
+            }
+        };
+        // O += P V for steps [e0, e1) of 16 keys; the second 64 weights stand 64 columns on
+        const auto product_o = [&](uint32_t d, uint32_t w, int at, int e0, int e1, bool starts) {
+            w += e0 < 4 ? 8 * e0 : 64 + 8 * (e0 - 4);
+            at = ahead(at, e0 >> lper);
+            int left = per - (e0 & (per - 1));
+            uint32_t v = dv + (uint32_t)(at * (int)(kSlot >> 4)) + (uint32_t)(e0 & (per - 1)) * (2048 >> 4);
+#pragma unroll 1
+            for (int e = e0; e < e1; e += 2) {      // a slot holds an even number of steps
+                mma_f16_ta(d, w, v, id_o, !(starts && e == 0));
+                if (e + 1 < e1) mma_f16_ta(d, w + 8, v + (2048 >> 4), id_o, 1);
+                w += e == 2 ? 48 : 16;
+                v += 2 * (2048 >> 4);
+                if ((left -= 2) == 0) {
+                    if (++at == slots) at = 0;
+                    v = dv + (uint32_t)(at * (int)(kSlot >> 4));
+                    left = per;
+                }
+            }
+        };
         // Tiles come, narrow: K0 V0 K1 V1 ..., wide: K0 K1 V0 K2 V1 ..., as they are first used.
         int slot = 0;                      // of the next item's first keys
         uint32_t tile = 0;                 // the same as a tile, counted as they come
         uint32_t uses[2] = {0, 0};         // of the S buffers, the last bit
-        uint32_t step = 0;
+        uint32_t step = 0, fixes = 0, qf = 0;
         bool ok = true;
-        if (firsts) {
-            // ---- S = Q K^T
-            const uint32_t id = idesc(fmt, 0, 0, 128, 128), dq = desc(qbase, 16), dk = desc(ring, 16);
-            const int rest = (a.nope_dim % 64) / 16, rope_steps = a.rope_dim / 16;
-            uint32_t qf = 0, began = 0;
+        const bool firsts = warp == 8;
+        if (NQ == 2) {
+            const int g = warp - 8;
+            uint32_t oe = 0, theirs = 0;   // theirs: the parity of the other stream's tiles so far
+            const uint32_t sd = tmem + 128 * g, od = tmem + kColO + 128 * g, q = dq + (uint32_t)(g * nk * (int)(kSlot >> 4));
             for (int it = 0; ok && cur.item(p, it, x); ++it) {
                 if (!x.n) continue;
-                if (!(ok = wait(&sm.q_full, qf))) break;
+                const int mine = x.tiles[g], other = x.tiles[g ^ 1];
+                if (!(ok = wait(&sm.q_full[g], qf))) break;
+                qf ^= 1;
+                // S of tile j, issued by one lane; its keys are free when both streams have read them
+                const auto first = [&](int j) {
+                    const uint32_t t = tile + 2 * j;
+                    product_s(sd, q, slot);
+                    mma_commit(&sm.s_full[g]);
+                    mma_commit(&sm.empty[t % kTiles]);
+                    if (j >= other) mma_commit(&sm.empty[t % kTiles]);
+                    if (j + 1 == mine) mma_commit(&sm.q_empty[g]);
+                };
+                const auto keys = [&](int j) { return wait(&sm.full[(tile + 2 * j) % kTiles], (tile + 2 * j) / kTiles & 1); };
+                // The second stream starts when the first has weights: the products of one then
+                // run under the softmax of the other (in step they cost 97 us where 87 do).
+                if (g == 1 && mine && other) ok = wait(&sm.p_ready[0][0], theirs);
+                theirs ^= other & 1;
+                if (!ok) break;
+                if (mine) {
+                    if (!(ok = keys(0))) break;
+                    tc_after_sync();
+                    if (lead) first(0);
+                    __syncwarp();
+                } else if (lead) mma_commit(&sm.q_empty[g]);
+                for (int j = 0; j < x.n; ++j) {
+                    const int live = x.nk - 128 * j, vs = ahead(slot, nk);
+                    const uint32_t fix = fixes, t = tile + 2 * j + 1;
+                    if (live < 128) ++fixes;
+                    if (ok && j < mine) {
+                        const int steps = (min(live, 128) + 15) / 16;
+                        ok = wait(&sm.full[t % kTiles], t / kTiles & 1) && (live >= 128 || wait(&sm.v_fixed[fix & 1], fix >> 1 & 1)) &&
+                             (j || wait(&sm.o_empty[g], oe ^ 1)) && wait(&sm.p_ready[g][0], uses[0]);
+                        if (!ok) break;
+                        if (!j) oe ^= 1;
+                        tc_after_sync();
+                        if (lead) {
+                            product_o(od, sd, vs, 0, min(steps, 4), j == 0);
+                            mma_commit(&sm.pv_done[g]);
+                        }
+                        __syncwarp();
+                        const bool more = j + 1 < mine;
+                        if (!(ok = wait(&sm.p_ready[g][1], uses[0]))) break;
+                        uses[0] ^= 1;
+                        tc_after_sync();
+                        slot = ahead(slot, nk + nv);
+                        if (lead) {
+                            product_o(od, sd, vs, 4, steps, false);
+                            mma_commit(&sm.empty[t % kTiles]);
+                            if (j >= other) mma_commit(&sm.empty[t % kTiles]);
+                            if (!more) mma_commit(&sm.o_full[g]);
+                        }
+                        __syncwarp();
+                        if (more) {
+                            if (!(ok = keys(j + 1))) break;
+                            tc_after_sync();
+                            if (lead) first(j + 1);
+                            __syncwarp();
+                        }
+                    } else {
+                        slot = ahead(slot, nk + nv);
+                    }
+                }
+                tile += 2 * x.n;
+            }
+        } else
+        if (firsts) {
+            // ---- S = Q K^T
+            uint32_t began = 0;
+            for (int it = 0; ok && cur.item(p, it, x); ++it) {
+                if (!x.n) continue;
+                if (!(ok = wait(&sm.q_full[0], qf))) break;
                 qf ^= 1;
                 for (int j = 0; j < x.n && ok; ++j) {
                     if (!(ok = wait(&sm.full[tile % kTiles], tile / kTiles & 1))) break;
-#pragma unroll
-                    for (int g = 0; g < NQ; ++g) {
-                        if (j >= x.tiles[g]) continue;
-                        const int b = NQ == 2 ? g : (int)(step++ & 1);
-                        // the weights of the step before in this buffer have been read
-                        if (began >> b & 1 && !(ok = wait(&sm.pv_done[b], uses[b] ^ 1))) break;
-                        began |= 1u << b;
-                        uses[b] ^= 1;
-                        tc_after_sync();
-                        if (lead) {
-                            const uint32_t d = tmem + 128 * b;
-                            uint32_t q = dq + (uint32_t)(NQ == 2 && g ? nk * (int)(kSlot >> 4) : 0);
-                            int at = slot;
-#pragma unroll 1
-                            for (int c = 0; c < nk; ++c, q += kSlot >> 4) {
-                                const uint32_t k = dk + (uint32_t)(at * (int)(kSlot >> 4));
-                                const int n = c >= p.nope_chunks ? rope_steps : c + 1 == p.nope_chunks && rest ? rest : 4;
-                                if (n == 4) {
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id, c + e != 0);
-                                } else {
-#pragma unroll 1
-                                    for (int e = 0; e < n; ++e) mma_f16(d, q + 2 * e, k + 2 * e, id, c + e != 0);
-                                }
-                                if (++at == slots) at = 0;
-                            }
-                            mma_commit(&sm.s_full[b]);
-                            // the last stream that sees this tile
-                            if (NQ == 1 || g == 1 || j >= x.tiles[1]) mma_commit(&sm.empty[tile % kTiles]);
-                        }
-                        __syncwarp();
+                    const int b = (int)(step++ & 1);
+                    // the weights of the step before in this buffer have been read
+                    if (began >> b & 1 && !(ok = wait(&sm.pv_done[b], uses[b] ^ 1))) break;
+                    began |= 1u << b;
+                    uses[b] ^= 1;
+                    tc_after_sync();
+                    if (lead) {
+                        product_s(tmem + 128 * b, dq, slot);
+                        mma_commit(&sm.s_full[b]);
+                        mma_commit(&sm.empty[tile % kTiles]);
                     }
-                    const bool v_next = NQ == 2 || j;
-                    slot = ahead(slot, nk + (v_next ? nv : 0));
-                    tile += v_next ? 2 : 1;
+                    __syncwarp();
+                    slot = ahead(slot, nk + (j ? nv : 0));
+                    tile += j ? 2 : 1;
                 }
-                if (ok && lead) mma_commit(&sm.q_empty);
+                if (ok && lead) mma_commit(&sm.q_empty[0]);
                 __syncwarp();
-                if (NQ == 1) {             // the last values stand before the next keys
-                    slot = ahead(slot, nv);
-                    ++tile;
-                }
+                slot = ahead(slot, nv);    // the last values stand before the next keys
+                ++tile;
             }
         } else {
             // ---- O += P V
-            const uint32_t id = idesc(fmt, 0, 1, 128, a.v_dim), dv = desc(ring, (uint32_t)p.v_rows * 128u);
-            const int per = p.v_rows / 16;
-            uint32_t fixes = 0, oe[2] = {0, 0};
+            uint32_t oe = 0;
             for (int it = 0; ok && cur.item(p, it, x); ++it) {
                 if (!x.n) continue;
-                const bool two = NQ == 1 && x.n > 1;
+                const bool two = x.n > 1;
                 slot = ahead(two ? ahead(slot, nk) : slot, nk);
                 tile += two ? 2 : 1;
                 for (int j = 0; j < x.n && ok; ++j) {
@@ -360,42 +473,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++fixes;
                     }
                     if (!(ok = wait(&sm.full[tile % kTiles], tile / kTiles & 1))) break;
-#pragma unroll
-                    for (int g = 0; g < NQ; ++g) {
-                        if (j >= x.tiles[g]) continue;
-                        const int b = NQ == 2 ? g : (int)(step++ & 1);
-                        if (!(ok = wait(&sm.p_ready[b], uses[b]))) break;
-                        uses[b] ^= 1;
-                        if (j == 0) {
-                            if (!(ok = wait(&sm.o_empty[g], oe[g] ^ 1))) break;
-                            oe[g] ^= 1;
-                        }
-                        tc_after_sync();
-                        if (lead) {
-                            const uint32_t d = tmem + kColO + 128 * g;
-                            uint32_t w = tmem + 128 * b;
-                            int at = slot;
-#pragma unroll 1
-                            for (int e = 0; e < steps; e += per) {
-                                const uint32_t v = dv + (uint32_t)(at * (int)(kSlot >> 4));
-#pragma unroll 1
-                                for (int f = 0; f < per && e + f < steps; f += 2) {
-                                    mma_f16_ta(d, w, v + f * (2048 >> 4), id, j + e + f != 0);
-                                    if (e + f + 1 < steps) mma_f16_ta(d, w + 8, v + (f + 1) * (2048 >> 4), id, 1);
-                                    w += NQ == 1 && e + f == 2 ? 48 : 16;  // wide: the second half of the weights is at column 64
-                                }
-                                if (++at == slots) at = 0;
-                            }
-                            mma_commit(&sm.pv_done[b]);
-                            if (j + 1 == x.tiles[g]) mma_commit(&sm.o_full[g]);
-                            if (NQ == 1 || g == 1 || j >= x.tiles[1]) mma_commit(&sm.empty[tile % kTiles]);
-                        }
-                        __syncwarp();
+                    const int b = (int)(step++ & 1);
+                    if (!(ok = (j || wait(&sm.o_empty[0], oe ^ 1)) && wait(&sm.p_ready[b][0], uses[b]))) break;
+                    uses[b] ^= 1;
+                    if (!j) oe ^= 1;
+                    tc_after_sync();
+                    if (lead) {
+                        product_o(tmem + kColO, tmem + 128 * b, slot, 0, steps, j == 0);
+                        mma_commit(&sm.pv_done[b]);
+                        if (j + 1 == x.n) mma_commit(&sm.o_full[0]);
+                        mma_commit(&sm.empty[tile % kTiles]);
                     }
-                    const bool k_next = NQ == 2 || j + 2 < x.n;
-                    // narrow: behind the last values the next item's keys begin
-                    slot = ahead(slot, nv + (k_next && !(NQ == 2 && j + 1 == x.n) ? nk : 0));
-                    tile += k_next && !(NQ == 2 && j + 1 == x.n) ? 2 : 1;
+                    __syncwarp();
+                    slot = ahead(slot, nv + (j + 2 < x.n ? nk : 0));
+                    tile += j + 2 < x.n ? 2 : 1;
                 }
             }
         }
@@ -408,7 +499,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---------------------------------------------------------- softmax
         constexpr float kOff = BF ? 0.f : 7.f;
-        constexpr int kCols = NQ == 2 ? 128 : 64;      // logits of a thread
         const int g = warp >> 2, row = tid & 127;      // stream (narrow) or half of the columns (wide)
         const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
         T *out = static_cast<T *>(a.out);
@@ -423,39 +513,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lead_row = NQ == 2 ? 128 * g + (row & ~31) : (row & ~31);
             const int whole = lead_row + 31 < x.nq ? Cursor<NQ>::seen(a, x, lead_row) / 128 : 0;
             float m = kFloor, l = 0.f;                 // the maximum in units of the logits
-            for (int j = 0; j < tiles; ++j) {
-                const int b = NQ == 2 ? g : (int)(step & 1);
-                mb_wait(&sm.s_full[b], sf[b], abort, &g_err);
-                sf[b] ^= 1;
-                tc_after_sync();
-                const uint32_t at = tmem + quad + 128 * b + (NQ == 2 ? 0 : 64 * g);  // this thread's columns
-                const int sees_here = sees - 128 * j - (NQ == 2 ? 0 : 64 * g);       // those that count
-                const bool masked = j >= whole;
-                // 64 logits; read twice (tensor memory is fast, and the code stays small)
-                const auto logits = [&](int c0, uint32_t (&s)[2][32]) {
-                    tmem_ld(at + c0, s[0]);
-                    tmem_ld(at + c0 + 32, s[1]);
-                    tmem_wait_ld();
-                    if (p.negate) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) s[c >> 5][c & 31] ^= 0x80000000u;
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (c0 + c >= sees_here) s[c >> 5][c & 31] = 0xff800000u;
-                    }
-                };
-                float top = kFloor;
+            // Steps of 64 logits a thread: narrow, the halves of a tile one after the other,
+            // each handed on by itself; wide, this group's half.
+            const int halves = NQ == 2 ? 2 : 1;
 #pragma unroll 1
-                for (int c0 = 0; c0 < kCols; c0 += 64) {
-                    uint32_t s[2][32];
-                    logits(c0, s);
-                    float t4[4] = {top, kFloor, kFloor, kFloor};
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) t4[c & 3] = fmaxf(t4[c & 3], __uint_as_float(s[c >> 5][c & 31]));
-                    top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+            for (int j = 0; j < tiles * halves; ++j) {
+                const int half = NQ == 2 ? j & 1 : g, b = NQ == 2 ? g : (int)(step & 1), ph = NQ == 2 ? half : 0;
+                if (NQ == 1 || !half) {
+                    mb_wait(&sm.s_full[b], sf[b], abort, &g_err);
+                    sf[b] ^= 1;
+                    tc_after_sync();
                 }
+                const uint32_t at = tmem + quad + 128 * b + 64 * half;               // this thread's columns
+                const int tile = NQ == 2 ? j >> 1 : j, sees_here = sees - 128 * tile - 64 * half;  // those that count
+                const bool masked = tile >= whole;
+                uint32_t s[2][32];
+                tmem_ld(at, s[0]);
+                tmem_ld(at + 32, s[1]);
+                tmem_wait_ld();
+                if (p.negate) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) s[c >> 5][c & 31] ^= 0x80000000u;
+                }
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (c >= sees_here) s[c >> 5][c & 31] = 0xff800000u;
+                }
+                float t4[4] = {kFloor, kFloor, kFloor, kFloor};
+#pragma unroll
+                for (int c = 0; c < 64; c += 2)
+                    t4[c >> 1 & 3] = max3(t4[c >> 1 & 3], __uint_as_float(s[c >> 5][c & 31]), __uint_as_float(s[c >> 5][(c & 31) + 1]));
+                float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
                 if (NQ == 1) {                         // the row's other half
                     sm.top[step & 1][g][row] = top;
                     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -467,9 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float to = fmaxf(m, top), f = ex2((m - to) * p.factor);
                     m = to;
                     l *= f;
-                    // O of the tiles before is complete, then its rows are scaled
-                    const int pb = NQ == 2 ? b : b ^ 1;
-                    mb_wait(&sm.pv_done[pb], pd[pb] ^ 1, abort, &g_err);
+                    // O of the steps before is complete, then its rows are scaled
+                    // (narrow: S of this tile came after all of the tile before)
+                    if (NQ == 2 && half) mb_wait(&sm.pv_done[g], pd[0], abort, &g_err);
+                    if (NQ == 1) mb_wait(&sm.pv_done[b ^ 1], pd[b ^ 1] ^ 1, abort, &g_err);
                     tc_after_sync();
                     const int c0 = NQ == 2 ? 0 : 16 * g, c1 = a.v_dim, dc = NQ == 2 ? 16 : 32;
                     for (int c = c0; c < c1; c += dc) {
@@ -481,36 +571,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st(tmem + quad + kColO + 128 * o + c, v);
                     }
                 }
-                pd[b] ^= 1;
+                if (NQ == 1) pd[b] ^= 1;
+                else if (half) pd[0] ^= 1;
                 const float mf = kOff - m * p.factor;
-                float l2[2] = {0.f, 0.f};
-#pragma unroll 1
-                for (int c0 = 0; c0 < kCols; c0 += 64) {
-                    uint32_t s[2][32];
-                    logits(c0, s);
+                float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[16];
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[16];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            float x0 = ex2(fmaf(__uint_as_float(s[h][c]), p.factor, mf)), x1 = ex2(fmaf(__uint_as_float(s[h][c + 1]), p.factor, mf));
-                            if (masked) {              // not by the logit: nothing is known of factor and m
-                                x0 = c0 + 32 * h + c < sees_here ? x0 : 0.f;
-                                x1 = c0 + 32 * h + c + 1 < sees_here ? x1 : 0.f;
-                            }
-                            l2[0] += x0;
-                            l2[1] += x1;
-                            w[c >> 1] = pack_pair(x0, x1, T());
+                    for (int c = 0; c < 32; c += 2) {
+                        float2 e = fma2(make_float2(__uint_as_float(s[h][c]), __uint_as_float(s[h][c + 1])), p.factor, mf);
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        if (masked) {                  // not by the logit: nothing is known of factor and m
+                            e.x = 32 * h + c < sees_here ? e.x : 0.f;
+                            e.y = 32 * h + c + 1 < sees_here ? e.y : 0.f;
                         }
-                        tmem_st(at + c0 / 2 + 16 * h, w);  // over logits that were read
+                        l2 = add2(l2, e);
+                        w[c >> 1] = pack_pair(e.x, e.y, T());
                     }
+                    tmem_st(at + 16 * h, w);           // over logits that were read
                 }
-                l += l2[0] + l2[1];
+                l += l2.x + l2.y;
                 tmem_wait_st();
                 tc_before_sync();
                 __syncwarp();
-                if (lane == 0) mb_arrive(&sm.p_ready[b]);
-                ++step;
+                if (lane == 0) mb_arrive(&sm.p_ready[b][ph]);
+                if (NQ == 1 || half) ++step;
             }
             if (NQ == 1) {                             // the row's whole sum
                 sm.top[step & 1][g][row] = l;
