@@ -96,10 +96,6 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t at) {
     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
     return v;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
 template <bool TOKM, int BN, typename T>
 __global__ void __launch_bounds__(Cfg<TOKM, BN>::kThreads, TOKM ? 1 : 2)
     fp8_linear_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const Params p) {
@@ -146,30 +142,50 @@ __global__ void __launch_bounds__(Cfg<TOKM, BN>::kThreads, TOKM ? 1 : 2)
 
     if (warp == 0) {
         // ------------------------------------------------------------- TMA
-        if (elect()) {
-            Ring r;
-            int issued = 0;
-            for (int i = first; i < n_tiles && !*abort; i += step) {
-                int t0, o0;
-                tile_at(i, t0, o0);
-                const int a0 = TOKM ? t0 : o0, b0 = TOKM ? o0 : t0;
-                for (int k = k0; k < k1; ++k) {
-                    if (!mb_wait(&sm.empty[r.slot], r.phase ^ 1, abort, &g_err)) break;
-                    mb_expect_tx(&sm.full[r.slot], C::kStage);
-                    const uint32_t at = sbase + (uint32_t)r.slot * C::kStage;
-                    tma_2d(at, &amap, k * 128, a0, &sm.full[r.slot]);
-                    tma_2d(at + C::kA, &bmap, k * 128, b0, &sm.full[r.slot]);
-                    ++issued;
-                    r.next(C::kStages);
-                }
+        // A stage is brought by kParts lanes in one instruction, 64 rows of A or what a
+        // box of B holds each; the first stages all together.
+        constexpr int kBoxB = BN < 128 ? BN : 128, kParts = 2 + BN / kBoxB;
+        const auto bring = [&](int part, int slot, int k, int a0, int b0) {
+            const uint32_t at = sbase + (uint32_t)slot * C::kStage;
+            if (part < 2) tma_2d(at + (uint32_t)part * (C::kA / 2), &amap, k * 128, a0 + 64 * part, &sm.full[slot]);
+            else tma_2d(at + C::kA + (uint32_t)(part - 2) * (kBoxB * 128), &bmap, k * 128, b0 + (part - 2) * kBoxB, &sm.full[slot]);
+        };
+        Ring r;
+        int issued = 0;
+        bool ok = true;
+        for (int i = first; i < n_tiles && ok; i += step) {
+            int t0, o0;
+            tile_at(i, t0, o0);
+            const int a0 = TOKM ? t0 : o0, b0 = TOKM ? o0 : t0;
+            int k = k0;
+            if (!issued) {
+                const int n = min(C::kStages, k1 - k0), slot = lane / kParts;
+                static_assert(C::kStages * kParts <= 32, "a lane a part");
+                if (lane < n) mb_expect_tx(&sm.full[lane], C::kStage);
+                __syncwarp();
+                if (slot < n) bring(lane - slot * kParts, slot, k + slot, a0, b0);
+                __syncwarp();
+                issued = n;
+                k += n;
+                r.slot = n - 1;
+                r.next(C::kStages);
             }
-            if (*abort) {  // copies in flight land before the block ends
-                const long long t = clock64();
-                for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
-                    while (!mb_try(&sm.full[i % C::kStages], (uint32_t)((i / C::kStages) & 1)) && clock64() - t < kWaitClk) {}
+            for (; k < k1; ++k) {
+                ok = __all_sync(0xffffffffu, mb_wait(&sm.empty[r.slot], r.phase ^ 1, abort, &g_err));
+                if (!ok) break;
+                if (lane == 0) mb_expect_tx(&sm.full[r.slot], C::kStage);
+                __syncwarp();
+                if (lane < kParts) bring(lane, r.slot, k, a0, b0);
+                __syncwarp();
+                ++issued;
+                r.next(C::kStages);
             }
         }
-        __syncwarp();
+        if (*abort) {  // copies in flight land before the block ends
+            const long long t = clock64();
+            for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+                while (!mb_try(&sm.full[i % C::kStages], (uint32_t)((i / C::kStages) & 1)) && clock64() - t < kWaitClk) {}
+        }
     } else if (warp == 1) {
         // ------------------------------------------------------------- MMA
         const uint32_t id = idesc(0, 0, 0, 128, BN);
@@ -323,8 +339,8 @@ cudaError_t launch(const MoeFp8LinearArgs &a, Params p, int dev, int slots, cuda
     const int64_t td[3] = {a.n_in, a.n_tokens, 1}, md[3] = {a.n_in, a.n_out, 1};
     const int64_t in16 = (a.n_in + 15) / 16 * 16;
     const int64_t ts[2] = {a.n_tokens > 1 ? a.x_stride : in16, 0}, ms[2] = {a.n_out > 1 ? a.w_stride : in16, 0};
-    cudaError_t e = encode_map(&tok, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.x8, 2, td, ts, TOKM ? 128 : BN);
-    if (e == cudaSuccess) e = encode_map(&mat, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.w8, 2, md, ms, TOKM ? BN : 128);
+    cudaError_t e = encode_map(&tok, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.x8, 2, td, ts, TOKM ? 64 : BN);
+    if (e == cudaSuccess) e = encode_map(&mat, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.w8, 2, md, ms, TOKM ? 128 : 64);
     if (e != cudaSuccess) return e;
     auto fn = fp8_linear_kernel<TOKM, BN, T>;
     static SmemOnce once;

@@ -37,7 +37,8 @@ using namespace tc;
 __device__ int32_t g_err;  // flags since the last read
 
 constexpr uint32_t kSlot = 16384;
-constexpr int kTiles = 8;         // tiles of keys or values in flight, at most (a tile has two slots or more)
+constexpr int kTiles = 8;         // narrow: tiles of keys or values in flight, at most
+constexpr int kSlots = 14;        // slots of the ring, at most
 constexpr int kThreads = 352;     // 8 softmax warps, two that issue MMAs, one TMA warp
 constexpr float kLazy = 8.f;
 constexpr float kFloor = -3.4028235e38f;
@@ -56,7 +57,7 @@ struct Params {
 };
 
 struct Shared {
-    uint64_t full[kTiles], empty[kTiles], q_full[2], q_empty[2], v_fixed[2], s_full[2], p_ready[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
+    uint64_t full[kSlots], empty[kSlots], q_full[2], q_empty[2], v_fixed[2], s_full[2], p_ready[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem;
     int abort;
     float top[2][2][128];         // wide heads: the halves' row maxima, by the step's parity
@@ -76,8 +77,9 @@ struct Cursor {
     // the it-th item of this block; the whole warp calls
     __device__ __forceinline__ bool item(const Params &p, int it, Item &x) {
         const MoePromptArgs &a = p.a;
-        const int G = gridDim.x, lane = threadIdx.x & 31;
-        const long long idx = (long long)it * G + (it & 1 ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        constexpr int kRows = 128 * NQ;
+        const int G = gridDim.x, c = blockIdx.x, lane = threadIdx.x & 31;  // wide: pairs of blocks
+        const long long idx = (long long)it * G + (it & 1 ? G - 1 - c : c);
         const long long unit = idx / a.n_heads;
         x.head = (int)(idx - unit * a.n_heads);
         for (; group < a.n_requests; group += 32) {
@@ -87,7 +89,7 @@ struct Cursor {
                 q0 = max(ld_in(a.q_start + b), 0);
                 q1 = min(ld_in(a.q_start + b + 1), a.n_queries);
             }
-            const int blocks = q1 > q0 ? (q1 - q0 + 128 * NQ - 1) / (128 * NQ) : 0;
+            const int blocks = q1 > q0 ? (q1 - q0 + kRows - 1) / kRows : 0;
             int sum = blocks;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -104,14 +106,14 @@ struct Cursor {
                 const int r = group + from;
                 x.k0 = min(max(ld_in(a.kv_start + r), 0), a.n_keys);
                 x.nk = max(min(ld_in(a.kv_start + r + 1), a.n_keys) - x.k0, 0);
-                x.q0 = q0 + (nb - 1 - (at - first)) * 128 * NQ;
+                x.q0 = q0 + (nb - 1 - (at - first)) * kRows;
                 x.last = q1 - x.q0;
-                x.nq = min(x.last, 128 * NQ);
+                x.nq = min(x.last, kRows);
                 x.n = 0;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const int rows = min(max(x.nq - 128 * g, 0), 128);
-                    const int sees = rows && (g < NQ) ? seen(a, x, 128 * g + rows - 1) : 0;
+                    const int sees = rows ? seen(a, x, 128 * g + rows - 1) : 0;
                     x.tiles[g] = (sees + 127) / 128;
                     x.n = max(x.n, x.tiles[g]);
                 }
@@ -124,6 +126,18 @@ struct Cursor {
     // keys that row r of the item sees
     static __device__ __forceinline__ int seen(const MoePromptArgs &a, const Item &x, int r) {
         return a.causal ? max(min(x.nk - (x.last - r) + 1, x.nk), 0) : x.nk;
+    }
+};
+
+// A position in the ring of slots.
+struct Place {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step(int n, int slots) {  // n <= slots
+        if ((slot += n) >= slots) {
+            slot -= slots;
+            phase ^= 1;
+        }
     }
 };
 
@@ -173,9 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort = &sm.abort;
 
     if (tid == 0) {
-        for (int i = 0; i < kTiles; ++i) {
+        for (int i = 0; i < kSlots; ++i) {  // narrow: one a tile, wide: one a slot
             mb_init(&sm.full[i], 1);
-            mb_init(&sm.empty[i], NQ);
+            mb_init(&sm.empty[i], NQ);  // the streams
         }
         for (int i = 0; i < 2; ++i) {
             mb_init(&sm.v_fixed[i], 1);  // in turn: the copies are an item ahead at most
@@ -211,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int slot = 0, room = p.slots;      // next slot, free ones
         uint32_t put = 0, got = 0;         // tiles brought, tiles whose slots are back
         uint32_t sizes = 0;                // of the tiles in flight, 4 bits each, the oldest lowest
+        Place here;                        // wide: the next slot
         uint32_t qp = 0, fixes = 0;
         bool ok = true;
         const auto take = [&](int n) {     // n free slots and a free pair of barriers
@@ -223,67 +238,106 @@ __global__ void __launch_bounds__(kThreads, 1)
             sizes |= (uint32_t)n << (4 * (put - got));
             room -= n;
         };
-        const auto next = [&]() {
-            const int at = slot;
-            if (++slot == p.slots) slot = 0;
-            return ring + (uint32_t)at * kSlot;
-        };
         for (int it = 0; ok && cur.item(p, it, x); ++it) {
             if (!x.n) continue;
             // a stream's queries, once its last product with the last ones is done
             const auto queries = [&](int g) {
                 ok = __all_sync(0xffffffffu, ok && mb_wait(&sm.q_empty[g], qp ^ 1, abort, &g_err));
-                if (ok && lane == 0) {
-                    mb_expect_tx(&sm.q_full[g], (uint32_t)nk * kSlot);
-                    for (int c = 0; c < nk; ++c)
-                        tma_3d(qbase + (uint32_t)(g * nk + c) * kSlot, &qmap, c < p.nope_chunks ? 64 * c : a.nope_dim, x.q0 + 128 * g,
+                if (ok && lane == 0) mb_expect_tx(&sm.q_full[g], (uint32_t)nk * kSlot);
+                __syncwarp();
+                if (ok && lane < nk) {
+                    const int c = lane;
+                    tma_3d(qbase + (uint32_t)(g * nk + c) * kSlot, &qmap, c < p.nope_chunks ? 64 * c : a.nope_dim, x.q0 + 128 * g,
                                p.q_heads * x.head, &sm.q_full[g]);
                 }
                 __syncwarp();
             };
+            const uint32_t box = (uint32_t)p.v_rows * 128u;
+            // rows of V behind the last key, as far as the last step of 16 goes, once they are there
+            const auto clear = [&](int live, int begin) {
+                const int n = (live + 15) / 16 * 16 - live;
+                for (int i = lane; i < n * 8 * p.v_boxes; i += 32) {
+                    const int c = i / (8 * n), r = live + i / 8 % n, part = r / p.v_rows;
+                    const int at = begin + part < p.slots ? begin + part : begin + part - p.slots;
+                    *reinterpret_cast<uint4 *>(dyn + (uint32_t)at * kSlot + (uint32_t)c * box + sw_off(r % p.v_rows, i & 7)) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mb_arrive(&sm.v_fixed[fixes & 1]);
+                ++fixes;
+            };
+            // a slot's part of a tile: chunk c of the keys, or rows of the values
+            const auto bring_k = [&](uint32_t at, int c, int j, uint64_t *full) {
+                const int row = x.k0 + 128 * j;
+                if (c < p.nope_chunks) tma_3d(at, &kmap, 64 * c, row, p.k_heads * x.head, full);
+                else tma_2d(at, &rmap, 0, row, full);
+            };
+            const auto bring_v = [&](uint32_t at, int i, int c, int j, uint64_t *full) {
+                tma_3d(at + (uint32_t)c * box, &vmap, 64 * c, x.k0 + 128 * j + i * p.v_rows, p.v_heads * x.head, full);
+            };
+            // Copies are issued by several lanes at once: a single thread gets 32 to 43
+            // bytes a cycle from the TMA unit, four lanes or two warps 70.
             const auto keys = [&](int j) {
+                if (NQ == 1) {
+                    for (int c = 0; c < nk && ok; c += 2) {  // two slots at a time
+                        const int n = min(2, nk - c);
+                        Place mine = here;
+                        if (lane & 1) mine.step(1, p.slots);
+                        ok = __all_sync(0xffffffffu, lane >= n || mb_wait(&sm.empty[mine.slot], mine.phase ^ 1, abort, &g_err));
+                        if (ok && lane < n) {
+                            mb_expect_tx(&sm.full[mine.slot], kSlot);
+                            bring_k(ring + (uint32_t)mine.slot * kSlot, c + lane, j, &sm.full[mine.slot]);
+                        }
+                        __syncwarp();
+                        here.step(n, p.slots);
+                    }
+                    return;
+                }
                 take(nk);
                 if (!ok) return;
                 uint64_t *const full = &sm.full[put % kTiles];
                 if (lane == 0) mb_expect_tx(full, (uint32_t)nk * kSlot);
-                for (int c = 0; c < nk; ++c) {
-                    const uint32_t at = next();
-                    if (lane) continue;
-                    if (c < p.nope_chunks) tma_3d(at, &kmap, 64 * c, x.k0 + 128 * j, p.k_heads * x.head, full);
-                    else tma_2d(at, &rmap, 0, x.k0 + 128 * j, full);
-                }
                 __syncwarp();
+                const int at = slot + lane < p.slots ? slot + lane : slot + lane - p.slots;
+                if (lane < nk) bring_k(ring + (uint32_t)at * kSlot, lane, j, full);
+                __syncwarp();
+                slot = slot + nk < p.slots ? slot + nk : slot + nk - p.slots;
                 ++put;
             };
             const auto values = [&](int j) {
                 const int live = x.nk - 128 * j;   // rows of this request
-                const uint32_t box = (uint32_t)p.v_rows * 128u;
+                if (NQ == 1) {
+                    const Place begin = here;
+                    for (int i = 0; i < nv && ok; ++i, here.step(1, p.slots)) {
+                        uint64_t *const full = &sm.full[here.slot];
+                        if (!(ok = __all_sync(0xffffffffu, mb_wait(&sm.empty[here.slot], here.phase ^ 1, abort, &g_err)))) return;
+                        if (lane == 0) mb_expect_tx(full, (uint32_t)p.v_boxes * box);
+                        __syncwarp();
+                        if (lane < p.v_boxes) bring_v(ring + (uint32_t)here.slot * kSlot, i, lane, j, full);
+                        __syncwarp();
+                    }
+                    if (live < 128) {
+                        Place at = begin;
+                        for (int i = 0; i < nv && ok; ++i, at.step(1, p.slots))
+                            ok = __all_sync(0xffffffffu, mb_wait(&sm.full[at.slot], at.phase, abort, &g_err));
+                        if (ok) clear(live, begin.slot);
+                    }
+                    return;
+                }
                 take(nv);
                 if (!ok) return;
                 uint64_t *const full = &sm.full[put % kTiles];
-                const int begin = slot;
+                const int begin = slot, i = lane >> 2;  // four lanes a slot
                 if (lane == 0) mb_expect_tx(full, (uint32_t)(nv * p.v_boxes) * box);
-                for (int i = 0; i < nv; ++i) {
-                    const uint32_t at = next();
-                    if (lane) continue;
-                    for (int c = 0; c < p.v_boxes; ++c)
-                        tma_3d(at + (uint32_t)c * box, &vmap, 64 * c, x.k0 + 128 * j + i * p.v_rows, p.v_heads * x.head, full);
-                }
                 __syncwarp();
+                const int at = slot + i < p.slots ? slot + i : slot + i - p.slots;
+                if (i < nv && (lane & 3) < p.v_boxes) bring_v(ring + (uint32_t)at * kSlot, i, lane & 3, j, full);
+                __syncwarp();
+                slot = slot + nv < p.slots ? slot + nv : slot + nv - p.slots;
                 if (live < 128) {
-                    // rows behind the last key, as far as the last step of 16 goes
                     ok = __all_sync(0xffffffffu, mb_wait(full, put / kTiles & 1, abort, &g_err));
-                    const int r0 = live, n = (live + 15) / 16 * 16 - live;
-                    for (int i = lane; i < n * 8 * p.v_boxes; i += 32) {
-                        const int c = i / (8 * n), r = r0 + i / 8 % n, part = r / p.v_rows;
-                        const int at = begin + part < p.slots ? begin + part : begin + part - p.slots;
-                        *reinterpret_cast<uint4 *>(dyn + (uint32_t)at * kSlot + (uint32_t)c * box + sw_off(r % p.v_rows, i & 7)) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mb_arrive(&sm.v_fixed[fixes & 1]);
-                    ++fixes;
+                    if (ok) clear(live, begin);
                 }
                 ++put;
             };
@@ -300,6 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (*abort) {  // copies in flight land before the block ends
             const long long t = clock64();
+            if (NQ == 1)
+                for (int i = 0; i < p.slots; ++i, here.step(1, p.slots))  // the last use of each slot
+                    while (!mb_test(&sm.full[here.slot], here.phase ^ 1) && clock64() - t < kWaitClk) {}
             for (uint32_t i = put > kTiles ? put - kTiles : 0; i < put; ++i)
                 while (!mb_test(&sm.full[i % kTiles], i / kTiles & 1) && clock64() - t < kWaitClk) {}
         }
@@ -317,9 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto wait = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_wait(bar, phase, abort, &g_err)); };
         const auto ahead = [&](int slot, int n) { return slot + n < slots ? slot + n : slot + n - slots; };
         // S of the keys at a slot, issued by one lane
-        const auto product_s = [&](uint32_t d, uint32_t q, int at) {
+        const auto product_s = [&](uint32_t d, uint32_t q, int at, int c0, int c1) {
 #pragma unroll 1
-            for (int c = 0; c < nk; ++c, q += kSlot >> 4) {
+            for (int c = c0; c < c1; ++c, q += kSlot >> 4) {
                 const uint32_t k = dk + (uint32_t)(at * (int)(kSlot >> 4));
                 const int n = c >= p.nope_chunks ? rope_steps : c + 1 == p.nope_chunks && rest ? rest : 4;
                 if (n == 4) {
@@ -370,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // S of tile j, issued by one lane; its keys are free when both streams have read them
                 const auto first = [&](int j) {
                     const uint32_t t = tile + 2 * j;
-                    product_s(sd, q, slot);
+                    product_s(sd, q, slot, 0, nk);
                     mma_commit(&sm.s_full[g]);
                     mma_commit(&sm.empty[t % kTiles]);
                     if (j >= other) mma_commit(&sm.empty[t % kTiles]);
@@ -428,65 +485,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tile += 2 * x.n;
             }
-        } else
-        if (firsts) {
-            // ---- S = Q K^T
+        } else if (firsts) {
+            // ---- S = Q K^T, a slot of keys after the other
+            Place at;
             uint32_t began = 0;
             for (int it = 0; ok && cur.item(p, it, x); ++it) {
                 if (!x.n) continue;
                 if (!(ok = wait(&sm.q_full[0], qf))) break;
                 qf ^= 1;
                 for (int j = 0; j < x.n && ok; ++j) {
-                    if (!(ok = wait(&sm.full[tile % kTiles], tile / kTiles & 1))) break;
                     const int b = (int)(step++ & 1);
                     // the weights of the step before in this buffer have been read
                     if (began >> b & 1 && !(ok = wait(&sm.pv_done[b], uses[b] ^ 1))) break;
                     began |= 1u << b;
                     uses[b] ^= 1;
-                    tc_after_sync();
-                    if (lead) {
-                        product_s(tmem + 128 * b, dq, slot);
-                        mma_commit(&sm.s_full[b]);
-                        mma_commit(&sm.empty[tile % kTiles]);
+                    uint32_t q = dq;
+                    for (int c = 0; c < nk; ++c, q += kSlot >> 4, at.step(1, slots)) {
+                        if (!(ok = wait(&sm.full[at.slot], at.phase))) break;
+                        tc_after_sync();
+                        if (lead) {
+                            product_s(tmem + 128 * b, q, at.slot, c, c + 1);
+                            mma_commit(&sm.empty[at.slot]);
+                            if (c + 1 == nk) mma_commit(&sm.s_full[b]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    slot = ahead(slot, nk + (j ? nv : 0));
-                    tile += j ? 2 : 1;
+                    if (j) at.step(nv, slots);
                 }
                 if (ok && lead) mma_commit(&sm.q_empty[0]);
                 __syncwarp();
-                slot = ahead(slot, nv);    // the last values stand before the next keys
-                ++tile;
+                at.step(nv, slots);        // the last values stand before the next keys
             }
         } else {
             // ---- O += P V
+            Place at;
             uint32_t oe = 0;
             for (int it = 0; ok && cur.item(p, it, x); ++it) {
                 if (!x.n) continue;
-                const bool two = x.n > 1;
-                slot = ahead(two ? ahead(slot, nk) : slot, nk);
-                tile += two ? 2 : 1;
+                at.step(nk, slots);
+                if (x.n > 1) at.step(nk, slots);
                 for (int j = 0; j < x.n && ok; ++j) {
-                    const int live = x.nk - 128 * j, steps = (min(live, 128) + 15) / 16;
+                    const int live = x.nk - 128 * j, steps = (min(live, 128) + 15) / 16, b = (int)(step++ & 1);
                     if (live < 128) {
                         if (!(ok = wait(&sm.v_fixed[fixes & 1], fixes >> 1 & 1))) break;
                         ++fixes;
                     }
-                    if (!(ok = wait(&sm.full[tile % kTiles], tile / kTiles & 1))) break;
-                    const int b = (int)(step++ & 1);
                     if (!(ok = (j || wait(&sm.o_empty[0], oe ^ 1)) && wait(&sm.p_ready[b][0], uses[b]))) break;
                     uses[b] ^= 1;
                     if (!j) oe ^= 1;
-                    tc_after_sync();
-                    if (lead) {
-                        product_o(tmem + kColO, tmem + 128 * b, slot, 0, steps, j == 0);
-                        mma_commit(&sm.pv_done[b]);
-                        if (j + 1 == x.n) mma_commit(&sm.o_full[0]);
-                        mma_commit(&sm.empty[tile % kTiles]);
+                    for (int i = 0; i < nv; ++i, at.step(1, slots)) {
+                        if (!(ok = wait(&sm.full[at.slot], at.phase))) break;
+                        tc_after_sync();
+                        if (lead) {
+                            product_o(tmem + kColO, tmem + 128 * b, ahead(at.slot, slots - i), per * i, min(steps, per * (i + 1)), j == 0);
+                            mma_commit(&sm.empty[at.slot]);
+                            if (i + 1 == nv) {
+                                mma_commit(&sm.pv_done[b]);
+                                if (j + 1 == x.n) mma_commit(&sm.o_full[0]);
+                            }
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    slot = ahead(slot, nv + (j + 2 < x.n ? nk : 0));
-                    tile += j + 2 < x.n ? 2 : 1;
+                    if (j + 2 < x.n) at.step(nk, slots);
                 }
             }
         }
@@ -507,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int it = 0; cur.item(p, it, x); ++it) {
             const int q = NQ == 2 ? 128 * g + row : row;   // of the item
             const bool mine = q < x.nq;
-            const int tiles = x.tiles[o];
+            const int tiles = NQ == 2 ? x.tiles[g] : x.n;
             const int sees = mine ? Cursor<NQ>::seen(a, x, q) : 0;
             // tiles that every row of this warp sees whole need no mask
-            const int lead_row = NQ == 2 ? 128 * g + (row & ~31) : (row & ~31);
+            const int lead_row = q & ~31;
             const int whole = lead_row + 31 < x.nq ? Cursor<NQ>::seen(a, x, lead_row) / 128 : 0;
             float m = kFloor, l = 0.f;                 // the maximum in units of the logits
             // Steps of 64 logits a thread: narrow, the halves of a tile one after the other,
@@ -656,6 +716,7 @@ cudaError_t launch(const MoePromptArgs &a, Params &p, int dev, int sms, cudaStre
     p.v_rows = v_pad == 1 ? 128 : v_pad == 2 ? 64 : 32;
     p.v_slots = 128 / p.v_rows;
     p.slots = (int)((227 * 1024 - 1024 - sizeof(Shared) - 64) / kSlot) - NQ * p.chunks;
+    static_assert((227 * 1024 - 1024 - sizeof(Shared) - 64) / kSlot <= kSlots, "barriers of the ring");
     const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap maps[4] = {};
     const auto map = [&](int i, const void *base, int dim, int rows, int64_t st, int64_t sh, int &heads, int box) {
@@ -665,7 +726,6 @@ cudaError_t launch(const MoePromptArgs &a, Params &p, int dev, int sms, cudaStre
         const int64_t d[3] = {dim, rows, one ? 1 : a.n_heads}, str[2] = {rows > 1 ? 2 * st : row, one ? row : 2 * sh};
         return encode_map(&maps[i], type, 2, base, 3, d, str, box);
     };
-    int unused;
     cudaError_t e = map(0, a.q, a.nope_dim + a.rope_dim, a.n_queries, a.q_stride_t, a.q_stride_h, p.q_heads, 128);
     // without keys nothing is loaded: any valid map will do
     if (e == cudaSuccess) e = a.n_keys ? map(1, a.k, a.nope_dim, a.n_keys, a.k_stride_t, a.k_stride_h, p.k_heads, 128) : (maps[1] = maps[0], cudaSuccess);
@@ -676,7 +736,6 @@ cudaError_t launch(const MoePromptArgs &a, Params &p, int dev, int sms, cudaStre
     } else {
         maps[2] = maps[0];
     }
-    (void)unused;
     if (e != cudaSuccess) return e;
     const size_t smem = (size_t)(p.slots + NQ * p.chunks) * kSlot + 1024;
     auto fn = prompt_kernel<T, NQ>;

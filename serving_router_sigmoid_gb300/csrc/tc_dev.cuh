@@ -104,6 +104,9 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(su32(bar))
                  : "memory");
 }
+// One thread that issues copies of 16 KB one after another gets 32 to 43 bytes a
+// cycle, whatever the map; four lanes of a warp in one instruction, or two warps,
+// get 70 to 80 (measured on all SMs, out of L2).
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -172,6 +175,10 @@ MOE_TC_MMA(mma_f8, "f8f6f4", "x", " mov.b64 x, {%1, %4};\n")
 // The barrier's arrival once all MMAs of this thread so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t *b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(b)) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ stores
