@@ -48,9 +48,9 @@ constexpr int kChunks = 9;            // of 64 dimensions: 512 + 64
 constexpr uint32_t kChunk = kTile * 128;
 constexpr uint32_t kStageB = kChunks * kChunk;
 constexpr int kStages = 2;
-constexpr int kParts = 5;             // of a stage: two chunks, what one step of the second product frees
+constexpr int kParts = 3;             // of a stage: four chunks, which come and are given back together
 constexpr int kProd = 8;              // producer warps
-constexpr int kThreads = 32 * (4 + 1 + kProd);
+constexpr int kThreads = 32 * (4 + 2 + kProd);  // softmax, two that issue MMAs, producers
 constexpr uint32_t kOffQ = 0, kOffK = kStageB, kOffP = kOffK + kStages * kStageB;
 constexpr size_t kSmem = kOffP + kHeads * 128 + 1024;
 constexpr uint32_t kColS = 256;       // tensor memory: O 4 x 64 columns, then S twice
@@ -77,7 +77,7 @@ struct Params {
 __host__ __device__ inline int64_t piece_floats(int latent) { return (int64_t)kHeads * latent + 2 * kHeads; }
 
 struct Shared {
-    uint64_t full[kStages][kParts], empty[kStages][kParts], valid_full[kStages], q_full, q_empty, s_full[2], p_ready, pv_done, o_full, o_empty, drain;
+    uint64_t full[kStages][kParts], empty[kStages][kParts], valid_full[kStages], q_full, q_empty, s_full[2], s_empty[2], p_ready, pv_done, o_full, o_empty, drain[2];
     uint32_t valid[kStages][2];
     uint32_t tmem;
     int abort;
@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             }
             mb_init(&sm.valid_full[i], LOAD == kByTma ? 1 : kProd);
             mb_init(&sm.s_full[i], 1);
+            mb_init(&sm.s_empty[i], 4);
         }
         mb_init(&sm.q_full, 32 * kProd);
         mb_init(&sm.q_empty, 1);
@@ -201,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         mb_init(&sm.pv_done, 1);
         mb_init(&sm.o_full, 1);
         mb_init(&sm.o_empty, 4);
-        mb_init(&sm.drain, 1);
+        mb_init(&sm.drain[0], 1);
+        mb_init(&sm.drain[1], 1);
         sm.abort = 0;
         mb_init_done();
     }
@@ -252,9 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     bool more = w.start(a, sm, lo, hi);
     const int h0 = group * p.per_group, nh = min(p.per_group, p.heads - h0);  // this group's heads
 
-    if (warp >= 5) {
+    if (warp >= 6) {
         // -------------------------------------------------------- producers
-        const int pw = warp - 5, sub = lane & 7;
+        const int pw = warp - 6, sub = lane & 7;
         const int row = 8 * pw + (lane >> 3);                  // and row + 4
         const uint8_t *cache = static_cast<const uint8_t *>(a.cache);
         const int pieces = p.dim / (E4 ? 16 : 8);              // of 16 bytes
@@ -292,12 +294,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             more = w.next(a, opens);
             return x;
         };
-        const int parts = (p.dim + 127) / 128, pieces16 = p.dim / 16;
+        const int parts = (p.dim + 255) / 256, chunks = (p.dim + 63) / 64;
         Next now = fetch(), nxt = fetch();
         Ring r;
         uint32_t q_phase = 0;
-        uint4 code[2][E4 ? kParts : 1];
-        const auto load = [&](const Next &x, int j) {          // codes of a part, 8 pieces of 16 bytes a row
+        constexpr int kCodes = E4 ? (kChunks + 1) / 2 : 1;
+        uint4 code[2][kCodes];
+        const auto load = [&](const Next &x, int j) {          // codes of two chunks, 8 pieces of 16 bytes a row
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 code[i][j] = make_uint4(0, 0, 0, 0);
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         };
         if constexpr (E4)
 #pragma unroll
-            for (int j = 0; j < kParts; ++j) load(now, j);
+            for (int j = 0; j < kCodes; ++j) load(now, j);
         const auto queries = [&](int b) {                      // of another request
             const T *q = static_cast<const T *>(a.q) + b * a.q_stride_b;
             const int qp = p.dim / 8;
@@ -322,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             }
             cp_arrive(&sm.q_full);
         };
-        const auto copy_part = [&](uint32_t at, int j) {       // this thread's pieces of two chunks
+        const auto copy_part = [&](uint32_t at, int j) {       // this thread's pieces of a part
 #pragma unroll
-            for (int c = 2 * j; c < 2 * j + 2; ++c)
+            for (int c = 4 * j; c < 4 * j + 4; ++c)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (8 * c + sub < pieces)
@@ -359,15 +362,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                         for (int g = 0; g < groups; ++g)
                             if ((uint32_t)__shfl_sync(0xffffffffu, now.page, g) < p.n_pages) lives |= 1u << g;
                         for (int k = 0; k < parts; ++k) {
-                            const int j = part_of(k), chunks = 8 * j + 4 < pieces16 ? 2 : 1;
+                            const int j = part_of(k), n = min(4, chunks - 4 * j);
                             ok = __all_sync(0xffffffffu, mb_wait(&sm.empty[r.slot][j], r.phase ^ 1, abort, &g_err) && ok);
                             if (!ok) continue;
-                            // lane: a group of rows of a chunk; a page that is none reads as zeros
-                            const int g = lane & (groups - 1), c = 2 * j + lane / groups;
+                            // lane: a group of rows of a chunk, 32 of them at most; a page that is none reads as zeros
+                            const int g = lane & (groups - 1), c = 4 * j + lane / groups;
                             const int id = __shfl_sync(0xffffffffu, now.page, g), off = __shfl_sync(0xffffffffu, now.off, g);
-                            if (lane == 0) mb_expect_tx(&sm.full[r.slot][j], (uint32_t)chunks * kChunk);
+                            if (lane == 0) mb_expect_tx(&sm.full[r.slot][j], (uint32_t)n * kChunk);
                             __syncwarp();
-                            if (lane < chunks * groups)
+                            if (lane < n * groups)
                                 tma_3d(sbase + at + (uint32_t)c * kChunk + (uint32_t)(g << gshift) * 128u, &cmap, 64 * c,
                                        lives >> g & 1 ? off : 0, lives >> g & 1 ? id : (int)p.n_pages, &sm.full[r.slot][j]);
                             __syncwarp();
@@ -413,16 +416,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                     if (j >= parts) continue;
                     ok = __all_sync(0xffffffffu, ok && mb_wait(&sm.empty[r.slot][j], r.phase ^ 1, abort, &g_err));
                     if constexpr (E4) {
-                        uint8_t *tile = dyn + at + (uint32_t)(2 * j + (sub >> 2)) * kChunk;
-                        if (8 * j + sub < pieces)
+                        // lanes of both chunks store to different banks: the upper ones their second 8 codes first
+                        const bool f = sub >> 2;
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                // lanes of both chunks store to different banks
-                                const uint4 lo8 = widen8<BF>(code[i][j].x, code[i][j].y), hi8 = widen8<BF>(code[i][j].z, code[i][j].w);
-                                const int c = 2 * (sub & 3), f = sub >> 2;
-                                *reinterpret_cast<uint4 *>(tile + sw_off(row + 4 * i, c + f)) = f ? hi8 : lo8;
-                                *reinterpret_cast<uint4 *>(tile + sw_off(row + 4 * i, c + (f ^ 1))) = f ? lo8 : hi8;
-                            }
+                        for (int h = 2 * j; h < 2 * j + 2 && h < kCodes; ++h) {
+                            uint8_t *tile = dyn + at + (uint32_t)(2 * h + (sub >> 2)) * kChunk;
+                            if (8 * h + sub < pieces)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const uint4 w = code[i][h];
+                                    const int c = 2 * (sub & 3);
+                                    *reinterpret_cast<uint4 *>(tile + sw_off(row + 4 * i, c + f)) = widen8<BF>(f ? w.z : w.x, f ? w.w : w.y);
+                                    *reinterpret_cast<uint4 *>(tile + sw_off(row + 4 * i, c + !f)) = widen8<BF>(f ? w.x : w.z, f ? w.y : w.w);
+                                }
+                        }
                     } else {
                         copy_part(at, j);
                         cp_arrive(&sm.full[r.slot][j]);
@@ -434,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                     __syncwarp();
                     if (lane < parts) mb_arrive(&sm.full[r.slot][lane]);
 #pragma unroll
-                    for (int j = 0; j < kParts; ++j) load(nxt, j);
+                    for (int j = 0; j < kCodes; ++j) load(nxt, j);
                 }
                 seen();  // read by the softmax before the second product, which frees the stage
                 if (lane == 0) mb_arrive(&sm.valid_full[r.slot]);
@@ -442,104 +449,87 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 4) {
+    } else if (warp >= 4) {
         // -------------------------------------------------------------- MMA
+        // One warp issues S, the other O, each as soon as what it needs is there.
         const uint32_t fmt = BF ? 1 : 0;
         const uint32_t id_s = idesc(fmt, 0, 0, 64, kTile), id_o = idesc(fmt, 1, 0, 128, p.n);
         const uint32_t dq = desc(sbase + kOffQ, 16), dk = desc(sbase + kOffK, 16);
         const uint32_t dv = desc(sbase + kOffK, kChunk), dp = desc(sbase + kOffP, 16);
-        const int steps = p.dim / 16, parts = (steps + 7) / 8, mts = (p.latent + 127) / 128;
+        const int steps = p.dim / 16, parts = (steps + 15) / 16, mts = (p.latent + 127) / 128, own = (mts + 1) / 2;  // own: parts that O reads
         const bool lead = elect();
-        Ring r, ro;                       // stages of the tiles whose S, whose O comes next
-        uint32_t qf = 0, pr = 0, oe = 0, i = 0;
-        bool first = true, ok = more;
-        bool pend = false, pend_first = false, pend_last = false;
-        const auto ready = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_test(bar, phase)); };
         const auto wait = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_wait(bar, phase, abort, &g_err)); };
-        const auto second = [&]() -> bool {  // O += V^T P^T of the pending tile, whose weights are there
-            pr ^= 1;
-            if (pend_first) {
-                if (!wait(&sm.o_empty, oe ^ 1)) return false;
-                oe ^= 1;
-            }
-            tc_after_sync();
-            if (lead) {
-                const uint32_t v = dv + (uint32_t)(ro.slot * (int)(kStageB >> 4));
-                for (int m = 0; m < mts; ++m) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16(tmem + 64 * m, v + (uint32_t)(m * (int)(2 * kChunk >> 4) + k * (2048 >> 4)), dp + 2 * k, id_o,
-                                !(pend_first && k == 0));
-                    mma_commit(&sm.empty[ro.slot][m]);
+        Ring r;
+        uint32_t i = 0, flip = 0;
+        bool first = true, ok = true;
+        if (warp == 4) {
+            // ---- S = Q K^T
+            uint32_t qf = 0;
+            while (ok && more) {
+                if (first) {
+                    if (!(ok = wait(&sm.q_full, qf))) break;
+                    qf ^= 1;
+                    fence_async_smem();  // copied by the generic proxy
                 }
-                mma_commit(&sm.pv_done);
-                if (pend_last) mma_commit(&sm.o_full);
-            }
-            __syncwarp();
-            ro.next(kStages);
-            pend = false;
-            return true;
-        };
-        while (ok && more) {
-            if (first) {  // the last request ends before the queries of the next are there
-                if (pend) ok = wait(&sm.p_ready, pr) && second();
-                if (!(ok = ok && wait(&sm.q_full, qf))) break;
-                qf ^= 1;
-                fence_async_smem();  // copied by the generic proxy
-            }
-            const bool last = w.t + 1 == w.te;
-            const uint32_t k = dk + (uint32_t)(r.slot * (int)(kStageB >> 4));
-            const uint32_t d = tmem + kColS + (i & 1) * kTile;
-            // until the tile is there: the second product of the one before, if its weights are
-            const auto whole = [&]() {
-                bool all = true;
+                const bool last = w.t + 1 == w.te;
+                for (int j = 0; j < parts && ok; ++j) ok = wait(&sm.full[r.slot][j], r.phase);
+                // the buffer of the tile before the last: its logits are read
+                if (ok && i >= 2) ok = wait(&sm.s_empty[i & 1], (i >> 1 & 1) ^ 1);
+                if (!ok) break;
+                if (LOAD == kByRow) fence_async_smem();  // the copies landed by the generic proxy
+                tc_after_sync();
+                if (lead) {
+                    const uint32_t k = dk + (uint32_t)(r.slot * (int)(kStageB >> 4)), d = tmem + kColS + (i & 1) * kTile;
+                    for (int c = 0; c < steps / 4; ++c)
 #pragma unroll
-                for (int x = 0; x < kParts; ++x)
-                    if (x < parts) all = mb_test(&sm.full[r.slot][x], r.phase) && all;
-                return __all_sync(0xffffffffu, all);
-            };
-            long long t0 = 0;
-            while (ok && !whole()) {
-                if (pend && ready(&sm.p_ready, pr)) ok = second();
-                else if (*abort) ok = false;
-                else if (!t0) t0 = clock64();
-                else if (clock64() - t0 > kWaitClk) {
-                    *abort = 1;
-                    atomicOr(&g_err, kErrSyncTimeout);
+                        for (int e = 0; e < 4; ++e)
+                            mma_f16(d, dq + (uint32_t)(c * (int)(kChunk >> 4) + 2 * e), k + (uint32_t)(c * (int)(kChunk >> 4) + 2 * e), id_s,
+                                    c + e != 0);
+                    for (int e = 0; e < steps % 4; ++e)
+                        mma_f16(d, dq + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * e),
+                                k + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * e), id_s, steps >= 4 || e != 0);
+                    mma_commit(&sm.s_full[i & 1]);
+                    for (int e = own; e < parts; ++e) mma_commit(&sm.empty[r.slot][e]);
+                    if (last) mma_commit(&sm.q_empty);
                 }
-                ok = __all_sync(0xffffffffu, ok);
+                __syncwarp();
+                r.next(kStages);
+                ++i;
+                more = w.next(a, first);
             }
-            if (!ok) break;
-            if (LOAD == kByRow) fence_async_smem();  // the copies landed by the generic proxy
-            tc_after_sync();
-            if (lead) {
-                for (int c = 0; c < steps / 4; ++c)
+        } else {
+            // ---- O += V^T P^T
+            uint32_t oe = 0;
+            while (ok && more) {
+                const bool last = w.t + 1 == w.te;
+                if (first) {
+                    if (!(ok = wait(&sm.o_empty, oe ^ 1))) break;
+                    oe ^= 1;
+                }
+                if (!(ok = wait(&sm.p_ready, flip))) break;
+                flip ^= 1;
+                tc_after_sync();
+                if (lead) {
+                    const uint32_t v = dv + (uint32_t)(r.slot * (int)(kStageB >> 4));
+                    for (int m = 0; m < mts; ++m) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_f16(d, dq + (uint32_t)(c * (int)(kChunk >> 4) + 2 * j), k + (uint32_t)(c * (int)(kChunk >> 4) + 2 * j), id_s,
-                                c + j != 0);
-                for (int j = 0; j < steps % 4; ++j)
-                    mma_f16(d, dq + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * j),
-                            k + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * j), id_s, 1);
-                mma_commit(&sm.s_full[i & 1]);
-                if (last) mma_commit(&sm.q_empty);
-                for (int e = mts; e < parts; ++e) mma_commit(&sm.empty[r.slot][e]);
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16(tmem + 64 * m, v + (uint32_t)(m * (int)(2 * kChunk >> 4) + k * (2048 >> 4)), dp + 2 * k, id_o,
+                                    !(first && k == 0));
+                        if (m & 1 || m + 1 == mts) mma_commit(&sm.empty[r.slot][m >> 1]);
+                    }
+                    mma_commit(&sm.pv_done);
+                    if (last) mma_commit(&sm.o_full);
+                }
+                __syncwarp();
+                r.next(kStages);
+                more = w.next(a, first);
             }
-            __syncwarp();
-            if (!ok) break;
-            r.next(kStages);
-            ++i;
-            if (pend) ok = wait(&sm.p_ready, pr) && second();
-            pend = true;
-            pend_first = first;
-            pend_last = last;
-            more = w.next(a, first);
         }
-        if (ok && pend) ok = wait(&sm.p_ready, pr) && second();
         if (*abort) {  // what was issued ends before the tensor memory is freed
-            if (lead) mma_commit(&sm.drain);
+            if (lead) mma_commit(&sm.drain[warp - 4]);
             const long long t = clock64();
-            while (!mb_try(&sm.drain, 0) && clock64() - t < kWaitClk) {}
+            while (!mb_try(&sm.drain[warp - 4], 0) && clock64() - t < kWaitClk) {}
         }
         __syncwarp();
     } else {
@@ -578,6 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             tmem_ld_rows(tmem + quad + kColS + (i & 1) * kTile, v);
             const uint32_t seen[2] = {*(volatile uint32_t *)&sm.valid[r.slot][0], *(volatile uint32_t *)&sm.valid[r.slot][1]};
             tmem_wait_ld();
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) mb_arrive(&sm.s_empty[i & 1]);
             float top[2] = {kFloor, kFloor};
             const bool whole = (seen[0] & seen[1]) == 0xffffffffu;
 #pragma unroll
