@@ -40,12 +40,6 @@ for _name, _args in {
     getattr(_lib, _name).restype = _ci
 
 
-def _st(t, *dims):
-    """Strides, 0 where there is nothing to step to."""
-    shape, stride = t.shape, t.stride()
-    return [stride[d] if shape[d] > 1 else 0 for d in dims]
-
-
 _templates = {}  # (shape, type, device) -> a tensor of that shape over one element
 
 
@@ -176,28 +170,33 @@ class LatentAttention:
         if act is None or shape != (n, heads, dim) or q.stride(2) != 1:
             raise ValueError(f"q: expected float16 or bfloat16 [n, {heads}, {dim}] with contiguous rows, got {dt} "
                              f"{tuple(shape)}")
-        cs, ct = cache.shape, cache.stride()
-        if cache.dtype not in (dt, _E4M3) or len(cs) not in (3, 4) or cs[-1] != dim or ct[-1] != 1 or (
+        cs, ct, qt, cd = cache.shape, cache.stride(), q.stride(), cache.dtype
+        if (cd is not dt and cd is not _E4M3) or len(cs) not in (3, 4) or cs[-1] != dim or ct[-1] != 1 or (
                 len(cs) == 4 and cs[2] != 1):
             raise ValueError(f"cache: expected {dt} or float8_e4m3fn [pages, page_size, 1, {dim}] with contiguous rows, got "
-                             f"{cache.dtype} {tuple(cs)}")
+                             f"{cd} {tuple(cs)}")
         cols, row = _table(block_table, n)
         if seq_len.dtype is not torch.int32 or seq_len.dim() != 1 or seq_len.shape[0] < n or \
                 not seq_len.is_contiguous():
             raise ValueError(f"seq_len: expected a contiguous int32 tensor of at least {n} entries")
+        latent = self.latent_dim
         if out is None:
-            out = _out((n, heads, self.latent_dim), dt, dev, stream)
-        elif out.dtype is not dt or out.shape != (n, heads, self.latent_dim) or out.stride(2) != 1:
-            raise ValueError(f"out: expected {dt} {(n, heads, self.latent_dim)} with contiguous rows")
+            out, os = _out((n, heads, latent), dt, dev, stream), (heads * latent, latent)
+        elif out.dtype is not dt or out.shape != (n, heads, latent) or out.stride(2) != 1:
+            raise ValueError(f"out: expected {dt} {(n, heads, latent)} with contiguous rows")
+        else:
+            os = out.stride()
         if lse is None:
             lse = _out((n, heads), torch.float32, dev, stream)
         else:
             _ints("lse", lse, (n, heads), torch.float32)
+        many, many_h = n > 1, heads > 1  # a stride counts where there is something to step to
         try:
             args = _LATENT_ARGS.pack(
-                n, act, act if cache.dtype is dt else MOE_E4M3, cs[1], cols, scale, k_scale, seq_len.data_ptr(),
+                n, act, act if cd is dt else MOE_E4M3, cs[1], cols, scale, k_scale, seq_len.data_ptr(),
                 block_table.data_ptr(), row, cs[0], q.data_ptr(), cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                *_st(q, 0, 1), *_st(out, 0, 1), *_st(cache, 0, 1))
+                qt[0] * many, qt[1] * many_h, os[0] * many, os[1] * many_h, ct[0] if cs[0] > 1 else 0,
+                ct[1] if cs[1] > 1 else 0)
         except _UNPACKABLE as e:
             _refuse(e)
         _check(_lib.moe_latent_decode(self.handle, args, _raw(stream, dev)))
@@ -218,31 +217,42 @@ def latent_prompt(q, k, k_rope, v, q_start, kv_start, scale, causal=True, out=No
     the last request are left as they were, a query that sees no key gets 0 and -inf."""
     dev = q.get_device()
     _here(dev, q, k, k_rope, v, q_start, kv_start, out, lse)
-    dt, act = q.dtype, _HALF.get(q.dtype)
-    if act is None or q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or (k_rope is not None and k_rope.dim() != 2):
-        raise ValueError(f"expected float16 or bfloat16 q, k and v [tokens, heads, dim] and k_rope [tokens, dim], got {dt} "
-                         f"{[None if t is None else tuple(t.shape) for t in (q, k, k_rope, v)]}")
-    (nq, heads, dim), (nk, _, nope), v_dim = q.shape, k.shape, v.shape[2]
-    rope = 0 if k_rope is None else k_rope.shape[1]
+    dt, qs, ks, vs = q.dtype, q.shape, k.shape, v.shape
+    act = _HALF.get(dt)
+    rs = None if k_rope is None else k_rope.shape
+    rope = rs[1] if rs is not None and len(rs) == 2 else 0
+    if act is None or len(qs) != 3 or len(ks) != 3 or len(vs) != 3 or k.dtype is not dt or v.dtype is not dt or \
+            ks[1] != qs[1] or vs[1] != qs[1] or vs[0] != ks[0] or qs[2] != ks[2] + rope or \
+            (rs is not None and (len(rs) != 2 or rs[0] != ks[0] or k_rope.dtype is not dt)):
+        raise ValueError("expected float16 or bfloat16 q [queries, heads, nope + rope], k [keys, heads, nope], k_rope [keys, rope] "
+                         f"and v [keys, heads, v_dim] of one type, got "
+                         f"{[None if t is None else (t.dtype, tuple(t.shape)) for t in (q, k, k_rope, v)]}")
+    nq, heads, _ = qs
+    nk, _, nope = ks
+    v_dim = vs[2]
     if out is None:
-        out = _out((nq, heads, v_dim), dt, dev, stream)
+        out, os = _out((nq, heads, v_dim), dt, dev, stream), (heads * v_dim, v_dim, 1)
+    elif out.dtype is not dt or out.shape != (nq, heads, v_dim):
+        raise ValueError(f"out: expected {dt} {(nq, heads, v_dim)}, got {out.dtype} {tuple(out.shape)}")
+    else:
+        os = out.stride()
     if lse is None:
         lse = _out((nq, heads), torch.float32, dev, stream)
     else:
         _ints("lse", lse, (nq, heads), torch.float32)
-    for name, t, want in (("q", q, (nq, heads, nope + rope)), ("k", k, (nk, heads, nope)), ("k_rope", k_rope, (nk, rope)),
-                          ("v", v, (nk, heads, v_dim)), ("out", out, (nq, heads, v_dim))):
-        if t is not None and (t.dtype is not dt or t.shape != want or (want[-1] > 1 and t.stride(-1) != 1)):
-            raise ValueError(f"{name}: expected {dt} {want} with contiguous rows, got {t.dtype} {tuple(t.shape)}")
-    n = q_start.shape[0] - 1 if q_start.dim() == 1 else -1
-    _ints("q_start", q_start, (max(n, 0) + 1,))
-    _ints("kv_start", kv_start, (max(n, 0) + 1,))
+    qt, kt, vt, rt = q.stride(), k.stride(), v.stride(), (0, 1) if rs is None else k_rope.stride()
+    if qt[2] != 1 or kt[2] != 1 or vt[2] != 1 or rt[1] != 1 or os[2] != 1:
+        raise ValueError("expected q, k, k_rope, v and out with contiguous rows")
+    n = q_start.shape[0] - 1 if q_start.dim() == 1 else 0
+    _ints("q_start", q_start, (n + 1,))
+    _ints("kv_start", kv_start, (n + 1,))
+    many_q, many_k, many_h = nq > 1, nk > 1, heads > 1  # a stride counts where there is something to step to
     try:
         args = _PROMPT_ARGS.pack(
             n, heads, nq, nk, nope, rope, v_dim, act, bool(causal), scale, q_start.data_ptr(), kv_start.data_ptr(),
-            q.data_ptr(), k.data_ptr(), 0 if k_rope is None else k_rope.data_ptr(), v.data_ptr(), out.data_ptr(),
-            lse.data_ptr(), *_st(q, 0, 1), *_st(k, 0, 1), *((0,) if k_rope is None else _st(k_rope, 0)), *_st(v, 0, 1),
-            *_st(out, 0, 1))
+            q.data_ptr(), k.data_ptr(), 0 if rs is None else k_rope.data_ptr(), v.data_ptr(), out.data_ptr(),
+            lse.data_ptr(), qt[0] * many_q, qt[1] * many_h, kt[0] * many_k, kt[1] * many_h, rt[0] * many_k, vt[0] * many_k,
+            vt[1] * many_h, os[0] * many_q, os[1] * many_h)
     except _UNPACKABLE as e:
         _refuse(e)
     _check(_lib.moe_latent_prompt(args, _raw(stream, dev)))

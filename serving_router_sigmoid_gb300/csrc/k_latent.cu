@@ -71,7 +71,7 @@ struct Params {
     int64_t c_page, c_tok;            // bytes
     uint32_t n_pages;
     float *part;                      // [2 * blocks] pieces
-    int4 *rec;                        // [blocks]: the request that begins and does not end in the block's run
+    int4 *rec;                        // [requests * groups]: first and last run of a request that several hold, else x < 0
 };
 
 __host__ __device__ inline int64_t piece_floats(int latent) { return (int64_t)kHeads * latent + 2 * kHeads; }
@@ -548,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                     from_f32(0.f, out[b * a.out_stride_b + (h0 + h) * a.out_stride_h + d]);
                 if (a.lse && tid == 0) a.lse[(int64_t)b * p.heads + h0 + h] = -INFINITY;
             }
+            if (tid == 0) p.rec[(int64_t)b * p.groups + group].x = -1;
         }
-        if (tid == 0) p.rec[blockIdx.x].x = -1;
 
         Ring r;
         uint32_t i = 0, pv = 0, of = 0;
@@ -645,6 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                 }
                 mb_wait(&sm.o_full, of, abort, &g_err);
                 of ^= 1;
+                // the runs that hold tiles of it: this one to the one of its last tile (the first writes)
+                if (from0 && tid == 0)
+                    p.rec[(int64_t)b * p.groups + group] =
+                        make_int4(ends ? -1 : run, (int)(((int64_t)(s + kSegCost + tiles) * p.runs - 1) / total), total, 0);
                 if (from0 && ends) {
                     if ((lane & 3) == 0)
 #pragma unroll
@@ -694,11 +698,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                             piece[(int64_t)kHeads * p.latent + hr + 8 * k] = m[k];
                             piece[(int64_t)kHeads * p.latent + kHeads + hr + 8 * k] = l[k];
                         }
-                    if (from0 && tid == 0) {
-                        // the runs that hold tiles of it: this one to the one of its last tile
-                        const int64_t end = s + kSegCost + tiles;
-                        p.rec[blockIdx.x] = make_int4(b, run, (int)((end * p.runs - 1) / total), total);
-                    }
                     tc_after_sync();
                     for (int c = 0; c < (p.latent + 127) / 128 * 64; c += 16) {
                         if ((c & 63) >= p.n) continue;
@@ -730,35 +729,24 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 }
 
 // Joins the pieces of the requests that several runs share.  A block takes 32
-// latent dimensions of the k-th such request of a head group, a lane one of them
-// for 8 heads (32 contiguous bytes a piece); its 8 warps take 8 heads each, or
-// (many: few requests over many runs) a part of the runs for the same 8 heads.
+// latent dimensions of a request and head group (or all of them in turn, where
+// requests outnumber the runs and few are shared), a lane one of them for 8 heads
+// (32 contiguous bytes a piece); its 8 warps take 8 heads each, or (many: few
+// requests over many runs) a part of the runs for the same 8 heads.
 constexpr int kMaxRuns = 152;
 template <typename T>
 __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ Params p, int many) {
     after_previous();
     __shared__ __align__(16) float wt[8][kMaxRuns][8];
     __shared__ float sums[8][8][32];
-    __shared__ int4 rec;
     const MoeLatentArgs &a = p.a;
-    const int group = blockIdx.x % p.groups, k = blockIdx.x / p.groups, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) rec.x = -1;
-    __syncthreads();
-    if (warp == 0) {  // the k-th request that begins in a run and ends in another
-        int seen = 0;
-        for (int r = 0; r < p.runs; r += 32) {
-            const int4 x = r + lane < p.runs ? p.rec[(r + lane) * p.groups + group] : make_int4(-1, 0, 0, 0);
-            const uint32_t has = __ballot_sync(0xffffffffu, x.x >= 0);
-            if (x.x >= 0 && seen + __popc(has & ((1u << lane) - 1)) == k) rec = x;
-            seen += __popc(has);
-        }
-    }
-    __syncthreads();
+    const int group = blockIdx.x % p.groups, b = blockIdx.x / p.groups, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int4 rec = p.rec[blockIdx.x];
     if (rec.x < 0) return;
     const int h0 = group * p.per_group, nh = min(p.per_group, p.heads - h0);
-    const int oct = many ? (int)blockIdx.z : warp, n = rec.z - rec.y + 1;
+    const int oct = many ? (int)blockIdx.z : warp, n = rec.y - rec.x + 1;
     const int64_t floats = piece_floats(p.latent);
-    const float *pieces = p.part + (2 * ((int64_t)rec.y * p.groups + group)) * floats;  // of run i: 2 i groups further; the first is a second piece
+    const float *pieces = p.part + (2 * ((int64_t)rec.x * p.groups + group)) * floats;  // of run i: 2 i groups further; the first is a second piece
     const auto piece = [&](int i) { return pieces + (2 * (int64_t)i * p.groups + (i == 0)) * floats; };
     float top = kFloor, l = 0.f;
     float (*const w)[8] = wt[many ? 0 : warp];
@@ -771,7 +759,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
         for (int k = 0; k < 5; ++k) {
             const int i = (i0 + k * team) >> 3;
             // a run may be empty: no weight
-            const bool holds = i < n && (int)((int64_t)rec.w * (rec.y + i) / p.runs) < (int)((int64_t)rec.w * (rec.y + i + 1) / p.runs);
+            const bool holds = i < n && (int)((int64_t)rec.z * (rec.x + i) / p.runs) < (int)((int64_t)rec.z * (rec.x + i + 1) / p.runs);
             m[k] = holds ? piece(i)[at] : -INFINITY;
         }
 #pragma unroll
@@ -816,38 +804,41 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     } else {
         __syncwarp();
     }
-    const int d = 32 * blockIdx.y + lane;
-    float s[8] = {};
-    if (8 * oct < nh)
-#pragma unroll 5
-        for (int i = many ? warp : 0; i < n; i += many ? 8 : 1) {
-            const float4 f0 = *reinterpret_cast<const float4 *>(w[i]), f1 = *reinterpret_cast<const float4 *>(w[i] + 4);
-            if (f0.x < 0.f) continue;
-            const float4 *v = reinterpret_cast<const float4 *>(piece(i) + d * kHeads + 8 * oct);
-            const float4 v0 = v[0], v1 = v[1];
-            s[0] += f0.x * v0.x; s[1] += f0.y * v0.y; s[2] += f0.z * v0.z; s[3] += f0.w * v0.w;
-            s[4] += f1.x * v1.x; s[5] += f1.y * v1.y; s[6] += f1.z * v1.z; s[7] += f1.w * v1.w;
-        }
-    if (many) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sums[warp][j][lane] = s[j];
-        __syncthreads();
-        if (warp) return;
-#pragma unroll
-        for (int q = 1; q < 8; ++q)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] += sums[q][j][lane];
-    }
     constexpr float kOff = std::is_same<T, __half>::value ? 7.f : 0.f;
+    for (int d = 32 * blockIdx.y + lane; d < p.latent; d += 32 * gridDim.y) {
+        float s[8] = {};
+        if (8 * oct < nh)
+#pragma unroll 5
+            for (int i = many ? warp : 0; i < n; i += many ? 8 : 1) {
+                const float4 f0 = *reinterpret_cast<const float4 *>(w[i]), f1 = *reinterpret_cast<const float4 *>(w[i] + 4);
+                if (f0.x < 0.f) continue;
+                const float4 *v = reinterpret_cast<const float4 *>(piece(i) + d * kHeads + 8 * oct);
+                const float4 v0 = v[0], v1 = v[1];
+                s[0] += f0.x * v0.x; s[1] += f0.y * v0.y; s[2] += f0.z * v0.z; s[3] += f0.w * v0.w;
+                s[4] += f1.x * v1.x; s[5] += f1.y * v1.y; s[6] += f1.z * v1.z; s[7] += f1.w * v1.w;
+            }
+        if (many) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float lj = __shfl_sync(0xffffffffu, l, j), mj = __shfl_sync(0xffffffffu, top, j);
-        const int h = 8 * oct + j;
-        if (h >= nh) continue;
-        from_f32(lj > 0.f ? s[j] * (a.k_scale / lj) : 0.f,
-                 static_cast<T *>(a.out)[rec.x * a.out_stride_b + (h0 + h) * a.out_stride_h + d]);
-        if (a.lse && blockIdx.y == 0 && lane == 0)
-            a.lse[(int64_t)rec.x * p.heads + h0 + h] = lj > 0.f ? (mj - kOff) / kLog2e + logf(lj) : -INFINITY;
+            for (int j = 0; j < 8; ++j) sums[warp][j][lane] = s[j];
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int q = 1; q < 8; ++q)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[j] += sums[q][j][lane];
+            }
+            __syncthreads();
+            if (warp) continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float lj = __shfl_sync(0xffffffffu, l, j), mj = __shfl_sync(0xffffffffu, top, j);
+            const int h = 8 * oct + j;
+            if (h >= nh) continue;
+            from_f32(lj > 0.f ? s[j] * (a.k_scale / lj) : 0.f,
+                     static_cast<T *>(a.out)[b * a.out_stride_b + (h0 + h) * a.out_stride_h + d]);
+            if (a.lse && d == 0) a.lse[(int64_t)b * p.heads + h0 + h] = lj > 0.f ? (mj - kOff) / kLog2e + logf(lj) : -INFINITY;
+        }
     }
 }
 
@@ -872,7 +863,7 @@ cudaError_t latent_prepare(const MoeLatentDesc &d, int num_sms, size_t *bytes) {
             if (e != cudaSuccess) return e;
         }
     const int64_t blocks = (int64_t)groups_of(d.n_heads) * runs_of(d.n_heads, num_sms);
-    *bytes = (size_t)blocks * (2 * (size_t)piece_floats(d.latent_dim) * 4 + sizeof(int4));
+    *bytes = (size_t)blocks * 2 * (size_t)piece_floats(d.latent_dim) * 4 + (size_t)d.max_requests * groups_of(d.n_heads) * sizeof(int4);
     return cudaSuccess;
 }
 
@@ -913,13 +904,13 @@ cudaError_t launch_latent_decode(const LatentHandle &h, const MoeLatentArgs &a, 
     void *args[] = {&cmap, &p};
     cudaError_t e = launch_after(fn, blocks, kThreads, kSmem, s, args);
     if (e != cudaSuccess) return e;
-    const int split = a.n_requests < p.runs ? a.n_requests : p.runs;  // requests over several runs, at most
-    int many = 8 * split <= p.runs;
+    int many = 8 * a.n_requests <= p.runs;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)(split * p.groups), (unsigned)(p.latent / 32), many ? (unsigned)(p.per_group + 7) / 8 : 1u);
+    c.gridDim = dim3((unsigned)(a.n_requests * p.groups), a.n_requests <= p.runs ? (unsigned)(p.latent / 32) : 1u,
+                     many ? (unsigned)(p.per_group + 7) / 8 : 1u);
     c.blockDim = dim3(256);
     c.stream = s;
     c.attrs = at;

@@ -113,10 +113,17 @@ int moe_latent_create(const MoeLatentDesc *d, void **handle_out) {
         delete h;
         return cuda_fail(ce, "device query");
     }
-    if (bytes && (ce = cudaMalloc(&h->part, bytes)) != cudaSuccess) {
+    if ((ce = cudaMalloc(&h->part, bytes)) != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return fail(MOE_ERR_NOMEM, "workspace of %zu bytes: %s", bytes, cudaGetErrorString(ce));
+    }
+    ce = cudaMemset(h->part, 0xff, bytes);  // no request is split before the first call says so
+    if (ce == cudaSuccess) ce = cudaDeviceSynchronize();
+    if (ce != cudaSuccess) {
+        cudaFree(h->part);
+        delete h;
+        return cuda_fail(ce, "handle initialisation");
     }
     h->magic = kLatentMagic;
     *handle_out = h;
