@@ -646,6 +646,8 @@ int moe_block_norm(const MoeNormArgs *args, cudaStream_t stream);
  *   x8    [n_tokens] rows of dim codes out, x8_stride apart
  *   scale [n_tokens, ceil(dim / 128)] out, contiguous
  * dim is a multiple of 16, 16..65536; every row of x and x8 starts on 16 bytes.
+ * As in the formula, a group with a NaN has scale NaN and codes of NaN, one with
+ * an infinity scale infinity and codes of NaN for its infinities, else 0.
  * No output overlaps x or the other output.
  * Errors: INVALID_ARG, SHAPE, CUDA.
  */
@@ -669,7 +671,7 @@ typedef struct {
  *   x_scale[t, b] * w_scale[o / 128, b] * sum over i in b of x8[t, i] * w8[o, i]
  * Sums are held in fp32; one rounding to out_type.  The layout of w_scale is
  * that of moe_fp8_block_to_int4.  Rows of x8 and w8 start on 16 bytes.  out
- * overlaps no input.  Codes of NaN give NaN.
+ * overlaps no input.  Codes of NaN give NaN.  n_tokens * n_out stays within 2^40.
  * Errors: INVALID_ARG, SHAPE, CUDA.
  */
 int moe_fp8_linear(const MoeFp8LinearArgs *args, cudaStream_t stream);
@@ -684,7 +686,7 @@ typedef struct {
 
 /*
  * Create / destroy a latent attention handle: the workspace in which a call
- * joins what it splits (it owns that device memory, up to 41 MB).  One stream
+ * joins what it splits (it owns that device memory, up to 43 MB).  One stream
  * at a time, on the device current at create; as with moe_attn_create, both
  * wait for the device, and graphs that captured a call use the workspace.
  * Destroying NULL is accepted.  Errors: INVALID_ARG, SHAPE, NOMEM, CUDA.
@@ -698,7 +700,7 @@ typedef struct {
     int act_type, cache_type;   /* q and out: MOE_F16 / BF16; cache: the same type, or MOE_E4M3 */
     int page_size;              /* 1..65536 */
     int max_pages;              /* entries of a table row */
-    float scale;                /* on q . c */
+    float scale;                /* on q . c; |scale * k_scale| at most 2^120 */
     float k_scale;              /* on E4M3 codes, > 0 (1 for the others) */
     const int32_t *seq_len;     /* [n_requests]; longer than the table row: cut to it */
     const int32_t *block_table; /* rows table_stride apart */
@@ -724,7 +726,8 @@ typedef struct {
  * product rounded to act_type.  The result does not depend on which block
  * finishes first.  May be captured in a CUDA graph.  Queries and rows that are
  * read hold finite numbers.  max_pages * page_size stays below 2^31 - 64,
- * n_requests * max_pages * page_size below 2^36.
+ * n_requests * max_pages * page_size below 2^36.  Strides of q and out lie in
+ * [0, 2^38) bytes; the rows of out are apart, out and lse overlap no input.
  * Errors: INVALID_ARG, SHAPE, CUDA.
  */
 int moe_latent_decode(void *handle, const MoeLatentArgs *args, cudaStream_t stream);
@@ -736,7 +739,7 @@ typedef struct {
     int nope_dim, rope_dim, v_dim;   /* multiples of 16: 16..256, 0..64 (together <= 256), 16..256 */
     int act_type;                    /* MOE_F16 / BF16 */
     int causal;
-    float scale;
+    float scale;                     /* at most 2^120 in magnitude */
     const int32_t *q_start, *kv_start; /* [n_requests + 1]: request b holds queries [q_start[b], q_start[b + 1])
                                         * and keys [kv_start[b], kv_start[b + 1]); neither falls */
     const void *q;                   /* [n_queries, n_heads, nope_dim + rope_dim] */
@@ -760,7 +763,9 @@ typedef struct {
  * Logits, statistics and sums are held in fp32; weights enter the second
  * product rounded to act_type.  Rows of q, k, k_rope and v start on 16 bytes
  * with strides in [0, 2^38) bytes.  May be captured in a CUDA graph.  The
- * queries, keys and values of a request are finite.  out overlaps no input.
+ * queries, keys and values of a request are finite.  The rows of out are apart
+ * (so are, a head at a time, those of q, k, k_rope and v); out and lse overlap no
+ * input.
  * Errors: INVALID_ARG, SHAPE, CUDA.
  */
 int moe_latent_prompt(const MoePromptArgs *args, cudaStream_t stream);

@@ -13,6 +13,13 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// The larger one, NaN if either is: the formula's maximum.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quant_fp8_kernel(const T *x, int64_t x_stride, int dim, FastDiv by_row,
                                                              uint32_t units, uint8_t *x8, int64_t x8_stride,
@@ -28,11 +35,11 @@ __global__ void __launch_bounds__(kThreads) quant_fp8_kernel(const T *x, int64_t
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         if (!live) v[i] = 0.f;
-        top = fmaxf(top, fabsf(v[i]));
+        top = max_nan(top, fabsf(v[i]));
     }
 #pragma unroll
-    for (int m = 4; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffu << (threadIdx.x & 24), top, m));
-    const float s = fmaxf(__fdiv_rn(top, 448.f), 1e-12f);
+    for (int m = 4; m; m >>= 1) top = max_nan(top, __shfl_xor_sync(0xffu << (threadIdx.x & 24), top, m));
+    const float s = max_nan(__fdiv_rn(top, 448.f), 1e-12f);
     if (live) {
         uint32_t w[4];
 #pragma unroll

@@ -17,6 +17,7 @@ constexpr int kMaxInner = 65536;
 constexpr int kMaxOuter = 1 << 20;
 constexpr int kMaxPage = 65536;
 constexpr int kMaxHeads = 1024;
+constexpr float kMaxScale = 1.3292280e36f;  // 2^120: times log2(e) it stays finite
 
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool is_act(int t) { return t == MOE_F32 || t == MOE_F16 || t == MOE_BF16; }
@@ -31,8 +32,21 @@ struct Span {
         return n > 0 && o.n > 0 && a < b + (uintptr_t)o.n && b < a + (uintptr_t)n;
     }
 };
+// n * stride, both from 0; what no address space holds stays at 2^60
+int64_t reach(int64_t n, int64_t stride) { return stride > 0 && n > (1ll << 60) / stride ? 1ll << 60 : n * stride; }
 // rows of `row` bytes, `stride` bytes apart
-Span rows(const void *p, int64_t n, int64_t stride, int64_t row) { return {p, n > 0 ? (n - 1) * stride + row : 0}; }
+Span rows(const void *p, int64_t n, int64_t stride, int64_t row) { return {p, n > 0 ? reach(n - 1, stride) + row : 0}; }
+// [n1][n2] rows of two-byte elements
+Span rows2(const void *p, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t dim) {
+    return rows(p, n1, 2 * s1, reach(n2 - 1, 2 * s2) + 2 * dim);
+}
+// Whether those rows are apart from each other.
+bool apart(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t dim) {
+    const auto nested = [&](int64_t no, int64_t so, int64_t ni, int64_t si) {
+        return (ni <= 1 || si >= dim) && (no <= 1 || so >= reach(ni - 1, si) + dim);
+    };
+    return nested(n1, s1, n2, s2) || nested(n2, s2, n1, s1);
+}
 
 }  // namespace
 
@@ -69,6 +83,7 @@ int moe_fp8_linear(const MoeFp8LinearArgs *p, cudaStream_t stream) {
         return fail(MOE_ERR_SHAPE, "n_tokens=%d n_in=%d n_out=%d: need 0..2^24, a multiple of 16 in 16..%d, 1..%d",
                     a.n_tokens, a.n_in, a.n_out, kMaxInner, kMaxOuter);
     if (!is_act(a.out_type)) return fail(MOE_ERR_INVALID_ARG, "out_type=%d", a.out_type);
+    if ((int64_t)a.n_tokens * a.n_out > 1ll << 40) return fail(MOE_ERR_SHAPE, "n_tokens * n_out must stay within 2^40");
     if (a.n_tokens == 0) return MOE_OK;
     const int64_t most = 1ll << 38, oe = (int64_t)moe::dtype_bytes(a.out_type);
     if ((a.n_tokens > 1 && (a.x_stride < a.n_in || a.x_stride >= most || a.out_stride < a.n_out || a.out_stride >= most)) ||
@@ -165,8 +180,8 @@ int moe_latent_decode(void *handle, const MoeLatentArgs *p, cudaStream_t stream)
     if (!is_half(a.act_type) || (a.cache_type != a.act_type && a.cache_type != MOE_E4M3))
         return fail(MOE_ERR_INVALID_ARG, "act_type=%d cache_type=%d: need F16 or BF16, and the same or E4M3",
                     a.act_type, a.cache_type);
-    if (!std::isfinite(a.scale) || !(a.k_scale > 0) || !std::isfinite(a.k_scale))
-        return fail(MOE_ERR_INVALID_ARG, "scale must be finite, k_scale positive");
+    if (!(a.k_scale > 0) || !std::isfinite(a.k_scale) || !(std::fabs(a.scale * a.k_scale) <= kMaxScale))
+        return fail(MOE_ERR_INVALID_ARG, "k_scale must be positive, |scale * k_scale| at most 2^120");
     if (a.cache_type != MOE_E4M3 && a.k_scale != 1.f)
         return fail(MOE_ERR_INVALID_ARG, "k_scale belongs to E4M3 caches");
     if (a.n_requests == 0) return MOE_OK;
@@ -181,6 +196,19 @@ int moe_latent_decode(void *handle, const MoeLatentArgs *p, cudaStream_t stream)
         return fail(MOE_ERR_INVALID_ARG, "cache rows must start on 16 bytes");
     for (int64_t st : {a.c_stride_page, a.c_stride_tok})
         if (st < 0 || st > INT32_MAX / ce) return fail(MOE_ERR_SHAPE, "cache strides must lie in [0, 2^31) bytes");
+    for (int64_t st : {a.q_stride_b, a.q_stride_h, a.out_stride_b, a.out_stride_h})
+        if (st < 0 || st >= 1ll << 37) return fail(MOE_ERR_SHAPE, "strides of q and out must lie in [0, 2^38) bytes");
+    const int64_t n = a.n_requests, dim = h->d.latent_dim + h->d.rope_dim;
+    if (!apart(n, a.out_stride_b, h->d.n_heads, a.out_stride_h, h->d.latent_dim))
+        return fail(MOE_ERR_INVALID_ARG, "rows of out overlap");
+    const Span out = rows2(a.out, n, a.out_stride_b, h->d.n_heads, a.out_stride_h, h->d.latent_dim),
+               lse = {a.lse, a.lse ? 4 * n * h->d.n_heads : 0};
+    const Span in[] = {rows2(a.q, n, a.q_stride_b, h->d.n_heads, a.q_stride_h, dim),
+                       rows(a.cache, a.n_pages, a.c_stride_page * ce, (a.page_size - 1) * a.c_stride_tok * ce + dim * ce),
+                       rows(a.block_table, a.max_pages ? n : 0, 4 * a.table_stride, 4ll * a.max_pages), {a.seq_len, 4 * n}};
+    for (const Span &i : in)
+        if (out.meets(i) || lse.meets(i)) return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input");
+    if (out.meets(lse)) return fail(MOE_ERR_INVALID_ARG, "out and lse overlap");
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -203,7 +231,7 @@ int moe_latent_prompt(const MoePromptArgs *p, cudaStream_t stream) {
         return fail(MOE_ERR_SHAPE, "nope_dim=%d rope_dim=%d v_dim=%d: need multiples of 16, rope_dim <= 64, "
                     "nope_dim + rope_dim and v_dim <= 256", a.nope_dim, a.rope_dim, a.v_dim);
     if (!is_half(a.act_type)) return fail(MOE_ERR_INVALID_ARG, "act_type=%d: need F16 or BF16", a.act_type);
-    if (!std::isfinite(a.scale)) return fail(MOE_ERR_INVALID_ARG, "scale must be finite");
+    if (!(std::fabs(a.scale) <= kMaxScale)) return fail(MOE_ERR_INVALID_ARG, "|scale| must be at most 2^120");
     if (a.n_requests == 0 || a.n_queries == 0) return MOE_OK;
     if (!a.q_start || !a.kv_start || !a.q || !a.out ||
         (a.n_keys > 0 && (!a.k || !a.v || (a.rope_dim > 0 && !a.k_rope))))
@@ -220,9 +248,10 @@ int moe_latent_prompt(const MoePromptArgs *p, cudaStream_t stream) {
         if (st < 0 || st >= 1ll << 37) return fail(MOE_ERR_INVALID_ARG, "out strides must lie in [0, 2^38) bytes");
     if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || (a.rope_dim > 0 && !aligned(a.k_rope, 16)))
         return fail(MOE_ERR_INVALID_ARG, "rows of q, k, k_rope and v must start on 16 bytes");
-    const int64_t hs = a.n_heads - 1;
+    if (!apart(a.n_queries, a.out_stride_t, a.n_heads, a.out_stride_h, a.v_dim))
+        return fail(MOE_ERR_INVALID_ARG, "rows of out overlap");
     const auto span = [&](const void *q, int64_t n, int64_t st, int64_t sh, int64_t dim) {
-        return rows(q, n, 2 * st, 2 * (hs * sh + dim));
+        return rows2(q, n, st, a.n_heads, sh, dim);
     };
     const Span out = span(a.out, a.n_queries, a.out_stride_t, a.out_stride_h, a.v_dim);
     const Span lse = {a.lse, a.lse ? 4ll * a.n_queries * a.n_heads : 0};
