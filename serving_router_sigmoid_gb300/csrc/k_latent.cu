@@ -15,22 +15,28 @@
 //
 // Per tile of 64 tokens the tensor core works 36 x 32 + 16 x 48 = 1920 cycles (the
 // second product is bound by its operands' 128 bytes a cycle); HBM brings a tile in
-// 3300 cycles a SM (16-bit) or 1650 (E4M3).
+// 3300 cycles a SM (16-bit) or 1650 (E4M3).  Measured: a tile in 4100 (16-bit), since
+// two stages beside 72 KB of queries leave the chain load, S, softmax, O little to
+// overlap; 32-token tiles in four stages were slower (fixed costs an MMA and a
+// barrier).  64 requests of up to 16384 tokens, 128 heads: 133 us (2.05 TB/s of rows
+// read once from HBM and twice from L2); 2 of 131072 in E4M3, 64 heads: 85 us.
 //
 // - Work is split by cost: the tiles of all requests, and kSegCost more for each
 //   request, form one line; each block takes an equal run, found from the lengths
 //   by itself.  More than 64 heads form groups; the blocks of a run's groups are
 //   neighbours and read the same rows at the same time, once from HBM.
-// - Eight producer warps copy rows (cp.async, any page size and stride), or load
-//   E4M3 codes and widen them, into two stages; one warp issues the MMAs: S of tile
-//   i + 1 before O of tile i, so that the softmax of one runs under the products of
-//   the other; four warps do the softmax and write the results.
+// - Eight producer warps copy rows (cp.async, any page size and stride), issue TMA
+//   copies of them, or load E4M3 codes and widen them, into two stages of three parts;
+//   a part is used and given back by itself.  One warp issues the products S, another
+//   the products O (one that issued both in turn let each wait for the other's
+//   barriers: 139 against 136 us); four warps do the softmax and write the results.
 // - The maximum moves only when a logit passes it by 2^kLazy; then O is scaled in
 //   tensor memory.  Weights are rounded to the operand type (their sum is not), for
 //   f16 times 2^7, so that its subnormals begin at 2^-31 of the maximum.
 // - A request that several blocks share leaves its pieces (O, m, l) in the handle's
 //   workspace; a second small launch joins them in order, so results do not depend
-//   on timing.
+//   on timing.  Pieces lie as [8 heads][latent][8], so that 32 lanes write and read
+//   1 KB in a row (256-byte steps took 20 us more for 2 requests of 30000 tokens).
 #include <type_traits>
 
 #include "tc_dev.cuh"
@@ -71,7 +77,7 @@ struct Params {
     int64_t c_page, c_tok;            // bytes
     uint32_t n_pages;
     float *part;                      // [2 * blocks] pieces
-    int4 *rec;                        // [requests * groups]: first and last run of a request that several hold, else x < 0
+    int2 *rec;                        // [requests * groups]: first and last run of a request that several hold, else x < 0
 };
 
 __host__ __device__ inline int64_t piece_floats(int latent) { return (int64_t)kHeads * latent + 2 * kHeads; }
@@ -237,7 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         if (w < warp) before += sm.sums[w];
         total += sm.sums[w];
     }
-    const int lo = (int)((int64_t)total * run / p.runs), hi = (int)((int64_t)total * (run + 1) / p.runs);
+    const int runs = min(max(total, 1), p.runs);  // none is empty
+    const int lo = run < runs ? (int)((int64_t)total * run / runs) : total;
+    const int hi = run < runs ? (int)((int64_t)total * (run + 1) / runs) : total;
     if (lo < hi && before <= lo && lo < before + mine) {
         int b = c0, s = before;
         for (;; ++b) {
@@ -648,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                 // the runs that hold tiles of it: this one to the one of its last tile (the first writes)
                 if (from0 && tid == 0)
                     p.rec[(int64_t)b * p.groups + group] =
-                        make_int4(ends ? -1 : run, (int)(((int64_t)(s + kSegCost + tiles) * p.runs - 1) / total), total, 0);
+                        make_int2(ends ? -1 : run, (int)(((int64_t)(s + kSegCost + tiles) * runs - 1) / total));
                 if (from0 && ends) {
                     if ((lane & 3) == 0)
 #pragma unroll
@@ -706,11 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                         tmem_wait_ld();
                         const int d = (c >> 6) * 128 + 32 * warp + lane;
                         if (d >= p.latent) continue;
-                        uint32_t *to = reinterpret_cast<uint32_t *>(piece) + d * kHeads + (c & 63);
+                        uint32_t *to = reinterpret_cast<uint32_t *>(piece) + (c & 63) * p.latent + 8 * d;  // by 8 heads
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const uint32_t y[8] = {o[8 * k], o[8 * k + 1], o[8 * k + 2], o[8 * k + 3], o[8 * k + 4], o[8 * k + 5], o[8 * k + 6], o[8 * k + 7]};
-                            st32(to + 8 * k, y);
+                            st32(to + 8 * k * p.latent, y);
                         }
                     }
                 }
@@ -731,36 +739,35 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 // Joins the pieces of the requests that several runs share.  A block takes 32
 // latent dimensions of a request and head group (or all of them in turn, where
 // requests outnumber the runs and few are shared), a lane one of them for 8 heads
-// (32 contiguous bytes a piece); its 8 warps take 8 heads each, or (many: few
-// requests over many runs) a part of the runs for the same 8 heads.
+// (32 contiguous bytes a piece); W of its 8 warps take 8 heads, each a part of the
+// runs.
 constexpr int kMaxRuns = 152;
-template <typename T>
-__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ Params p, int many) {
+constexpr int kBatch = 6;  // pieces that a lane loads at once
+template <typename T, int W>
+__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ Params p) {
     after_previous();
-    __shared__ __align__(16) float wt[8][kMaxRuns][8];
+    __shared__ __align__(16) float wt[8 / W][kMaxRuns][8];
     __shared__ float sums[8][8][32];
     const MoeLatentArgs &a = p.a;
     const int group = blockIdx.x % p.groups, b = blockIdx.x / p.groups, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int4 rec = p.rec[blockIdx.x];
+    const int2 rec = p.rec[blockIdx.x];
     if (rec.x < 0) return;
     const int h0 = group * p.per_group, nh = min(p.per_group, p.heads - h0);
-    const int oct = many ? (int)blockIdx.z : warp, n = rec.y - rec.x + 1;
+    const int oct = blockIdx.z * (8 / W) + warp / W, part = warp % W, n = rec.y - rec.x + 1;
     const int64_t floats = piece_floats(p.latent);
     const float *pieces = p.part + (2 * ((int64_t)rec.x * p.groups + group)) * floats;  // of run i: 2 i groups further; the first is a second piece
     const auto piece = [&](int i) { return pieces + (2 * (int64_t)i * p.groups + (i == 0)) * floats; };
     float top = kFloor, l = 0.f;
-    float (*const w)[8] = wt[many ? 0 : warp];
-    // maxima and sums of the pieces, (run, head) pairs over the 8 heads' threads: all of them (many) or a warp
-    const int team = many ? 256 : 32, me = many ? tid : lane, pairs = 8 * oct < nh ? 8 * n : 0;
+    float (*const w)[8] = wt[warp / W];
+    // maxima and sums of the pieces, (run, head) pairs over the W warps' threads
+    const int team = 32 * W, me = 32 * part + lane, pairs = 8 * oct < nh ? 8 * n : 0;
     const int64_t at = (int64_t)kHeads * p.latent + 8 * oct + (lane & 7);
     for (int i0 = me; i0 < pairs; i0 += 5 * team) {
         float m[5];
 #pragma unroll
         for (int k = 0; k < 5; ++k) {
             const int i = (i0 + k * team) >> 3;
-            // a run may be empty: no weight
-            const bool holds = i < n && (int)((int64_t)rec.z * (rec.x + i) / p.runs) < (int)((int64_t)rec.z * (rec.x + i + 1) / p.runs);
-            m[k] = holds ? piece(i)[at] : -INFINITY;
+            m[k] = i < n ? piece(i)[at] : -INFINITY;
         }
 #pragma unroll
         for (int k = 0; k < 5; ++k) {
@@ -770,11 +777,11 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-    if (many) {
+    if (W > 1) {
         if (lane < 8) sums[0][warp][lane] = top;
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) top = fmaxf(top, sums[0][q][lane & 7]);
+        for (int q = 0; q < W; ++q) top = fmaxf(top, sums[0][warp - part + q][lane & 7]);
     }
     for (int i0 = me; i0 < pairs; i0 += 5 * team) {
         float v[5];
@@ -787,19 +794,19 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
         for (int k = 0; k < 5; ++k) {
             const int i = (i0 + k * team) >> 3;
             if (i >= n) continue;
-            const float m = w[i][lane & 7], f = m == -INFINITY ? -1.f : ex2(m - top);
+            const float f = ex2(w[i][lane & 7] - top);
             w[i][lane & 7] = f;
-            if (f > 0.f) l += f * v[k];
+            l += f * v[k];
         }
     }
     l += __shfl_xor_sync(0xffffffffu, l, 8);
     l += __shfl_xor_sync(0xffffffffu, l, 16);
-    if (many) {
+    if (W > 1) {
         if (lane < 8) sums[1][warp][lane] = l;
         __syncthreads();
         l = 0.f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) l += sums[1][q][lane & 7];
+        for (int q = 0; q < W; ++q) l += sums[1][warp - part + q][lane & 7];
         __syncthreads();
     } else {
         __syncwarp();
@@ -807,28 +814,36 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     constexpr float kOff = std::is_same<T, __half>::value ? 7.f : 0.f;
     for (int d = 32 * blockIdx.y + lane; d < p.latent; d += 32 * gridDim.y) {
         float s[8] = {};
-        if (8 * oct < nh)
-#pragma unroll 5
-            for (int i = many ? warp : 0; i < n; i += many ? 8 : 1) {
-                const float4 f0 = *reinterpret_cast<const float4 *>(w[i]), f1 = *reinterpret_cast<const float4 *>(w[i] + 4);
-                if (f0.x < 0.f) continue;
-                const float4 *v = reinterpret_cast<const float4 *>(piece(i) + d * kHeads + 8 * oct);
-                const float4 v0 = v[0], v1 = v[1];
-                s[0] += f0.x * v0.x; s[1] += f0.y * v0.y; s[2] += f0.z * v0.z; s[3] += f0.w * v0.w;
-                s[4] += f1.x * v1.x; s[5] += f1.y * v1.y; s[6] += f1.z * v1.z; s[7] += f1.w * v1.w;
+        for (int i0 = part; i0 < n && 8 * oct < nh; i0 += kBatch * W) {
+            float4 v[kBatch][2];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {  // all in flight at once
+                if (i0 + k * W >= n) continue;
+                const float4 *at = reinterpret_cast<const float4 *>(piece(i0 + k * W) + 8 * (oct * p.latent + d));
+                v[k][0] = at[0];
+                v[k][1] = at[1];
             }
-        if (many) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * W;
+                if (i >= n) continue;
+                const float4 f0 = *reinterpret_cast<const float4 *>(w[i]), f1 = *reinterpret_cast<const float4 *>(w[i] + 4);
+                s[0] += f0.x * v[k][0].x; s[1] += f0.y * v[k][0].y; s[2] += f0.z * v[k][0].z; s[3] += f0.w * v[k][0].w;
+                s[4] += f1.x * v[k][1].x; s[5] += f1.y * v[k][1].y; s[6] += f1.z * v[k][1].z; s[7] += f1.w * v[k][1].w;
+            }
+        }
+        if (W > 1) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) sums[warp][j][lane] = s[j];
             __syncthreads();
-            if (warp == 0) {
+            if (part == 0) {
 #pragma unroll
-                for (int q = 1; q < 8; ++q)
+                for (int q = 1; q < W; ++q)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[j] += sums[q][j][lane];
+                    for (int j = 0; j < 8; ++j) s[j] += sums[warp + q][j][lane];
             }
             __syncthreads();
-            if (warp) continue;
+            if (part) continue;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -854,6 +869,31 @@ const void *kernel(bool bf) {
               : reinterpret_cast<const void *>(latent_decode_kernel<false, LOAD>);
 }
 
+template <typename T>
+cudaError_t launch_join(Params &p, cudaStream_t s) {
+    const int n = p.a.n_requests;
+    // by the pieces a request has at most. Measured, decode and join of requests of up to
+    // 3000 tokens, 64 heads, W = 1 2 4 8: 2 requests 20.1 17.0 15.5 14.7 us; 4: 29.0 21.2
+    // 17.4 18.7; 8: 23.9 19.7 21.2 23.1; 18: 25.0 27.3 30.0 37.1
+    const int W = 3 * n <= p.runs ? 8 : 6 * n <= p.runs ? 4 : 12 * n <= p.runs ? 2 : 1;
+    const void *fn = W == 8 ? reinterpret_cast<const void *>(latent_join_kernel<T, 8>)
+                     : W == 4 ? reinterpret_cast<const void *>(latent_join_kernel<T, 4>)
+                     : W == 2 ? reinterpret_cast<const void *>(latent_join_kernel<T, 2>)
+                              : reinterpret_cast<const void *>(latent_join_kernel<T, 1>);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(n * p.groups), n <= p.runs ? (unsigned)(p.latent / 32) : 1u,
+                     (unsigned)((p.per_group + 7) / 8 * W + 7) / 8);
+    c.blockDim = dim3(256);
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    void *args[] = {&p};
+    return cudaLaunchKernelExC(&c, fn, args);
+}
+
 }  // namespace
 
 cudaError_t latent_prepare(const MoeLatentDesc &d, int num_sms, size_t *bytes) {
@@ -863,7 +903,7 @@ cudaError_t latent_prepare(const MoeLatentDesc &d, int num_sms, size_t *bytes) {
             if (e != cudaSuccess) return e;
         }
     const int64_t blocks = (int64_t)groups_of(d.n_heads) * runs_of(d.n_heads, num_sms);
-    *bytes = (size_t)blocks * 2 * (size_t)piece_floats(d.latent_dim) * 4 + (size_t)d.max_requests * groups_of(d.n_heads) * sizeof(int4);
+    *bytes = (size_t)blocks * 2 * (size_t)piece_floats(d.latent_dim) * 4 + (size_t)d.max_requests * groups_of(d.n_heads) * sizeof(int2);
     return cudaSuccess;
 }
 
@@ -886,7 +926,7 @@ cudaError_t launch_latent_decode(const LatentHandle &h, const MoeLatentArgs &a, 
     p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride_b % 16 == 0 && a.out_stride_h % 16 == 0;
     p.part = h.part;
     const int blocks = p.groups * p.runs;
-    p.rec = reinterpret_cast<int4 *>(h.part + 2 * blocks * piece_floats(p.latent));
+    p.rec = reinterpret_cast<int2 *>(h.part + 2 * blocks * piece_floats(p.latent));
     const bool bf = a.act_type == MOE_BF16;
     for (p.box = kTile; p.box > 1 && a.page_size % p.box;) p.box /= 2;
     CUtensorMap cmap = {};
@@ -894,9 +934,12 @@ cudaError_t launch_latent_decode(const LatentHandle &h, const MoeLatentArgs &a, 
     if (a.cache_type == MOE_E4M3) {
         fn = kernel<kByCode>(bf);
     } else {
-        // boxes of 8 rows and more keep the swizzle's atoms; rows and pages that overlap have no map
+        // (rows that overlap have no map)
         const int64_t dims[3] = {p.dim, a.page_size, a.n_pages}, str[2] = {p.c_tok, a.n_pages > 1 ? p.c_page : p.c_tok * a.page_size};
-        const bool tma = p.box >= 8 && a.n_pages > 0 && p.c_tok >= 2 * p.dim && str[1] >= 2 * p.dim &&
+        // Boxes of 8 rows and more keep the swizzle's atoms, small ones are slow. Measured, 64
+        // requests, 128 heads, TMA and rows: pages of 8 tokens 190 and 148 us, 16: 147.6 and
+        // 147.6, 32: 143.5 and 147.6, 64: 142 and 147.5
+        const bool tma = p.box >= 32 && a.n_pages > 0 && p.c_tok >= 2 * p.dim && str[1] >= 2 * p.dim &&
                          encode_map(&cmap, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.cache, 3, dims,
                                     str, p.box) == cudaSuccess;
         fn = tma ? kernel<kByTma>(bf) : kernel<kByRow>(bf);
@@ -904,20 +947,7 @@ cudaError_t launch_latent_decode(const LatentHandle &h, const MoeLatentArgs &a, 
     void *args[] = {&cmap, &p};
     cudaError_t e = launch_after(fn, blocks, kThreads, kSmem, s, args);
     if (e != cudaSuccess) return e;
-    int many = 8 * a.n_requests <= p.runs;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)(a.n_requests * p.groups), a.n_requests <= p.runs ? (unsigned)(p.latent / 32) : 1u,
-                     many ? (unsigned)(p.per_group + 7) / 8 : 1u);
-    c.blockDim = dim3(256);
-    c.stream = s;
-    c.attrs = at;
-    c.numAttrs = 1;
-    void *jargs[] = {&p, &many};
-    return cudaLaunchKernelExC(&c, bf ? reinterpret_cast<const void *>(latent_join_kernel<__nv_bfloat16>)
-                                      : reinterpret_cast<const void *>(latent_join_kernel<__half>), jargs);
+    return bf ? launch_join<__nv_bfloat16>(p, s) : launch_join<__half>(p, s);
 }
 
 cudaError_t latent_decode_flags(int32_t *out) {
