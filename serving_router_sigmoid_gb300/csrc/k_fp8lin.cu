@@ -9,16 +9,25 @@
 // The scales are fp32, not powers of two, so the tensor cores cannot apply them.
 //
 // Two orientations:
-//  - Few tokens (up to 64): 128 matrix rows on the MMA's M side, the tokens (16 to
-//    64) on N.  The matrix streams once; HBM bounds it.  A stage is 16 KB and a
-//    little, six of them let two blocks share an SM.
+//  - Few tokens (up to 32): 128 matrix rows on the MMA's M side, the tokens (16 or
+//    32) on N.  The matrix streams once; HBM bounds it, and at the smallest the
+//    launch.  A stage is 18 or 20 KB, five or six of them let two blocks share an SM.
+//    Measured: 1 token, 6144 -> 2048 (12.6 MB) 6.1 us; 8 tokens, 2048 -> 12288 (25 MB)
+//    7.3 us.
 //  - More: 128 tokens on M, 128 or 256 matrix rows on N: a thread's sums belong to
 //    one token, whose scale is one register, and the matrix scale is one number a
-//    block of 128 rows: one FMA an element.
+//    block of 128 rows: one FMA an element.  Every accumulator is read from tensor
+//    memory once a block of inputs, by up to 16 warps (8 with twice the sums took 117
+//    us where these take 112).  Measured: 2048 tokens, 8192 -> 6144: 112 us, 1.84
+//    PFLOP/s.  About 750 cycles a block of inputs where the MMAs need 512: operands
+//    leave shared memory at 128 bytes a cycle and the reads of the accumulators take
+//    tensor-memory cycles from the MMAs.
 // Where the tiles do not fill the SMs, a cluster of up to 8 blocks shares a tile's
 // contraction; each leaves its sums in its own shared memory and adds up a part of
 // the tile from all of them, in rank order, so results do not depend on timing and
 // no workspace is needed.
+#include <algorithm>
+
 #include "tc_dev.cuh"
 
 namespace moe {
@@ -27,6 +36,8 @@ namespace {
 using namespace tc;
 
 __device__ int32_t g_err;  // flags since the last read
+
+constexpr int kMaxSplit = 8;  // blocks of a cluster: the portable size
 
 struct Params {
     int n_tokens, n_in, n_out, nb;
@@ -46,7 +57,7 @@ struct Cfg {
     static constexpr int kThreads = 128 + 32 * kEpi;
     static constexpr int kCols = TOKM ? 64 : BN;  // of a thread
     static constexpr uint32_t kA = 128 * 128, kB = BN * 128, kStage = kA + kB;
-    static constexpr int kStages = TOKM ? (BN == 256 ? 4 : 6) : BN == 16 ? 6 : BN == 32 ? 5 : 4;
+    static constexpr int kStages = TOKM ? (BN == 256 ? 4 : 6) : BN == 16 ? 6 : 5;
     static constexpr uint32_t kTmem = 2 * BN < 32 ? 32 : 2 * BN;  // a power of two
     static constexpr int kAcc = BN;                               // columns of an accumulator
     static constexpr size_t kSmem = kStages * kStage + 1024;
@@ -345,15 +356,13 @@ __global__ void __launch_bounds__(Cfg<TOKM, BN>::kThreads, TOKM ? 1 : 2)
 }
 
 template <bool TOKM, int BN, typename T>
-cudaError_t launch(const MoeFp8LinearArgs &a, Params p, int dev, int slots, cudaStream_t s) {
+cudaError_t launch(const MoeFp8LinearArgs &a, Params p, int dev, int sms, cudaStream_t s) {
     using C = Cfg<TOKM, BN>;
+    const int slots = (TOKM ? 1 : 2) * sms;  // blocks that run at once
     p.tiles_t = (a.n_tokens + (TOKM ? 127 : BN - 1)) / (TOKM ? 128 : BN);
     p.tiles_o = (a.n_out + (TOKM ? BN - 1 : 127)) / (TOKM ? BN : 128);
     const int64_t tiles = (int64_t)p.tiles_t * p.tiles_o;
     if (tiles > INT32_MAX / 16) return cudaErrorInvalidValue;
-    int split = 1;
-    while (split < 8 && (split + 1) * tiles <= slots && split + 1 <= p.nb) ++split;
-    p.split = split;
     CUtensorMap tok, mat;
     const int64_t td[3] = {a.n_in, a.n_tokens, 1}, md[3] = {a.n_in, a.n_out, 1};
     const int64_t in16 = (a.n_in + 15) / 16 * 16;
@@ -365,27 +374,51 @@ cudaError_t launch(const MoeFp8LinearArgs &a, Params p, int dev, int slots, cuda
     static SmemOnce once;
     if ((e = once.allow(reinterpret_cast<const void *>(fn), dev, C::kSmem)) != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim = {(unsigned)split, 1, 1};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)(split > 1 ? tiles * split : tiles < slots ? tiles : slots));
     c.blockDim = dim3(C::kThreads);
     c.dynamicSmemBytes = C::kSmem;
     c.stream = s;
     c.attrs = at;
+    // As many blocks a tile as find room at once: clusters lie within a GPC, so that of
+    // 152 SMs 15 clusters of 8 have one a block; a 16th makes two turns (128 tokens, 6144 ->
+    // 2048: 14 us, with 6 blocks a tile 9.4).
+    static std::atomic<int> room[kDevices][kMaxSplit + 1];  // clusters of so many blocks, one a SM
+    const int per_sm = slots / sms;
+    int split = (int)std::min<int64_t>(std::min(kMaxSplit, p.nb), std::max<int64_t>(slots / tiles, 1));
+    for (; split > 1; --split) {
+        int n = dev < kDevices ? room[dev][split].load(std::memory_order_relaxed) : 0;
+        if (n == 0) {
+            at[0].val.clusterDim = {(unsigned)split, 1, 1};
+            c.gridDim = dim3((unsigned)split);
+            c.numAttrs = 1;
+            if ((e = cudaOccupancyMaxActiveClusters(&n, fn, &c)) != cudaSuccess) return e;
+            n = std::max(std::min(n, sms / split), 1);
+            if (dev < kDevices) room[dev][split].store(n, std::memory_order_relaxed);
+        }
+        if ((int64_t)n * per_sm >= tiles) break;
+    }
+    p.split = split;
+    at[0].val.clusterDim = {(unsigned)split, 1, 1};
+    c.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, slots)));
     c.numAttrs = 2;
     return cudaLaunchKernelEx(&c, fn, TOKM ? tok : mat, TOKM ? mat : tok, p);
 }
 
 template <typename T>
 cudaError_t pick(const MoeFp8LinearArgs &a, const Params &p, int dev, int sms, cudaStream_t s) {
-    if (a.n_tokens <= 16) return launch<false, 16, T>(a, p, dev, 2 * sms, s);
-    if (a.n_tokens <= 32) return launch<false, 32, T>(a, p, dev, 2 * sms, s);
-    if (a.n_tokens <= 64) return launch<false, 64, T>(a, p, dev, 2 * sms, s);
-    const int64_t wide = (int64_t)((a.n_tokens + 127) / 128) * ((a.n_out + 255) / 256);
-    return wide >= sms ? launch<true, 256, T>(a, p, dev, sms, s) : launch<true, 128, T>(a, p, dev, sms, s);
+    // Measured, matrix rows on M and tokens on M: 32 tokens, 6144 -> 2048 7.2 and 7.6 us;
+    // 64 tokens, 6144 -> 2048 9.0 and 8.2, 2048 -> 12288 9.6 and 8.4, 8192 -> 6144 17.4 and 14.8
+    if (a.n_tokens <= 16) return launch<false, 16, T>(a, p, dev, sms, s);
+    if (a.n_tokens <= 32) return launch<false, 32, T>(a, p, dev, sms, s);
+    // A tile of 256 rows takes 1.5 times as long as one of 128. Measured, 128 and 256 rows:
+    // 300 tokens, 6144 -> 576 9.4 and 12.5 us; 512, 6144 -> 6144 37.1 and 29.1; 1024 54.7 and
+    // 55.7; 2048, 8192 -> 6144 141.6 and 111.7
+    const int64_t t = (a.n_tokens + 127) / 128, narrow = t * ((a.n_out + 127) / 128), wide = t * ((a.n_out + 255) / 256);
+    return 3 * ((wide + sms - 1) / sms) <= 2 * ((narrow + sms - 1) / sms) ? launch<true, 256, T>(a, p, dev, sms, s)
+                                                                          : launch<true, 128, T>(a, p, dev, sms, s);
 }
 
 }  // namespace

@@ -4,10 +4,10 @@
 // A tcgen05.mma costs the tensor core N/2 cycles (M = 128, 32 bytes of K a row),
 // at least what its operands take from shared memory at 128 bytes a cycle, if its
 // issuer keeps up.  Measured: M = 128: N = 256 128 cycles, 128 64, 64 48, 16 39; M
-// = 64: N = 64 32; A in tensor memory, N = 64: 32.  An issuer takes 60 to 90 cycles
-// an instruction inside a branch that one lane takes, 26 without a branch: the
-// whole warp runs along and a predicate picks the lane, the upper half of the
-// descriptors is a constant.  A test of a barrier and a fence take some 160.
+// = 64: N = 64 32; A in tensor memory, N = 64: 32.  An issuer takes some 36 cycles an
+// instruction where one branch that one lane takes holds a whole loop of them, up
+// to 90 where it holds one.  A commit takes 50; from a commit to a thread that waits
+// for its barrier 300 to 440 pass.
 #pragma once
 
 #include <atomic>
