@@ -18,16 +18,19 @@
 // 3300 cycles a SM (16-bit) or 1650 (E4M3).  Measured: a tile in 4100 (16-bit), since
 // two stages beside 72 KB of queries leave the chain load, S, softmax, O little to
 // overlap; 32-token tiles in four stages were slower (fixed costs an MMA and a
-// barrier).  64 requests of up to 16384 tokens, 128 heads: 133 us (2.05 TB/s of rows
-// read once from HBM and twice from L2); 2 of 131072 in E4M3, 64 heads: 85 us.
+// barrier).  64 requests of up to 16384 tokens, 128 heads: 127 us (2.2 TB/s of rows
+// read once from HBM and twice from L2); 2 of 131072 in E4M3, 64 heads: 81 us.
+// Prefetches to L2 two or three tiles ahead changed nothing (TMA) or cost 3 to 20%
+// (16-bit rows by prefetch instructions).
 //
 // - Work is split by cost: the tiles of all requests, and kSegCost more for each
 //   request, form one line; each block takes an equal run, found from the lengths
 //   by itself.  More than 64 heads form groups; the blocks of a run's groups are
 //   neighbours and read the same rows at the same time, once from HBM.
 // - Eight producer warps copy rows (cp.async, any page size and stride), issue TMA
-//   copies of them, or load E4M3 codes and widen them, into two stages of three parts;
-//   a part is used and given back by itself.  One warp issues the products S, another
+//   copies of them (a warp a part: 127 against 128 us), or load E4M3 codes and widen
+//   them, into two stages of three parts; S starts on a part when it is there, and a
+//   part is given back by itself.  One warp issues the products S, another
 //   the products O (one that issued both in turn let each wait for the other's
 //   barriers: 139 against 136 us); four warps do the softmax and write the results.
 // - The maximum moves only when a logit passes it by 2^kLazy; then O is scaled in
@@ -349,11 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             for (int k = 0; k < 4; ++k) m |= (b0 >> (8 * k) & 1) << k | (b1 >> (8 * k) & 1) << (4 + k);
             if (lane == 0) reinterpret_cast<volatile uint8_t *>(sm.valid[r.slot])[pw] = (uint8_t)m;
         };
-        const auto part_of = [&](int k) { return parts < kParts ? k : (k + kParts - 1) % kParts; };  // what only S reads is free first
         bool ok = true;
         if constexpr (LOAD == kByTma) {
-            // one warp waits and issues; the others join it where rows are copied.  Nobody leaves early: all
-            // warps meet at every barrier, whatever was given up
+            // a warp a part waits and issues; all copy where it goes row by row.  Nobody leaves early: all warps
+            // meet at every barrier, whatever was given up
             int issued[kStages] = {-1, -1};
             for (; now.have; now = nxt, nxt = fetch()) {
                 if (now.first) {
@@ -364,26 +366,26 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                 }
                 const uint32_t at = kOffK + (uint32_t)r.slot * kStageB;
                 if (now.whole) {
-                    if (pw == 0) {
-                        const int groups = kTile >> gshift;
-                        uint32_t lives = 0;
-                        for (int g = 0; g < groups; ++g)
-                            if ((uint32_t)__shfl_sync(0xffffffffu, now.page, g) < p.n_pages) lives |= 1u << g;
-                        for (int k = 0; k < parts; ++k) {
-                            const int j = part_of(k), n = min(4, chunks - 4 * j);
-                            ok = __all_sync(0xffffffffu, mb_wait(&sm.empty[r.slot][j], r.phase ^ 1, abort, &g_err) && ok);
-                            if (!ok) continue;
-                            // lane: a group of rows of a chunk, 32 of them at most; a page that is none reads as zeros
-                            const int g = lane & (groups - 1), c = 4 * j + lane / groups;
-                            const int id = __shfl_sync(0xffffffffu, now.page, g), off = __shfl_sync(0xffffffffu, now.off, g);
-                            if (lane == 0) mb_expect_tx(&sm.full[r.slot][j], (uint32_t)n * kChunk);
+                    const int groups = kTile >> gshift;
+                    uint32_t lives = 0;
+                    for (int g = 0; g < groups; ++g)
+                        if ((uint32_t)__shfl_sync(0xffffffffu, now.page, g) < p.n_pages) lives |= 1u << g;
+                    if (pw < parts) {
+                        // a part a warp; lane: a group of rows of a chunk, 32 of them at most; a page that is none reads as zeros
+                        const int n = min(4, chunks - 4 * pw), g = lane & (groups - 1), c = 4 * pw + lane / groups;
+                        const int id = __shfl_sync(0xffffffffu, now.page, g), off = __shfl_sync(0xffffffffu, now.off, g);
+                        ok = __all_sync(0xffffffffu, ok && mb_wait(&sm.empty[r.slot][pw], r.phase ^ 1, abort, &g_err));
+                        if (ok) {
+                            if (lane == 0) mb_expect_tx(&sm.full[r.slot][pw], (uint32_t)n * kChunk);
                             __syncwarp();
                             if (lane < n * groups)
                                 tma_3d(sbase + at + (uint32_t)c * kChunk + (uint32_t)(g << gshift) * 128u, &cmap, 64 * c,
-                                       lives >> g & 1 ? off : 0, lives >> g & 1 ? id : (int)p.n_pages, &sm.full[r.slot][j]);
-                            __syncwarp();
+                                       lives >> g & 1 ? off : 0, lives >> g & 1 ? id : (int)p.n_pages, &sm.full[r.slot][pw]);
+                            issued[r.slot] = (int)r.phase;
                         }
-                        if (ok) issued[r.slot] = (int)r.phase;
+                        __syncwarp();
+                    }
+                    if (pw == 0) {  // part 0 was free: the softmax has read what was there
                         if (lane < 8) reinterpret_cast<volatile uint8_t *>(sm.valid[r.slot])[lane] = lives >> (8 * lane >> gshift) & 1 ? 0xff : 0;
                         __syncwarp();
                         if (lane == 0) mb_arrive(&sm.valid_full[r.slot]);
@@ -404,11 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                 }
                 r.next(kStages);
             }
-            if (pw == 0 && *abort) {  // copies in flight land before the block ends
+            if (pw < parts && *abort) {  // copies in flight land before the block ends
                 const long long t = clock64();
                 for (int i = 0; i < kStages; ++i)
-                    for (int j = 0; j < parts && issued[i] >= 0; ++j)
-                        while (!mb_test(&sm.full[i][j], (uint32_t)issued[i]) && clock64() - t < kWaitClk) {}
+                    while (issued[i] >= 0 && !mb_test(&sm.full[i][pw], (uint32_t)issued[i]) && clock64() - t < kWaitClk) {}
             }
         } else {
             for (; now.have && ok; now = nxt, nxt = fetch()) {
@@ -465,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         const uint32_t dq = desc(sbase + kOffQ, 16), dk = desc(sbase + kOffK, 16);
         const uint32_t dv = desc(sbase + kOffK, kChunk), dp = desc(sbase + kOffP, 16);
         const int steps = p.dim / 16, parts = (steps + 15) / 16, mts = (p.latent + 127) / 128, own = (mts + 1) / 2;  // own: parts that O reads
+        const auto part_of = [&](int k) { return parts < kParts ? k : (k + kParts - 1) % kParts; };  // what only S reads comes first
         const bool lead = elect();
         const auto wait = [&](uint64_t *bar, uint32_t phase) { return __all_sync(0xffffffffu, mb_wait(bar, phase, abort, &g_err)); };
         Ring r;
@@ -480,22 +482,29 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
                     fence_async_smem();  // copied by the generic proxy
                 }
                 const bool last = w.t + 1 == w.te;
-                for (int j = 0; j < parts && ok; ++j) ok = wait(&sm.full[r.slot][j], r.phase);
                 // the buffer of the tile before the last: its logits are read
-                if (ok && i >= 2) ok = wait(&sm.s_empty[i & 1], (i >> 1 & 1) ^ 1);
-                if (!ok) break;
-                if (LOAD == kByRow) fence_async_smem();  // the copies landed by the generic proxy
-                tc_after_sync();
-                if (lead) {
-                    const uint32_t k = dk + (uint32_t)(r.slot * (int)(kStageB >> 4)), d = tmem + kColS + (i & 1) * kTile;
-                    for (int c = 0; c < steps / 4; ++c)
+                if (i >= 2) ok = wait(&sm.s_empty[i & 1], (i >> 1 & 1) ^ 1);
+                const uint32_t slot = dk + (uint32_t)(r.slot * (int)(kStageB >> 4)), d = tmem + kColS + (i & 1) * kTile;
+                for (int k = 0; k < parts && ok; ++k) {  // as they come
+                    const int j = part_of(k);
+                    if (!(ok = wait(&sm.full[r.slot][j], r.phase))) break;
+                    if (LOAD == kByRow) fence_async_smem();  // the copies landed by the generic proxy
+                    tc_after_sync();
+                    if (lead) {
+                        const int n = min(16, steps - 16 * j);
+                        for (int c = 4 * j; c < 4 * j + n / 4; ++c)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mma_f16(d, dq + (uint32_t)(c * (int)(kChunk >> 4) + 2 * e), k + (uint32_t)(c * (int)(kChunk >> 4) + 2 * e), id_s,
-                                    c + e != 0);
-                    for (int e = 0; e < steps % 4; ++e)
-                        mma_f16(d, dq + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * e),
-                                k + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * e), id_s, steps >= 4 || e != 0);
+                            for (int e = 0; e < 4; ++e)
+                                mma_f16(d, dq + (uint32_t)(c * (int)(kChunk >> 4) + 2 * e), slot + (uint32_t)(c * (int)(kChunk >> 4) + 2 * e),
+                                        id_s, k + (c - 4 * j) + e != 0);
+                        for (int e = 0; e < n % 4; ++e)
+                            mma_f16(d, dq + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * e),
+                                    slot + (uint32_t)(steps / 4 * (int)(kChunk >> 4) + 2 * e), id_s, k + n / 4 + e != 0);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (lead) {
                     mma_commit(&sm.s_full[i & 1]);
                     for (int e = own; e < parts; ++e) mma_commit(&sm.empty[r.slot][e]);
                     if (last) mma_commit(&sm.q_empty);

@@ -9,22 +9,30 @@
 //
 // - Narrow heads (values up to 128, keys up to 192 dimensions): a block holds 256
 //   queries as two streams that share the keys; while one stream's softmax runs,
-//   the tensor core works for the other (512 columns: S and O of both).  Wide heads
-//   (to 256): 128 queries, S of two tiles in turn, one O of 256 columns; both
-//   groups of softmax warps work on one tile, half the columns each.
+//   the tensor core works for the other (512 columns: S and O of both).  A warp a
+//   stream issues its products (one for both: 112 against 95 us for 2048 tokens).  Wide
+//   heads (to 256), and few blocks of 256 queries: 128 queries, S of two tiles in turn,
+//   one O of 256 columns; one warp issues S, another PV, and both groups of softmax
+//   warps work on one tile, half the columns each.
 //   In both the order is S(0), S(1), PV(0), S(2), PV(1), ... over the steps, where
 //   step k + 2 reuses the S buffer of step k.
 // - A softmax thread holds a row (narrow) or half a row of logits in registers: no
 //   shuffles.  The maximum moves only when a logit passes it by 2^kLazy; then the
 //   row of O is scaled in tensor memory.  Weights are rounded to the operand type
 //   (their sum is not), for f16 times 2^7, so that its subnormals begin at 2^-31.
-// - One warp brings tiles by TMA into a ring of 16 KB slots: 128 keys by 64
-//   dimensions, or as many rows of V as fit.  What lies outside a tensor reads as
+// - One warp brings tiles by TMA into a ring of 16 KB slots, several lanes at once: 128
+//   keys by 64 dimensions, or as many rows of V as fit; tiles are handed on in halves
+//   (narrow) or slots (wide).  What lies outside a tensor reads as
 //   zeros; rows of V behind a request's last key, which belong to others, are set
 //   to zero (a weight of 0 does not hide a NaN).
 // - Blocks are persistent; work items (request, 256 or 128 queries, head) go to them
 //   in turn and back, a request's last queries first: the longest come first where
 //   the mask is causal.
+//
+// Measured: 2048 tokens, 64 heads of 128 + 64 / 128, causal: 92 us, 0.94 PFLOP/s; 1000
+// queries over 5000 keys, 32 heads of 192 + 64 / 256: 156 us, 0.94.  What bounds it is the
+// chain of a step: some 300 to 440 cycles from a product's end to whoever waits for it, twice, and
+// the softmax between (two steps of both streams 4560 cycles, their MMAs 2560).
 #include <type_traits>
 
 #include "tc_dev.cuh"
@@ -435,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 const auto keys = [&](int j) { return wait(&sm.full[(tile + 2 * j) % kTiles], (tile + 2 * j) / kTiles & 1); };
                 // The second stream starts when the first has weights: the products of one then
-                // run under the softmax of the other (in step they cost 97 us where 87 do).
+                // run under the softmax of the other (8 heads of 8192 tokens 162 us, without it 172;
+                // 20 x 300, 16 heads 41.2 and 39.8; 64 heads of 2048 92 either way).
                 if (g == 1 && mine && other) ok = wait(&sm.p_ready[0][0], theirs);
                 theirs ^= other & 1;
                 if (!ok) break;
