@@ -200,3 +200,23 @@ def test_int32_offsets_are_passed(moe):
     x8, xs, w8, ws = operands(n, inner, outer, 4)
     out = moe.fp8_linear(x8, xs, w8, ws)
     check(out[-130:], x8[-130:], xs[-130:], w8, ws)
+
+
+def test_quant_offsets_beyond_32_bits(moe):
+    step = 1 << 30
+    x = torch.randn((5, 272), device="cuda").half()
+    big, codes = (torch.empty(4 * step + 512, dtype=t, device="cuda") for t in (torch.float16, torch.uint8))
+    xf, cf = (torch.as_strided(b, (5, 272), (step, 1)) for b in (big, codes))
+    xf.copy_(x)
+    want, ws = moe.quant_act_fp8(x)
+    got, s = moe.quant_act_fp8(xf, x8=cf)
+    assert torch.equal(got, want.view(torch.uint8)) and torch.equal(s, ws)
+
+
+def test_as_many_blocks_as_find_room(moe):
+    """Tile counts around what clusters of every size hold at once, with contractions to split."""
+    for n, inner, outer in ((128, 1152, 1024), (128, 1152, 1920), (130, 1152, 1920), (128, 1152, 2944), (200, 640, 3584),
+                            (128, 1152, 6144), (128, 256, 9728), (20, 1152, 5888), (20, 1152, 6144), (40, 1152, 19456)):
+        x8, xs, w8, ws = operands(n, inner, outer, n + outer)
+        check(moe.fp8_linear(x8, xs, w8, ws, dtype=torch.float32), x8, xs, w8, ws)
+    assert moe.dense_status() == 0

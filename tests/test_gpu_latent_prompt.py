@@ -221,3 +221,81 @@ def test_repeats_graph_and_streams(moe):
         ks.copy_(starts(nk))
         graph.replay()
         check(out, lse, *a, 0.07, True)
+
+
+def some(a, out, lse, step=31):
+    """Inputs and outputs of a few heads, for the check."""
+    q, k, kr, v, qs, ks = a
+    h = slice(None, None, step)
+    return out[:, h], lse[:, h], q[:, h], k[:, h], kr, v[:, h], qs, ks
+
+
+# with so many heads a block holds 256 queries as two streams, where heads are narrow
+@pytest.mark.parametrize("nope,rope,v", [(128, 64, 128), (64, 32, 64), (96, 64, 80), (16, 0, 16), (112, 48, 112), (128, 16, 128)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_head_sizes_of_many_heads(moe, nope, rope, v, dt):
+    a = setup([70, 200], [70, 333], 160, nope, rope, v, dt, seed=nope + v, spare=5)
+    for causal in (True, False):
+        out, lse = moe.latent_prompt(*a, 1 / math.sqrt(nope + rope), causal=causal)
+        check(*some(a, out, lse), 1 / math.sqrt(nope + rope), causal)
+    assert moe.dense_status() == 0
+
+
+@pytest.mark.parametrize("nq,nk", RAGGED)
+@pytest.mark.parametrize("causal", [True, False])
+def test_ragged_lengths_of_many_heads(moe, nq, nk, causal):
+    a = setup(nq, nk, 160, 128, 64, 128, torch.bfloat16, seed=sum(nq), spare=3)
+    out, lse = moe.latent_prompt(*a, 0.07, causal=causal)
+    check(*some(a, out, lse), 0.07, causal)
+    assert moe.dense_status() == 0
+
+
+@pytest.mark.parametrize("nope,rope,v", [(208, 48, 64), (240, 16, 16), (192, 64, 128)])
+def test_wide_keys_and_narrow_values(moe, nope, rope, v):
+    a = setup([70, 200], [70, 333], 3, nope, rope, v, torch.bfloat16, seed=nope + v, spare=5)
+    for causal in (True, False):
+        out, lse = moe.latent_prompt(*a, 1 / math.sqrt(nope + rope), causal=causal)
+        check(out, lse, *a, 1 / math.sqrt(nope + rope), causal)
+
+
+def test_neighbours_of_many_heads(moe):
+    """Infinities and NaN in other rows change nothing, rows of no request stay."""
+    a = setup([50, 300, 70], [100, 300, 130], 160, 128, 64, 128, torch.bfloat16, seed=6)
+    q, k, kr, v, qs, ks = a
+    want, wl = moe.latent_prompt(*a, 0.07)
+    for t, s in ((q, qs), (k, ks), (kr, ks), (v, ks)):
+        t[:int(s[1])] = math.nan
+        t[int(s[2]):] = math.inf
+    out, lse = torch.full_like(want, 7.0), torch.full_like(wl, 7.0)
+    moe.latent_prompt(q, k, kr, v, qs[1:3].contiguous(), ks[1:3].contiguous(), 0.07, out=out, lse=lse)
+    at = slice(50, 350)
+    assert torch.equal(out[at], want[at]) and torch.equal(lse[at], wl[at])
+    for t in (out, lse):
+        assert bool((t[:50] == 7).all()) and bool((t[350:] == 7).all())
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_far_apart_logits_of_many_heads(moe, dt):
+    a = setup([300], [900], 160, 64, 32, 64, dt, seed=12, std=3.0)
+    out, lse = moe.latent_prompt(*a, 0.3)
+    check(*some(a, out, lse), 0.3, True)
+
+
+def test_offsets_beyond_32_bits(moe):
+    """Tokens 2^23 elements apart: rows beyond 2^31 elements of every tensor."""
+    heads, step = 2, 1 << 23
+    a = setup([150, 130], [170, 150], heads, 128, 64, 128, torch.bfloat16, seed=13)
+    q, k, kr, v, qs, ks = a
+    want, wl = moe.latent_prompt(*a, 0.07)
+    big, room = (torch.empty(330 * step, dtype=torch.bfloat16, device="cuda") for _ in range(2))  # 5.5 GB each
+
+    def far(t, at):
+        shape = t.shape
+        inner = (shape[2], 1) if t.dim() == 3 else (1,)
+        f = torch.as_strided(big, shape, (step,) + inner, at)
+        f.copy_(t)
+        return f
+    out = torch.as_strided(room, want.shape, (step, 128, 1), 64)
+    got, gl = moe.latent_prompt(far(q, 0), far(k, 4096), far(kr, 8192), far(v, 12288), qs, ks, 0.07, out=out)
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+    check(got, gl, *a, 0.07, True)
