@@ -884,7 +884,7 @@ cudaError_t launch_join(Params &p, cudaStream_t s) {
     // by the pieces a request has at most. Measured, decode and join of requests of up to
     // 3000 tokens, 64 heads, W = 1 2 4 8: 2 requests 20.1 17.0 15.5 14.7 us; 4: 29.0 21.2
     // 17.4 18.7; 8: 23.9 19.7 21.2 23.1; 18: 25.0 27.3 30.0 37.1
-    const int W = 3 * n <= p.runs ? 8 : 6 * n <= p.runs ? 4 : 12 * n <= p.runs ? 2 : 1;
+    const int W = 50 * n <= p.runs ? 8 : 25 * n <= p.runs ? 4 : 12 * n <= p.runs ? 2 : 1;
     const void *fn = W == 8 ? reinterpret_cast<const void *>(latent_join_kernel<T, 8>)
                      : W == 4 ? reinterpret_cast<const void *>(latent_join_kernel<T, 4>)
                      : W == 2 ? reinterpret_cast<const void *>(latent_join_kernel<T, 2>)

@@ -222,3 +222,15 @@ def test_offsets_beyond_32_bits(moe):
     q, n = normal(g, (1, 64, dim), torch.bfloat16), torch.tensor([250], dtype=torch.int32, device="cuda")
     out, lse = moe.LatentAttention(1, 64).decode(q, cache, table, n, 0.07)
     check(out, lse, q, cache, table, n, 512, 0.07)
+
+
+@pytest.mark.parametrize("n,heads", [(1, 64), (3, 64), (5, 40), (6, 128), (11, 64), (13, 100), (30, 64)])
+def test_joins_of_many_pieces(moe, n, heads):
+    """Few and more requests, each over several blocks."""
+    lens = [1400 + 97 * i % 900 for i in range(n)]
+    q, cache, table, ln = setup(lens, heads, 512, 64, torch.bfloat16, torch.bfloat16, 64, seed=n)
+    attn = moe.LatentAttention(n, heads)
+    out, lse = attn.decode(q, cache, table, ln, 0.07)
+    check(out, lse, q, cache, table, ln, 512, 0.07)
+    again = attn.decode(q, cache, table, ln, 0.07)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
