@@ -18,8 +18,8 @@
 // 3300 cycles a SM (16-bit) or 1650 (E4M3).  Measured: a tile in 4100 (16-bit), since
 // two stages beside 72 KB of queries leave the chain load, S, softmax, O little to
 // overlap; 32-token tiles in four stages were slower (fixed costs an MMA and a
-// barrier).  64 requests of up to 16384 tokens, 128 heads: 127 us (2.2 TB/s of rows
-// read once from HBM and twice from L2); 2 of 131072 in E4M3, 64 heads: 81 us.
+// barrier).  64 requests of up to 16384 tokens, 128 heads: 124 us (2.2 TB/s of rows
+// read once from HBM and twice from L2); 2 of 131072 in E4M3, 64 heads: 82 us.
 // Prefetches to L2 two or three tiles ahead changed nothing (TMA) or cost 3 to 20%
 // (16-bit rows by prefetch instructions).
 //
@@ -746,10 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 }
 
 // Joins the pieces of the requests that several runs share.  A block takes 32
-// latent dimensions of a request and head group (or all of them in turn, where
-// requests outnumber the runs and few are shared), a lane one of them for 8 heads
-// (32 contiguous bytes a piece); W of its 8 warps take 8 heads, each a part of the
-// runs.
+// latent dimensions of a request and head group, or several times 32 in turn, a lane one
+// of them for 8 heads (32 contiguous bytes a piece); W of its 8 warps take 8 heads, each
+// a part of the runs.
 constexpr int kMaxRuns = 152;
 constexpr int kBatch = 6;  // pieces that a lane loads at once
 template <typename T, int W>
@@ -885,6 +884,12 @@ cudaError_t launch_join(Params &p, cudaStream_t s) {
     // 3000 tokens, 64 heads, W = 1 2 4 8: 2 requests 20.1 17.0 15.5 14.7 us; 4: 29.0 21.2
     // 17.4 18.7; 8: 23.9 19.7 21.2 23.1; 18: 25.0 27.3 30.0 37.1
     const int W = 50 * n <= p.runs ? 8 : 25 * n <= p.runs ? 4 : 12 * n <= p.runs ? 2 : 1;
+    // Blocks a request: by 32 columns; by 64 where those make more than three blocks an SM (30
+    // requests of up to 3000 tokens 31.6 and, by 32, 32.6 us, 64 of 6000 with 128 heads 138 and
+    // 142; 18 of 3000 29.2 and 24.8); four beyond the runs, where most have nothing to join (300
+    // of 300: 55 us, with one block 76, 16 61), one for thousands (8192 of 40: 289, with four 317)
+    const int by32 = p.latent / 32;
+    const int columns = n > 16 * p.runs ? 1 : n > p.runs ? (by32 < 4 ? by32 : 4) : n * by32 > 3 * p.runs ? by32 / 2 : by32;
     const void *fn = W == 8 ? reinterpret_cast<const void *>(latent_join_kernel<T, 8>)
                      : W == 4 ? reinterpret_cast<const void *>(latent_join_kernel<T, 4>)
                      : W == 2 ? reinterpret_cast<const void *>(latent_join_kernel<T, 2>)
@@ -893,7 +898,7 @@ cudaError_t launch_join(Params &p, cudaStream_t s) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)(n * p.groups), n <= p.runs ? (unsigned)(p.latent / 32) : 1u,
+    c.gridDim = dim3((unsigned)(n * p.groups), (unsigned)columns,
                      (unsigned)((p.per_group + 7) / 8 * W + 7) / 8);
     c.blockDim = dim3(256);
     c.stream = s;
