@@ -18,7 +18,7 @@
 // 3300 cycles a SM (16-bit) or 1650 (E4M3).  Measured: a tile in 4100 (16-bit), since
 // two stages beside 72 KB of queries leave the chain load, S, softmax, O little to
 // overlap; 32-token tiles in four stages were slower (fixed costs an MMA and a
-// barrier).  64 requests of up to 16384 tokens, 128 heads: 124 us (2.2 TB/s of rows
+// barrier).  64 requests of up to 16384 tokens, 128 heads: 120 us (2.3 TB/s of rows
 // read once from HBM and twice from L2); 2 of 131072 in E4M3, 64 heads: 82 us.
 // Prefetches to L2 two or three tiles ahead changed nothing (TMA) or cost 3 to 20%
 // (16-bit rows by prefetch instructions).
@@ -63,7 +63,10 @@ constexpr int kThreads = 32 * (4 + 2 + kProd);  // softmax, two that issue MMAs,
 constexpr uint32_t kOffQ = 0, kOffK = kStageB, kOffP = kOffK + kStages * kStageB;
 constexpr size_t kSmem = kOffP + kHeads * 128 + 1024;
 constexpr uint32_t kColS = 256;       // tensor memory: O 4 x 64 columns, then S twice
-constexpr int kSegCost = 2;           // what a request costs besides its tiles, in tiles
+// What a request costs besides its tiles, in tiles.  Measured with 1 2 3 4: 64 requests of up to
+// 16384 tokens, 128 heads 135.5 123.8 120.4 121.5 us, 300 of 300 63.4 55.3 56.4 53.4, 200 of 3000
+// 128.0 127.5 125.3 125.1, 2000 of 100 177 174 171 171
+constexpr int kSegCost = 3;
 constexpr float kLazy = 8.f;
 constexpr float kFloor = -3.4028235e38f;  // maximum before any token: no logit lies below
 constexpr float kLog2e = 1.4426950408889634f;
