@@ -48,6 +48,7 @@ constexpr uint32_t kSlot = 16384;
 constexpr int kTiles = 8;         // narrow: tiles of keys or values in flight, at most
 constexpr int kSlots = 14;        // slots of the ring, at most
 constexpr int kThreads = 352;     // 8 softmax warps, two that issue MMAs, one TMA warp
+constexpr long long kStartClk = 20000;  // cycles that the second stream waits for the first to be ahead, at most
 constexpr float kLazy = 8.f;
 constexpr float kFloor = -3.4028235e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -68,6 +69,7 @@ struct Shared {
     uint64_t full[kSlots], empty[kSlots], q_full[2], q_empty[2], v_fixed[2], s_full[2], p_ready[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem;
     int abort;
+    int began;                    // narrow: behind the last item whose first stream has weights
     float top[2][2][128];         // wide heads: the halves' row maxima, by the step's parity
 };
 
@@ -211,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mb_init(&sm.o_empty[i], NQ == 2 ? 4 : 8);
         }
         sm.abort = 0;
+        sm.began = 0;
         mb_init_done();
         tma_prefetch(&qmap);
         tma_prefetch(&kmap);
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool firsts = warp == 8;
         if (NQ == 2) {
             const int g = warp - 8;
-            uint32_t oe = 0, theirs = 0;   // theirs: the parity of the other stream's tiles so far
+            uint32_t oe = 0;
             const uint32_t sd = tmem + 128 * g, od = tmem + kColO + 128 * g, q = dq + (uint32_t)(g * nk * (int)(kSlot >> 4));
             for (int it = 0; ok && cur.item(p, it, x); ++it) {
                 if (!x.n) continue;
@@ -443,11 +446,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 const auto keys = [&](int j) { return wait(&sm.full[(tile + 2 * j) % kTiles], (tile + 2 * j) / kTiles & 1); };
                 // The second stream starts when the first has weights: the products of one then
-                // run under the softmax of the other (8 heads of 8192 tokens 162 us, without it 172;
-                // 20 x 300, 16 heads 41.2 and 39.8; 64 heads of 2048 92 either way).
-                if (g == 1 && mine && other) ok = wait(&sm.p_ready[0][0], theirs);
-                theirs ^= other & 1;
-                if (!ok) break;
+                // run under the softmax of the other (8 heads of 8192 tokens 159 us, without it 172;
+                // 20 x 300, 16 heads 41.0 and 39.8; 64 heads of 2048 92 either way).  This is for
+                // speed alone, and the first stream may be tiles or an item further by now: so it is a
+                // count, compared, and given up after a while (a barrier's parity would come round).
+                if (g == 1 && mine && other) {
+                    const long long t = clock64();
+                    while (*(volatile int *)&sm.began <= it && !*abort && clock64() - t < kStartClk) {}
+                    __syncwarp();
+                }
                 if (mine) {
                     if (!(ok = keys(0))) break;
                     tc_after_sync();
@@ -666,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_before_sync();
                 __syncwarp();
                 if (lane == 0) mb_arrive(&sm.p_ready[b][ph]);
+                if (NQ == 2 && j == 0 && tid == 0) *(volatile int *)&sm.began = it + 1;
                 if (NQ == 1 || half) ++step;
             }
             if (NQ == 1) {                             // the row's whole sum

@@ -299,3 +299,27 @@ def test_offsets_beyond_32_bits(moe):
     got, gl = moe.latent_prompt(far(q, 0), far(k, 4096), far(kr, 8192), far(v, 12288), qs, ks, 0.07, out=out)
     assert torch.equal(got, want) and torch.equal(gl, wl)
     check(got, gl, *a, 0.07, True)
+
+
+# two streams: more tiles of keys in the ring than one, or just one (the last)
+@pytest.mark.parametrize("nope,rope,v", [(128, 0, 128), (64, 64, 128), (64, 32, 64), (64, 0, 64), (128, 64, 64), (128, 64, 128)])
+@pytest.mark.parametrize("nq,nk", [
+    ([256] * 11, [384, 256] * 5 + [384]),                       # (2, 3) and (1, 2) tiles, five items a block
+    ([256] + [0] * 500 + [256, 256] + [0] * 900 + [256] * 2, [256] + [9] * 500 + [384, 384] + [0] * 900 + [384] * 2),
+    ([256, 128, 200, 256, 300, 256, 40], [512, 128, 333, 384, 300, 640, 384]),
+])
+def test_streams_that_run_apart(moe, nope, rope, v, nq, nk):
+    """Several items a block, logits that grow towards the diagonal (O is scaled in both halves of each tile),
+    searches past many empty requests."""
+    q, k, kr, val, qs, ks = setup(nq, nk, 64, nope, rope, v, torch.bfloat16, seed=nope + v + len(nq), spare=2)
+    scale = 0.07
+    q[..., 0] = 4.0
+    k[:-2, :, 0] = torch.cat([torch.arange(n, device="cuda") for n in nk])[:, None] * (0.125 / (4 * scale))
+    a = (q, k, kr, val, qs, ks)
+    out, lse = moe.latent_prompt(*a, scale)
+    assert moe.dense_status() == 0
+    check(*some(a, out, lse, 21), scale, True)
+    for _ in range(20):
+        again, al = moe.latent_prompt(*a, scale)
+        assert torch.equal(again[:sum(nq)], out[:sum(nq)]) and torch.equal(al[:sum(nq)], lse[:sum(nq)])
+    assert moe.dense_status() == 0
