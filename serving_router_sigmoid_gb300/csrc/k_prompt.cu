@@ -47,6 +47,12 @@ __device__ int32_t g_err;  // flags since the last read
 constexpr uint32_t kSlot = 16384;
 constexpr int kTiles = 8;         // narrow: tiles of keys or values in flight, at most
 constexpr int kSlots = 14;        // slots of the ring, at most
+// Tiles of values whose last rows are cleared, in flight at most (one an item).  The copies
+// come to an item once S of the item before is complete; that S (wide, items of one
+// tile) needs PV of the item two further back at most, by its two buffers.  So when an
+// item's rows are cleared, those of the third one before have been waited for, and of
+// three in flight none may share a barrier.
+constexpr int kFixes = 4;
 constexpr int kThreads = 352;     // 8 softmax warps, two that issue MMAs, one TMA warp
 constexpr long long kStartClk = 20000;  // cycles that the second stream waits for the first to be ahead, at most
 constexpr float kLazy = 8.f;
@@ -66,7 +72,7 @@ struct Params {
 };
 
 struct Shared {
-    uint64_t full[kSlots], empty[kSlots], q_full[2], q_empty[2], v_fixed[2], s_full[2], p_ready[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
+    uint64_t full[kSlots], empty[kSlots], q_full[2], q_empty[2], v_fixed[kFixes], s_full[2], p_ready[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem;
     int abort;
     int began;                    // narrow: behind the last item whose first stream has weights
@@ -201,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mb_init(&sm.full[i], 1);
             mb_init(&sm.empty[i], NQ);  // the streams
         }
+        for (int i = 0; i < kFixes; ++i) mb_init(&sm.v_fixed[i], 1);
         for (int i = 0; i < 2; ++i) {
-            mb_init(&sm.v_fixed[i], 1);  // in turn: the copies are an item ahead at most
             mb_init(&sm.q_full[i], 1);
             mb_init(&sm.q_empty[i], 1);
             mb_init(&sm.s_full[i], 1);
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mb_arrive(&sm.v_fixed[fixes & 1]);
+                if (lane == 0) mb_arrive(&sm.v_fixed[fixes % kFixes]);
                 ++fixes;
             };
             // a slot's part of a tile: chunk c of the keys, or rows of the values
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (live < 128) ++fixes;
                     if (ok && j < mine) {
                         const int steps = (min(live, 128) + 15) / 16;
-                        ok = wait(&sm.full[t % kTiles], t / kTiles & 1) && (live >= 128 || wait(&sm.v_fixed[fix & 1], fix >> 1 & 1)) &&
+                        ok = wait(&sm.full[t % kTiles], t / kTiles & 1) && (live >= 128 || wait(&sm.v_fixed[fix % kFixes], fix / kFixes & 1)) &&
                              (j || wait(&sm.o_empty[g], oe ^ 1)) && wait(&sm.p_ready[g][0], uses[0]);
                         if (!ok) break;
                         if (!j) oe ^= 1;
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < x.n && ok; ++j) {
                     const int live = x.nk - 128 * j, steps = (min(live, 128) + 15) / 16, b = (int)(step++ & 1);
                     if (live < 128) {
-                        if (!(ok = wait(&sm.v_fixed[fixes & 1], fixes >> 1 & 1))) break;
+                        if (!(ok = wait(&sm.v_fixed[fixes % kFixes], fixes / kFixes & 1))) break;
                         ++fixes;
                     }
                     if (!(ok = (j || wait(&sm.o_empty[0], oe ^ 1)) && wait(&sm.p_ready[b][0], uses[b]))) break;

@@ -323,3 +323,24 @@ def test_streams_that_run_apart(moe, nope, rope, v, nq, nk):
         again, al = moe.latent_prompt(*a, scale)
         assert torch.equal(again[:sum(nq)], out[:sum(nq)]) and torch.equal(al[:sum(nq)], lse[:sum(nq)])
     assert moe.dense_status() == 0
+
+
+@pytest.mark.parametrize("nope,rope,v", [(64, 32, 64), (128, 0, 128), (64, 0, 16), (128, 64, 64), (192, 64, 256)])
+@pytest.mark.parametrize("gap", [0, 70])
+def test_many_items_of_one_tile(moe, nope, rope, v, gap):
+    """One stream, dozens of items a block, each of one tile with rows behind its last key; `gap` requests
+    without queries between those that have some."""
+    g = torch.Generator().manual_seed(gap)
+    nk = [int(x) for x in torch.randint(1, 128, (100,), generator=g)]
+    nq = [min(1 + i % 3, n) for i, n in enumerate(nk)]
+    nq = [x for n in nq for x in [n] + [0] * gap]
+    nk = [x for n in nk for x in [n] + [0] * gap]
+    a = setup(nq, nk, 64, nope, rope, v, torch.bfloat16, seed=nope + gap, spare=1)
+    for causal in (True, False):
+        out, lse = moe.latent_prompt(*a, 0.1, causal=causal)
+        assert moe.dense_status() == 0
+        check(*some(a, out, lse), 0.1, causal)
+        for _ in range(20):
+            again, _ = moe.latent_prompt(*a, 0.1, causal=causal)
+            assert torch.equal(again[:sum(nq)], out[:sum(nq)])
+    assert moe.dense_status() == 0

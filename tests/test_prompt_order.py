@@ -216,6 +216,122 @@ def two_streams(b, items, nk, nv, slots, tiles_max, fixes_n, start):
     return b.run([copies(), issue(0), issue(1), softmax(0), softmax(1)])
 
 
+def one_stream(b, items, nk, nv, slots, fixes_n):
+    """items: (tiles, whether the last one is cleared)."""
+    bars = lambda n: [Barrier() for _ in range(n)]  # noqa: E731
+    full, empty, v_fixed = bars(slots), bars(slots), bars(fixes_n)
+    q_full, q_empty, o_full, o_empty = (Barrier() for _ in range(4))
+    s_full, p_ready, pv_done = bars(2), bars(2), bars(2)
+
+    def copies():
+        here = qp = fixes = 0
+
+        def bring(n):
+            nonlocal here
+            for _ in range(n):
+                yield "wait", empty[here % slots], here // slots & 1 ^ 1
+                b.later(COPY, full[here % slots])
+                here += 1
+
+        def values(cleared):
+            nonlocal fixes
+            begin = here
+            yield from bring(nv)
+            if cleared:
+                for at in range(begin, begin + nv):
+                    yield "wait", full[at % slots], at // slots & 1
+                yield "for", b.delay(200)
+                b.arrive(v_fixed[fixes % fixes_n])
+                fixes += 1
+        for n, cleared in items:
+            yield "for", b.delay(LOOKUP)
+            yield "wait", q_empty, qp ^ 1
+            b.later(COPY, q_full)
+            for j in range(n):
+                yield from bring(nk)
+                if j:
+                    yield from values(False)
+            yield from values(cleared)
+            qp ^= 1
+
+    def products_s():
+        at = step = qf = began = 0
+        uses = [0, 0]
+        for n, _ in items:
+            yield "for", b.delay(LOOKUP)
+            yield "wait", q_full, qf
+            qf ^= 1
+            end = 0
+            for j in range(n):
+                k = step & 1
+                step += 1
+                if began >> k & 1:
+                    yield "wait", pv_done[k], uses[k] ^ 1
+                began |= 1 << k
+                uses[k] ^= 1
+                for c in range(nk):
+                    yield "wait", full[at % slots], at // slots & 1
+                    end = b.product(250)
+                    b.commit(empty[at % slots], end)
+                    if c + 1 == nk:
+                        b.commit(s_full[k], end)
+                    at += 1
+                if j:
+                    at += nv
+            b.commit(q_empty, end)
+            at += nv
+
+    def products_o():
+        at = step = fixes = oe = 0
+        uses = [0, 0]
+        for n, cleared in items:
+            yield "for", b.delay(LOOKUP)
+            at += nk * min(n, 2)
+            for j in range(n):
+                k = step & 1
+                step += 1
+                if cleared and j == n - 1:
+                    yield "wait", v_fixed[fixes % fixes_n], fixes // fixes_n & 1
+                    fixes += 1
+                if j == 0:
+                    yield "wait", o_empty, oe ^ 1
+                    oe ^= 1
+                yield "wait", p_ready[k], uses[k]
+                uses[k] ^= 1
+                for i in range(nv):
+                    yield "wait", full[at % slots], at // slots & 1
+                    end = b.product(128)
+                    b.commit(empty[at % slots], end)
+                    if i + 1 == nv:
+                        b.commit(pv_done[k], end)
+                        if j + 1 == n:
+                            b.commit(o_full, end)
+                    at += 1
+                if j + 2 < n:
+                    at += nk
+
+    def softmax():
+        sf, pd, of, step = [0, 0], [0, 0], 0, 0
+        for n, _ in items:
+            yield "for", b.delay(LOOKUP)
+            for j in range(n):
+                k = step & 1
+                step += 1
+                yield "wait", s_full[k], sf[k]
+                sf[k] ^= 1
+                if j and b.r.random() < 0.5:
+                    yield "wait", pv_done[k ^ 1], pd[k ^ 1] ^ 1
+                    yield "for", b.delay(RESCALE)
+                pd[k] ^= 1
+                yield "for", b.delay(SOFTMAX)
+                b.arrive(p_ready[k])
+            yield "wait", o_full, of
+            of ^= 1
+            yield "for", b.delay(600)
+            b.arrive(o_empty)
+    return b.run([copies(), products_s(), products_o(), softmax()])
+
+
 def ring(chunks, streams):
     """Slots of the ring: 13 of 16 KB hold the ring and the queries."""
     return 13 - streams * chunks
@@ -223,6 +339,7 @@ def ring(chunks, streams):
 
 # chunks of 64 key dimensions, slots of a tile of values
 TWO = [(1, 1), (1, 2), (2, 1), (2, 2), (3, 1), (3, 2)]
+ONE = TWO + [(4, 4), (4, 1), (2, 4)]
 
 
 def draw_two(r):
@@ -237,14 +354,26 @@ def draw_two(r):
 def test_two_streams_come_to_their_end(nk, nv):
     for seed in range(300):
         items = draw_two(random.Random(seed))
-        assert two_streams(Block(seed), items, nk, nv, ring(nk, 2), constant("kTiles"), 2, "count"), (seed, items)
+        assert two_streams(Block(seed), items, nk, nv, ring(nk, 2), constant("kTiles"), constant("kFixes"), "count"), (seed, items)
+
+
+@pytest.mark.parametrize("nk,nv", ONE)
+def test_one_stream_comes_to_its_end(nk, nv):
+    for seed in range(300):
+        r = random.Random(seed)
+        items = [(r.choice([1, 1, 1, 2, 3]), r.random() < 0.8) for _ in range(r.randint(1, 8))]
+        assert one_stream(Block(seed), items, nk, nv, ring(nk, 1), constant("kFixes")), (seed, items)
 
 
 def test_the_model_sees_a_phase_that_is_missed():
-    """A start by the parity of the first stream's weights is overtaken."""
+    """A start by the parity of the first stream's weights, and two barriers of cleared rows, are each overtaken."""
     def two(seed):
-        return two_streams(Block(seed), [((2, 3), False)] * 3, 2, 2, ring(2, 2), 8, 2, "parity")
+        return two_streams(Block(seed), [((2, 3), False)] * 3, 2, 2, ring(2, 2), 8, 4, "parity")
+
+    def one(seed):
+        return one_stream(Block(seed), [(1, True)] * 8, 2, 1, ring(2, 1), 2)
     assert not all(two(s) for s in range(300))
+    assert not all(one(s) for s in range(300))
 
 
 def test_the_second_stream_starts_by_a_count():
@@ -255,6 +384,6 @@ def test_the_second_stream_starts_by_a_count():
 
 def test_slots_of_the_ring():
     """227 KB less the rest of a block's shared memory are 13 slots."""
-    shared = 8 * (2 * constant("kSlots") + 2 * 10) + 4 * (3 + 512)  # barriers; flags and row maxima
+    shared = 8 * (2 * constant("kSlots") + constant("kFixes") + 2 * 9) + 4 * (3 + 512)  # barriers; flags and row maxima
     room = 227 * 1024 - 1024 - shared - 64
     assert room // 16384 == 13 and room - 13 * 16384 > 64
