@@ -65,13 +65,16 @@ struct Cfg {
     static constexpr int kPitch = TOKM ? BN + 4 : 128;
     static constexpr size_t kPart = (size_t)(TOKM ? 128 : BN) * kPitch * 4;
     static_assert(kPart <= kStages * kStage, "the sums take the stages' place");
+    static_assert(TOKM || BN <= 32, "columns of Shared::sc");
 };
 
 struct Shared {
     uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
-    float sc[4][64];  // few tokens: the scales of a block's columns
+    // few tokens: the scales of a block's columns, by the accumulator they belong to.  Accumulators take
+    // turns across tiles too, so a row is written two barriers after the one behind which it was read
+    float sc[2][32];
 };
 
 template <typename T>
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(Cfg<TOKM, BN>::kThreads, TOKM ? 1 : 2)
                     nw = ld_in(ws + k + 1);
                 }
                 if (!TOKM) {
-                    if ((tid & 127) < BN) sm.sc[k & 3][tid & 127] = s;
+                    if ((tid & 127) < BN) sm.sc[acc.slot][tid & 127] = s;
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
                 if (!mb_wait(&sm.acc_full[acc.slot], acc.phase, abort, &g_err)) ok = false;
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(Cfg<TOKM, BN>::kThreads, TOKM ? 1 : 2)
                         tmem_ld(at + c, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) sum[c + j] = fmaf(__uint_as_float(v[j]), sm.sc[k & 3][c + j], sum[c + j]);
+                        for (int j = 0; j < 16; ++j) sum[c + j] = fmaf(__uint_as_float(v[j]), sm.sc[acc.slot][c + j], sum[c + j]);
                     }
                 }
                 tc_before_sync();

@@ -220,3 +220,17 @@ def test_as_many_blocks_as_find_room(moe):
         x8, xs, w8, ws = operands(n, inner, outer, n + outer)
         check(moe.fp8_linear(x8, xs, w8, ws, dtype=torch.float32), x8, xs, w8, ws)
     assert moe.dense_status() == 0
+
+
+@pytest.mark.parametrize("inner", [128, 640, 1152, 1040, 256])
+@pytest.mark.parametrize("n", [5, 16, 32])
+def test_few_tokens_of_many_tiles(moe, n, inner):
+    """More tiles of 128 rows than blocks run at once, scales of neighbouring blocks of rows 2^20 apart."""
+    outer = 80_000
+    x8, xs, w8, ws = operands(n, inner, outer, n + inner)
+    ws *= torch.where(torch.arange(ws.shape[0], device="cuda") * 7 % 5 < 2, 2.0**-20, 1.0)[:, None]
+    out = moe.fp8_linear(x8, xs, w8, ws, dtype=torch.float32)
+    check(out, x8, xs, w8, ws)
+    for _ in range(50):
+        assert torch.equal(moe.fp8_linear(x8, xs, w8, ws, dtype=torch.float32), out)
+    assert moe.dense_status() == 0
