@@ -58,12 +58,12 @@ cudaError_t launch(const void *x, int64_t x_stride, int n, int dim, uint8_t *x8,
     const T *xp = static_cast<const T *>(x);
     const uint32_t row = (uint32_t)(dim + 127) / 128 * 8;
     // units are counted in 31 bits: a launch takes what fits
-    const int most = (int)((1u << 30) / row);
-    for (int t0 = 0; t0 < n; t0 += most) {
-        const int m = n - t0 < most ? n - t0 : most;
-        const T *xt = xp + (int64_t)t0 * x_stride;
-        uint8_t *ot = x8 + (int64_t)t0 * x8_stride;
-        float *st = scale + (int64_t)t0 * (row / 8);
+    const int64_t most = (1u << 30) / row;
+    for (int64_t t0 = 0; t0 < n; t0 += most) {  // in 64 bits: the last step may pass 2^31
+        const int64_t m = n - t0 < most ? n - t0 : most;
+        const T *xt = xp + t0 * x_stride;
+        uint8_t *ot = x8 + t0 * x8_stride;
+        float *st = scale + t0 * (row / 8);
         FastDiv by_row(row);
         uint32_t units = (uint32_t)m * row;
         void *args[] = {&xt, &x_stride, &dim, &by_row, &units, &ot, &x8_stride, &st};

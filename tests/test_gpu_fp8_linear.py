@@ -234,3 +234,17 @@ def test_few_tokens_of_many_tiles(moe, n, inner):
     for _ in range(50):
         assert torch.equal(moe.fp8_linear(x8, xs, w8, ws, dtype=torch.float32), out)
     assert moe.dense_status() == 0
+
+
+def test_quant_as_many_rows_as_are_counted(moe):
+    """2^31 - 2 rows: the last launch begins where one step more passes 31 bits (codes and scales 43 GB)."""
+    n = 2**31 - 2
+    row = torch.randn((1, 16), device="cuda").half()
+    want, ws = by_formula(row)
+    x8 = torch.full((n, 16), 0x55, dtype=torch.uint8, device="cuda")
+    x8, s = moe.quant_act_fp8(row.expand(n, 16), x8=x8)
+    step = 1 << 27
+    for t in range(0, n, step):
+        assert bool((x8[t:t + step].view(torch.int64) == want.view(torch.int64)).all())
+        assert bool((s[t:t + step] == ws).all())
+    torch.cuda.synchronize()
