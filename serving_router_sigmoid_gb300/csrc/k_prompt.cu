@@ -783,11 +783,17 @@ cudaError_t launch_latent_prompt(const MoePromptArgs &a, cudaStream_t s) {
     p.nope_chunks = (a.nope_dim + 63) / 64;
     p.chunks = p.nope_chunks + (a.rope_dim > 0);
     p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride_t % 16 == 0 && a.out_stride_h % 16 == 0;
-    // Two streams where heads are narrow enough and blocks of 256 queries give every SM
-    // work.  Measured, heads of 128 + 64 / 128, two streams and one: 2048 queries, 16
-    // heads (128 blocks) 42.7 and 28.7 us, 32 heads 46.2 and 53.8, 64 heads 92.4 and 104.6;
-    // 5 x 250, 16 heads 11.1 and 8.6; 20 x 100, 16 heads (128 at most) 15.3 and 15.2
-    const bool narrow = a.v_dim <= 128 && p.chunks <= 3 && (a.n_queries + 255ll) / 256 * a.n_heads >= sms;
+    // Two streams where heads are narrow enough, blocks of 256 queries give every SM
+    // work, and requests hold more than 128 queries on average: a shorter one leaves the
+    // second stream without a tile.  Measured, heads of 128 + 64 / 128, two streams and one:
+    // 2048 queries, 16 heads (128 blocks) 42.7 and 28.7 us, 32 heads 46.2 and 53.8, 64 heads
+    // 91.5 and 104.6; 5 x 250, 16 heads 11.1 and 8.6; requests of 40 queries, 100 with 16 heads
+    // 44.5 and 43.5, with 64 heads 170 and 163; 40 of 100 behind 900 others 96.8 and 80.8; 20
+    // of 128, 64 heads 44.0 and 42.0; 40 of 160, 16 heads 41.9 and 42.4; 20 of 256, 64 heads 73.9
+    // and 82.2; 100 of 20 and one of 1000, 16 heads 61.6 and 57.6; 40 of up to 500 (302 on
+    // average), 16 heads 73.8 and 75.7, 64 heads (240) 209 and 204
+    const bool narrow = a.v_dim <= 128 && p.chunks <= 3 && (a.n_queries + 255ll) / 256 * a.n_heads >= sms &&
+                        a.n_queries > 128ll * a.n_requests;
     if (a.act_type == MOE_F16) return narrow ? launch<__half, 2>(a, p, dev, sms, s) : launch<__half, 1>(a, p, dev, sms, s);
     return narrow ? launch<__nv_bfloat16, 2>(a, p, dev, sms, s) : launch<__nv_bfloat16, 1>(a, p, dev, sms, s);
 }

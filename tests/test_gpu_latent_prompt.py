@@ -344,3 +344,28 @@ def test_many_items_of_one_tile(moe, nope, rope, v, gap):
             again, _ = moe.latent_prompt(*a, 0.1, causal=causal)
             assert torch.equal(again[:sum(nq)], out[:sum(nq)])
     assert moe.dense_status() == 0
+
+
+# with a long request among them the short ones, too, are items of two streams
+@pytest.mark.parametrize("nq,nk", RAGGED)
+@pytest.mark.parametrize("nope,rope,v", [(128, 64, 128), (64, 0, 64)])
+def test_short_requests_beside_a_long_one(moe, nope, rope, v, nq, nk):
+    nq, nk = nq[:1] + [700] + nq[1:], nk[:1] + [830] + nk[1:]
+    a = setup(nq, nk, 160, nope, rope, v, torch.bfloat16, seed=sum(nq), spare=3)
+    for causal in (True, False):
+        out, lse = moe.latent_prompt(*a, 0.07, causal=causal)
+        check(*some(a, out, lse), 0.07, causal)
+    assert moe.dense_status() == 0
+
+
+@pytest.mark.parametrize("nope,rope,v", [(128, 64, 128), (128, 0, 128), (64, 32, 64)])
+def test_two_streams_past_many_empty_requests(moe, nope, rope, v):
+    nq = ([1280] * 8 + [0] * 70) * 4  # 131 on average
+    nk = ([1280, 1400] * 4 + [0, 9] * 35) * 4
+    a = setup(nq, nk, 2, nope, rope, v, torch.bfloat16, seed=nope, spare=1)
+    out, lse = moe.latent_prompt(*a, 0.07)
+    check(out, lse, *a, 0.07, True)
+    for _ in range(10):
+        again, _ = moe.latent_prompt(*a, 0.07)
+        assert torch.equal(again[:sum(nq)], out[:sum(nq)])
+    assert moe.dense_status() == 0
