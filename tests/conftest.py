@@ -13,7 +13,14 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: GLM-sized case (minutes)")
 
 
+# Two of its cases count ids as handed out that no table row can hold; moe_kv_plan keeps those on
+# the free list (test_gpu_kv_plan_pages.py).  It fails there, so it comes last: a run that stops at
+# its first failure has then seen all others.
+LAST = "test_gpu_kv_plan.py::test_shortages_are_flagged_and_leave_no_slot"
+
+
 def pytest_collection_modifyitems(config, items):
+    items.sort(key=lambda item: item.nodeid.endswith(LAST))
     try:
         import torch
         has_gpu = torch.cuda.is_available()
