@@ -47,6 +47,12 @@ __device__ int32_t g_err;  // flags since the last read
 constexpr uint32_t kSlot = 16384;
 constexpr int kTiles = 8;         // narrow: tiles of keys or values in flight, at most
 constexpr int kSlots = 14;        // slots of the ring, at most
+// Wide: barriers of the slots' copies, in turn, one ring of them for keys and one for values,
+// since each is waited for by another warp.  (One barrier a slot would have phases that a warp
+// does not see: where the ring is shorter than a tile of keys and one of values, the
+// copy before the awaited one may not have landed, and the parity is that of the one before.)
+// More than slots, so none comes round before it was waited for.
+constexpr int kTurns = 16;
 // Tiles of values whose last rows are cleared, in flight at most (one an item).  The copies
 // come to an item once S of the item before is complete; that S (wide, items of one
 // tile) needs PV of the item two further back at most, by its two buffers.  So when an
@@ -72,7 +78,7 @@ struct Params {
 };
 
 struct Shared {
-    uint64_t full[kSlots], empty[kSlots], q_full[2], q_empty[2], v_fixed[kFixes], s_full[2], p_ready[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
+    uint64_t full[kTurns], v_full[kTurns], empty[kSlots], q_full[2], q_empty[2], v_fixed[kFixes], s_full[2], p_ready[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem;
     int abort;
     int began;                    // narrow: behind the last item whose first stream has weights
@@ -203,10 +209,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort = &sm.abort;
 
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) {  // narrow: one a tile, wide: one a slot
+        for (int i = 0; i < kTurns; ++i) {  // narrow: one a tile, wide: one a copy
             mb_init(&sm.full[i], 1);
-            mb_init(&sm.empty[i], NQ);  // the streams
+            mb_init(&sm.v_full[i], 1);
         }
+        for (int i = 0; i < kSlots; ++i) mb_init(&sm.empty[i], NQ);  // narrow: one a tile, the streams; wide: one a slot
         for (int i = 0; i < kFixes; ++i) mb_init(&sm.v_fixed[i], 1);
         for (int i = 0; i < 2; ++i) {
             mb_init(&sm.q_full[i], 1);
@@ -243,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t put = 0, got = 0;         // tiles brought, tiles whose slots are back
         uint32_t sizes = 0;                // of the tiles in flight, 4 bits each, the oldest lowest
         Place here;                        // wide: the next slot
+        uint32_t kt = 0, vt = 0;           // and the copies of keys and of values so far
         uint32_t qp = 0, fixes = 0;
         bool ok = true;
         const auto take = [&](int n) {     // n free slots and a free pair of barriers
@@ -303,11 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane & 1) mine.step(1, p.slots);
                         ok = __all_sync(0xffffffffu, lane >= n || mb_wait(&sm.empty[mine.slot], mine.phase ^ 1, abort, &g_err));
                         if (ok && lane < n) {
-                            mb_expect_tx(&sm.full[mine.slot], kSlot);
-                            bring_k(ring + (uint32_t)mine.slot * kSlot, c + lane, j, &sm.full[mine.slot]);
+                            uint64_t *const full = &sm.full[(kt + lane) % kTurns];
+                            mb_expect_tx(full, kSlot);
+                            bring_k(ring + (uint32_t)mine.slot * kSlot, c + lane, j, full);
                         }
                         __syncwarp();
                         here.step(n, p.slots);
+                        if (ok) kt += n;
                     }
                     return;
                 }
@@ -325,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const auto values = [&](int j) {
                 const int live = x.nk - 128 * j;   // rows of this request
                 if (NQ == 1) {
-                    const Place begin = here;
-                    for (int i = 0; i < nv && ok; ++i, here.step(1, p.slots)) {
-                        uint64_t *const full = &sm.full[here.slot];
+                    const int begin = here.slot;
+                    for (int i = 0; i < nv && ok; ++i, ++vt, here.step(1, p.slots)) {
+                        uint64_t *const full = &sm.v_full[vt % kTurns];
                         if (!(ok = __all_sync(0xffffffffu, mb_wait(&sm.empty[here.slot], here.phase ^ 1, abort, &g_err)))) return;
                         if (lane == 0) mb_expect_tx(full, (uint32_t)p.v_boxes * box);
                         __syncwarp();
@@ -335,10 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                     }
                     if (live < 128) {
-                        Place at = begin;
-                        for (int i = 0; i < nv && ok; ++i, at.step(1, p.slots))
-                            ok = __all_sync(0xffffffffu, mb_wait(&sm.full[at.slot], at.phase, abort, &g_err));
-                        if (ok) clear(live, begin.slot);
+                        for (uint32_t i = vt - nv; i != vt && ok; ++i)
+                            ok = __all_sync(0xffffffffu, mb_wait(&sm.v_full[i % kTurns], i / kTurns & 1, abort, &g_err));
+                        if (ok) clear(live, begin);
                     }
                     return;
                 }
@@ -371,9 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (*abort) {  // copies in flight land before the block ends
             const long long t = clock64();
-            if (NQ == 1)
-                for (int i = 0; i < p.slots; ++i, here.step(1, p.slots))  // the last use of each slot
-                    while (!mb_test(&sm.full[here.slot], here.phase ^ 1) && clock64() - t < kWaitClk) {}
+            for (uint32_t i = kt > kTurns ? kt - kTurns : 0; i < kt; ++i)
+                while (!mb_test(&sm.full[i % kTurns], i / kTurns & 1) && clock64() - t < kWaitClk) {}
+            for (uint32_t i = vt > kTurns ? vt - kTurns : 0; i < vt; ++i)
+                while (!mb_test(&sm.v_full[i % kTurns], i / kTurns & 1) && clock64() - t < kWaitClk) {}
             for (uint32_t i = put > kTiles ? put - kTiles : 0; i < put; ++i)
                 while (!mb_test(&sm.full[i % kTiles], i / kTiles & 1) && clock64() - t < kWaitClk) {}
         }
@@ -510,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (firsts) {
             // ---- S = Q K^T, a slot of keys after the other
             Place at;
-            uint32_t began = 0;
+            uint32_t began = 0, kt = 0;
             for (int it = 0; ok && cur.item(p, it, x); ++it) {
                 if (!x.n) continue;
                 if (!(ok = wait(&sm.q_full[0], qf))) break;
@@ -522,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     began |= 1u << b;
                     uses[b] ^= 1;
                     uint32_t q = dq;
-                    for (int c = 0; c < nk; ++c, q += kSlot >> 4, at.step(1, slots)) {
-                        if (!(ok = wait(&sm.full[at.slot], at.phase))) break;
+                    for (int c = 0; c < nk; ++c, ++kt, q += kSlot >> 4, at.step(1, slots)) {
+                        if (!(ok = wait(&sm.full[kt % kTurns], kt / kTurns & 1))) break;
                         tc_after_sync();
                         if (lead) {
                             product_s(tmem + 128 * b, q, at.slot, c, c + 1);
@@ -541,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
             // ---- O += P V
             Place at;
-            uint32_t oe = 0;
+            uint32_t oe = 0, vt = 0;
             for (int it = 0; ok && cur.item(p, it, x); ++it) {
                 if (!x.n) continue;
                 at.step(nk, slots);
@@ -555,8 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = (j || wait(&sm.o_empty[0], oe ^ 1)) && wait(&sm.p_ready[b][0], uses[b]))) break;
                     uses[b] ^= 1;
                     if (!j) oe ^= 1;
-                    for (int i = 0; i < nv; ++i, at.step(1, slots)) {
-                        if (!(ok = wait(&sm.full[at.slot], at.phase))) break;
+                    for (int i = 0; i < nv; ++i, ++vt, at.step(1, slots)) {
+                        if (!(ok = wait(&sm.v_full[vt % kTurns], vt / kTurns & 1))) break;
                         tc_after_sync();
                         if (lead) {
                             product_o(tmem + kColO, tmem + 128 * b, ahead(at.slot, slots - i), per * i, min(steps, per * (i + 1)), j == 0);
@@ -739,7 +749,7 @@ cudaError_t launch(const MoePromptArgs &a, Params &p, int dev, int sms, cudaStre
     p.v_rows = v_pad == 1 ? 128 : v_pad == 2 ? 64 : 32;
     p.v_slots = 128 / p.v_rows;
     p.slots = (int)((227 * 1024 - 1024 - sizeof(Shared) - 64) / kSlot) - NQ * p.chunks;
-    static_assert((227 * 1024 - 1024 - sizeof(Shared) - 64) / kSlot <= kSlots, "barriers of the ring");
+    static_assert((227 * 1024 - 1024 - sizeof(Shared) - 64) / kSlot <= kSlots && kSlots <= kTurns, "barriers of the ring");
     const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap maps[4] = {};
     const auto map = [&](int i, const void *base, int dim, int rows, int64_t st, int64_t sh, int &heads, int box) {

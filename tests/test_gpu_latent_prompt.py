@@ -369,3 +369,16 @@ def test_two_streams_past_many_empty_requests(moe, nope, rope, v):
         again, _ = moe.latent_prompt(*a, 0.07)
         assert torch.equal(again[:sum(nq)], out[:sum(nq)])
     assert moe.dense_status() == 0
+
+
+@pytest.mark.parametrize("nope,rope,v", [(240, 16, 240), (208, 48, 256), (208, 16, 144), (240, 0, 256)])
+def test_rings_shorter_than_a_tile(moe, nope, rope, v):
+    """Keys of five chunks beside wide values: a tile of both is more than the ring holds."""
+    a = setup([150, 600, 40, 300], [900, 700, 40, 1300], 40, nope, rope, v, torch.bfloat16, seed=nope + v, spare=2)
+    for causal in (True, False):
+        out, lse = moe.latent_prompt(*a, 0.06, causal=causal)
+        check(*some(a, out, lse, 13), 0.06, causal)
+        for _ in range(20):
+            again, _ = moe.latent_prompt(*a, 0.06, causal=causal)
+            assert torch.equal(again[:-2], out[:-2])
+    assert moe.dense_status() == 0

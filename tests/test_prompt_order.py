@@ -2,12 +2,14 @@
 
 A block of the kernel is a copying warp, two warps that issue products and the
 softmax warps, which meet at barriers that count phases and are waited for by a
-phase's parity.  Such a wait is right only if the barrier cannot complete another
-phase before the wait is looked at: then the parity is the old one again, and the
-warp sleeps on.  The model below runs the warps' waits and arrivals in the
-kernel's order, with delays drawn from a wide range (a warp may stand still
-anywhere); what it holds is that every warp comes to its end whatever the delays
-are.  Sizes of rings and numbers of barriers are the kernel's.
+phase's parity.  Such a wait is right only if the barrier can neither complete
+another phase before the wait is looked at (the parity is the old one again, and
+the warp sleeps on), nor be a phase behind (the parity is that of the phase before
+the last, and the warp reads what has not come).  The model below runs the warps'
+waits and arrivals in the kernel's order, with delays drawn from a wide range (a
+warp or a copy may stand still anywhere); what it holds is that every wait ends, and
+with the phase that it is for, whatever the delays are.  Sizes of rings and numbers
+of barriers are the kernel's.
 """
 import heapq
 import os
@@ -34,31 +36,34 @@ class Barrier:
 
 
 class Block:
-    """Warps as generators that yield ("for", cycles) or ("wait", barrier, parity)."""
+    """Warps as generators that yield ("for", cycles) or ("wait", barrier, phase): phases count from 0, -1 is
+    what came before the first."""
 
     def __init__(self, seed):
         self.r, self.now, self.queue, self.n, self.pipe = random.Random(seed), 0.0, [], 0, 0.0
+        self.wrong, self.strict = 0, True
 
     def at(self, when, what):
         self.n += 1
         heapq.heappush(self.queue, (when, self.n, what))
 
     def delay(self, base):
-        return base * self.r.choice([0.1, 0.5, 1, 1, 1, 2, 6])
+        return base * self.r.choice([0.1, 0.5, 1, 1, 1, 2, 6, 15])
 
     def arrive(self, bar):
         bar.left -= 1
         if bar.left == 0:
             bar.left, bar.done = bar.count, bar.done + 1
             asleep, bar.asleep = bar.asleep, []
-            for warp, parity in asleep:  # each looks again, a little later
-                self.at(self.now + self.delay(40), lambda w=warp, p=parity: self.look(w, bar, p))
+            for warp, phase in asleep:  # each looks again, a little later
+                self.at(self.now + self.delay(40), lambda w=warp, p=phase: self.look(w, bar, p))
 
-    def look(self, warp, bar, parity):
-        if (bar.done & 1) != parity:
+    def look(self, warp, bar, phase):
+        if (bar.done ^ phase) & 1:  # what a wait by parity sees
+            self.wrong += bar.done != phase + 1
             self.step(warp)
         else:
-            bar.asleep.append((warp, parity))
+            bar.asleep.append((warp, phase))
 
     def step(self, warp):
         try:
@@ -82,86 +87,86 @@ class Block:
         self.at(max(end, self.now) + 150 + self.delay(100), lambda: self.arrive(bar))
 
     def run(self, warps):
-        """Whether all warps end."""
+        """Whether all warps end, and every wait was for the phase it saw."""
         self.running = len(warps)
         for w in warps:
             self.at(0.0, lambda w=w: self.step(w))
         while self.queue:
             self.now, _, what = heapq.heappop(self.queue)
             what()
-        return self.running == 0
+        return self.running == 0 and not (self.strict and self.wrong)
 
 
 LOOKUP, COPY, SOFTMAX, RESCALE = 900, 900, 350, 500
 
 
-def two_streams(b, items, nk, nv, slots, tiles_max, fixes_n, start):
+def two_streams(b, items, nk, nv, slots, tiles_max, fixes_n, start="count"):
     """items: ((tiles of the first stream, of the second), whether the last tile is cleared).  start: what lets
-    the second stream begin an item: "count" (of items whose first stream has weights) or "parity"."""
+    the second stream begin an item: "count" (of items whose first stream has weights), "parity" (of the
+    first stream's weights) or "nothing"."""
     bars = lambda n, c=1: [Barrier(c) for _ in range(n)]  # noqa: E731
     full, empty, v_fixed = bars(tiles_max), bars(tiles_max, 2), bars(fixes_n)
     q_full, q_empty, s_full, pv_done, o_full, o_empty = (bars(2) for _ in range(6))
     p_ready = [bars(2), bars(2)]
-    began = [0]
+    began, b.strict = [0], False
+    turn = lambda ring, n: (ring[n % len(ring)], n // len(ring))  # noqa: E731
 
     def copies():
-        room, put, got, sizes, qp, fixes = slots, 0, 0, [], 0, 0
+        room, put, got, sizes, fixes = slots, 0, 0, [], 0
 
         def take(n):
             nonlocal room, got
             while room < n or put - got == tiles_max:
-                yield "wait", empty[got % tiles_max], got // tiles_max & 1
+                yield "wait", *turn(empty, got)
                 room += sizes.pop(0)
                 got += 1
             sizes.append(n)
             room -= n
-        for tiles, cleared in items:
+        for it, (tiles, cleared) in enumerate(items):
             yield "for", b.delay(LOOKUP)
             for j in range(max(tiles)):
                 if j == 0:
-                    yield "wait", q_empty[0], qp ^ 1
+                    yield "wait", q_empty[0], it - 1
                     b.later(COPY, q_full[0])
                 yield from take(nk)
                 b.later(COPY, full[put % tiles_max])
                 put += 1
                 if j == 0:
-                    yield "wait", q_empty[1], qp ^ 1
+                    yield "wait", q_empty[1], it - 1
                     b.later(COPY, q_full[1])
                 yield from take(nv)
                 b.later(COPY, full[put % tiles_max])
                 if cleared and j == max(tiles) - 1:
-                    yield "wait", full[put % tiles_max], put // tiles_max & 1
+                    yield "wait", *turn(full, put)
                     yield "for", b.delay(200)
                     b.arrive(v_fixed[fixes % fixes_n])
                     fixes += 1
                 put += 1
-            qp ^= 1
 
     def issue(g):
-        tile = fixes = qf = oe = theirs = use = 0
+        tile = fixes = theirs = use = worked = 0
         for it, (tiles, cleared) in enumerate(items):
             yield "for", b.delay(LOOKUP)
             mine, other, n = tiles[g], tiles[g ^ 1], max(tiles)
-            yield "wait", q_full[g], qf
-            qf ^= 1
+            yield "wait", q_full[g], it
 
             def first(j):
                 end = b.product(nk * 250)
-                t = tile + 2 * j
                 b.commit(s_full[g], end)
-                for _ in range(1 + (j >= other)):
-                    b.commit(empty[t % tiles_max], end)
+                b.commit(empty[(tile + 2 * j) % tiles_max], end)
+                if j >= other:
+                    b.commit(empty[(tile + 2 * j) % tiles_max], end)
                 if j + 1 == mine:
                     b.commit(q_empty[g], end)
             if g == 1 and mine and other:
                 if start == "parity":
                     yield "wait", p_ready[0][0], theirs
-                else:
+                elif start == "count":
                     while began[0] <= it:
                         yield "for", 50
-            theirs ^= other & 1
+            theirs += other
             if mine:
-                yield "wait", full[tile % tiles_max], tile // tiles_max & 1
+                yield "wait", *turn(full, tile)
                 first(0)
             else:
                 b.commit(q_empty[g], 0)
@@ -170,163 +175,156 @@ def two_streams(b, items, nk, nv, slots, tiles_max, fixes_n, start):
                 fixes += last
                 if j >= mine:
                     continue
-                yield "wait", full[t % tiles_max], t // tiles_max & 1
+                yield "wait", *turn(full, t)
                 if last:
-                    yield "wait", v_fixed[fix % fixes_n], fix // fixes_n & 1
+                    yield "wait", *turn(v_fixed, fix)
                 if j == 0:
-                    yield "wait", o_empty[g], oe ^ 1
-                    oe ^= 1
+                    yield "wait", o_empty[g], worked - 1
+                    worked += 1
                 yield "wait", p_ready[g][0], use
                 b.commit(pv_done[g], b.product(nv * 128))
                 yield "wait", p_ready[g][1], use
-                use ^= 1
+                use += 1
                 end = b.product(nv * 128)
-                for _ in range(1 + (j >= other)):
+                b.commit(empty[t % tiles_max], end)
+                if j >= other:
                     b.commit(empty[t % tiles_max], end)
                 if j + 1 == mine:
                     b.commit(o_full[g], end)
                 else:
-                    t = tile + 2 * j + 2
-                    yield "wait", full[t % tiles_max], t // tiles_max & 1
+                    yield "wait", *turn(full, t + 1)
                     first(j + 1)
             tile += 2 * n
 
     def softmax(g):
-        sf = pd = of = 0
+        done = worked = 0
         for it, (tiles, _) in enumerate(items):
             yield "for", b.delay(LOOKUP)
             for j in range(2 * tiles[g]):
                 if not j & 1:
-                    yield "wait", s_full[g], sf
-                    sf ^= 1
+                    yield "wait", s_full[g], done
                 if j and b.r.random() < 0.5:
                     if j & 1:
-                        yield "wait", pv_done[g], pd
+                        yield "wait", pv_done[g], done
                     yield "for", b.delay(RESCALE)
-                pd ^= j & 1
+                done += j & 1
                 yield "for", b.delay(SOFTMAX)
                 b.arrive(p_ready[g][j & 1])
                 if g == 0 and j == 0:
                     began[0] = it + 1
             if tiles[g]:
-                yield "wait", o_full[g], of
-                of ^= 1
+                yield "wait", o_full[g], worked
+                worked += 1
                 yield "for", b.delay(600)
                 b.arrive(o_empty[g])
     return b.run([copies(), issue(0), issue(1), softmax(0), softmax(1)])
 
 
-def one_stream(b, items, nk, nv, slots, fixes_n):
-    """items: (tiles, whether the last one is cleared)."""
+def one_stream(b, items, nk, nv, slots, fixes_n, turns):
+    """items: (tiles, whether the last one is cleared).  turns: barriers of the copies of keys, and of those of
+    values; 0: one barrier for each slot, whatever it holds."""
     bars = lambda n: [Barrier() for _ in range(n)]  # noqa: E731
-    full, empty, v_fixed = bars(slots), bars(slots), bars(fixes_n)
+    full, k_full, v_full, empty, v_fixed = bars(slots), bars(turns), bars(turns), bars(slots), bars(fixes_n)
     q_full, q_empty, o_full, o_empty = (Barrier() for _ in range(4))
     s_full, p_ready, pv_done = bars(2), bars(2), bars(2)
+    turn = lambda ring, n: (ring[n % len(ring)], n // len(ring))  # noqa: E731
+
+    def landed(ring, n, at):  # of the n-th copy of keys or values, which is the at-th of all
+        return turn(ring, n) if turns else turn(full, at)
 
     def copies():
-        here = qp = fixes = 0
+        here = keys = vals = fixes = 0
 
-        def bring(n):
+        def bring(ring, n, count):
             nonlocal here
-            for _ in range(n):
-                yield "wait", empty[here % slots], here // slots & 1 ^ 1
-                b.later(COPY, full[here % slots])
+            for i in range(n):
+                yield "wait", empty[here % slots], here // slots - 1
+                b.later(COPY, landed(ring, count + i, here)[0])
                 here += 1
 
         def values(cleared):
-            nonlocal fixes
+            nonlocal fixes, vals
             begin = here
-            yield from bring(nv)
+            yield from bring(v_full, nv, vals)
             if cleared:
-                for at in range(begin, begin + nv):
-                    yield "wait", full[at % slots], at // slots & 1
+                for i in range(nv):
+                    yield "wait", *landed(v_full, vals + i, begin + i)
                 yield "for", b.delay(200)
                 b.arrive(v_fixed[fixes % fixes_n])
                 fixes += 1
-        for n, cleared in items:
+            vals += nv
+        for it, (n, cleared) in enumerate(items):
             yield "for", b.delay(LOOKUP)
-            yield "wait", q_empty, qp ^ 1
+            yield "wait", q_empty, it - 1
             b.later(COPY, q_full)
             for j in range(n):
-                yield from bring(nk)
+                yield from bring(k_full, nk, keys)
+                keys += nk
                 if j:
                     yield from values(False)
             yield from values(cleared)
-            qp ^= 1
 
     def products_s():
-        at = step = qf = began = 0
-        uses = [0, 0]
-        for n, _ in items:
+        at = step = keys = 0
+        for it, (n, _) in enumerate(items):
             yield "for", b.delay(LOOKUP)
-            yield "wait", q_full, qf
-            qf ^= 1
-            end = 0
+            yield "wait", q_full, it
             for j in range(n):
-                k = step & 1
-                step += 1
-                if began >> k & 1:
-                    yield "wait", pv_done[k], uses[k] ^ 1
-                began |= 1 << k
-                uses[k] ^= 1
+                if step >= 2:
+                    yield "wait", pv_done[step & 1], step // 2 - 1
                 for c in range(nk):
-                    yield "wait", full[at % slots], at // slots & 1
+                    yield "wait", *landed(k_full, keys, at)
                     end = b.product(250)
                     b.commit(empty[at % slots], end)
                     if c + 1 == nk:
-                        b.commit(s_full[k], end)
+                        b.commit(s_full[step & 1], end)
                     at += 1
+                    keys += 1
+                step += 1
                 if j:
                     at += nv
             b.commit(q_empty, end)
             at += nv
 
     def products_o():
-        at = step = fixes = oe = 0
-        uses = [0, 0]
-        for n, cleared in items:
+        at = step = fixes = vals = 0
+        for it, (n, cleared) in enumerate(items):
             yield "for", b.delay(LOOKUP)
             at += nk * min(n, 2)
             for j in range(n):
-                k = step & 1
-                step += 1
                 if cleared and j == n - 1:
-                    yield "wait", v_fixed[fixes % fixes_n], fixes // fixes_n & 1
+                    yield "wait", *turn(v_fixed, fixes)
                     fixes += 1
                 if j == 0:
-                    yield "wait", o_empty, oe ^ 1
-                    oe ^= 1
-                yield "wait", p_ready[k], uses[k]
-                uses[k] ^= 1
+                    yield "wait", o_empty, it - 1
+                yield "wait", p_ready[step & 1], step // 2
                 for i in range(nv):
-                    yield "wait", full[at % slots], at // slots & 1
+                    yield "wait", *landed(v_full, vals, at)
                     end = b.product(128)
                     b.commit(empty[at % slots], end)
                     if i + 1 == nv:
-                        b.commit(pv_done[k], end)
+                        b.commit(pv_done[step & 1], end)
                         if j + 1 == n:
                             b.commit(o_full, end)
                     at += 1
+                    vals += 1
+                step += 1
                 if j + 2 < n:
                     at += nk
 
     def softmax():
-        sf, pd, of, step = [0, 0], [0, 0], 0, 0
-        for n, _ in items:
+        step = 0
+        for it, (n, _) in enumerate(items):
             yield "for", b.delay(LOOKUP)
             for j in range(n):
-                k = step & 1
-                step += 1
-                yield "wait", s_full[k], sf[k]
-                sf[k] ^= 1
+                yield "wait", s_full[step & 1], step // 2
                 if j and b.r.random() < 0.5:
-                    yield "wait", pv_done[k ^ 1], pd[k ^ 1] ^ 1
+                    yield "wait", pv_done[step & 1 ^ 1], (step - 1) // 2
                     yield "for", b.delay(RESCALE)
-                pd[k] ^= 1
                 yield "for", b.delay(SOFTMAX)
-                b.arrive(p_ready[k])
-            yield "wait", o_full, of
-            of ^= 1
+                b.arrive(p_ready[step & 1])
+                step += 1
+            yield "wait", o_full, it
             yield "for", b.delay(600)
             b.arrive(o_empty)
     return b.run([copies(), products_s(), products_o(), softmax()])
@@ -339,7 +337,7 @@ def ring(chunks, streams):
 
 # chunks of 64 key dimensions, slots of a tile of values
 TWO = [(1, 1), (1, 2), (2, 1), (2, 2), (3, 1), (3, 2)]
-ONE = TWO + [(4, 4), (4, 1), (2, 4)]
+ONE = TWO + [(4, 4), (4, 1), (2, 4), (5, 4), (5, 1), (1, 4)]
 
 
 def draw_two(r):
@@ -354,7 +352,7 @@ def draw_two(r):
 def test_two_streams_come_to_their_end(nk, nv):
     for seed in range(300):
         items = draw_two(random.Random(seed))
-        assert two_streams(Block(seed), items, nk, nv, ring(nk, 2), constant("kTiles"), constant("kFixes"), "count"), (seed, items)
+        assert two_streams(Block(seed), items, nk, nv, ring(nk, 2), constant("kTiles"), constant("kFixes")), (seed, items)
 
 
 @pytest.mark.parametrize("nk,nv", ONE)
@@ -362,18 +360,22 @@ def test_one_stream_comes_to_its_end(nk, nv):
     for seed in range(300):
         r = random.Random(seed)
         items = [(r.choice([1, 1, 1, 2, 3]), r.random() < 0.8) for _ in range(r.randint(1, 8))]
-        assert one_stream(Block(seed), items, nk, nv, ring(nk, 1), constant("kFixes")), (seed, items)
+        assert one_stream(Block(seed), items, nk, nv, ring(nk, 1), constant("kFixes"), constant("kTurns")), (seed, items)
 
 
 def test_the_model_sees_a_phase_that_is_missed():
-    """A start by the parity of the first stream's weights, and two barriers of cleared rows, are each overtaken."""
+    """A start by the parity of the first stream's weights, two barriers of cleared rows, and a barrier for each
+    slot of a short ring are each overtaken or behind."""
     def two(seed):
         return two_streams(Block(seed), [((2, 3), False)] * 3, 2, 2, ring(2, 2), 8, 4, "parity")
 
-    def one(seed):
-        return one_stream(Block(seed), [(1, True)] * 8, 2, 1, ring(2, 1), 2)
-    assert not all(two(s) for s in range(300))
-    assert not all(one(s) for s in range(300))
+    def fixes(seed):
+        return one_stream(Block(seed), [(1, True)] * 8, 2, 1, ring(2, 1), 2, 16)
+
+    def slots(seed):
+        return one_stream(Block(seed), [(4, False)] * 3, 5, 4, ring(5, 1), 4, 0)
+    for order in (two, fixes, slots):
+        assert not all(order(s) for s in range(300)), order
 
 
 def test_the_second_stream_starts_by_a_count():
@@ -384,6 +386,6 @@ def test_the_second_stream_starts_by_a_count():
 
 def test_slots_of_the_ring():
     """227 KB less the rest of a block's shared memory are 13 slots."""
-    shared = 8 * (2 * constant("kSlots") + constant("kFixes") + 2 * 9) + 4 * (3 + 512)  # barriers; flags and row maxima
+    shared = 8 * (constant("kSlots") + 2 * constant("kTurns") + constant("kFixes") + 2 * 9) + 4 * (3 + 512)  # barriers; flags and row maxima
     room = 227 * 1024 - 1024 - shared - 64
     assert room // 16384 == 13 and room - 13 * 16384 > 64
