@@ -457,13 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     product_s(sd, q, slot, 0, nk);
                     mma_commit(&sm.s_full[g]);
                     mma_commit(&sm.empty[t % kTiles]);
-                    if (j >= other) mma_commit(&sm.empty[t % kTiles]);
                     if (j + 1 == mine) mma_commit(&sm.q_empty[g]);
                 };
                 const auto keys = [&](int j) { return wait(&sm.full[(tile + 2 * j) % kTiles], (tile + 2 * j) / kTiles & 1); };
                 // The second stream starts when the first has weights: the products of one then
-                // run under the softmax of the other (8 heads of 8192 tokens 159 us, without it 172;
-                // 20 x 300, 16 heads 41.0 and 39.8; 64 heads of 2048 92 either way).  This is for
+                // run under the softmax of the other (8 heads of 8192 tokens 157 us, without it 172;
+                // 20 x 300, 16 heads 41.9 and 39.8; 64 heads of 2048 91 either way).  This is for
                 // speed alone, and the first stream may be tiles or an item further by now: so it is a
                 // count, compared, and given up after a while (a barrier's parity would come round).
                 if (g == 1 && mine && other) {
@@ -481,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int live = x.nk - 128 * j, vs = ahead(slot, nk);
                     const uint32_t fix = fixes, t = tile + 2 * j + 1;
                     if (live < 128) ++fixes;
-                    if (ok && j < mine) {
+                    if (j < mine) {
                         const int steps = (min(live, 128) + 15) / 16;
                         ok = wait(&sm.full[t % kTiles], t / kTiles & 1) && (live >= 128 || wait(&sm.v_fixed[fix % kFixes], fix / kFixes & 1)) &&
                              (j || wait(&sm.o_empty[g], oe ^ 1)) && wait(&sm.p_ready[g][0], uses[0]);
@@ -501,7 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lead) {
                             product_o(od, sd, vs, 4, steps, false);
                             mma_commit(&sm.empty[t % kTiles]);
-                            if (j >= other) mma_commit(&sm.empty[t % kTiles]);
                             if (!more) mma_commit(&sm.o_full[g]);
                         }
                         __syncwarp();
@@ -512,6 +510,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                         }
                     } else {
+                        // A tile for the other stream alone is waited for and given back all the same: a
+                        // phase of its barrier that goes by unseen could be taken for a later one
+                        if (!(ok = wait(&sm.full[(t - 1) % kTiles], (t - 1) / kTiles & 1) &&
+                                   wait(&sm.full[t % kTiles], t / kTiles & 1)))
+                            break;
+                        if (lead) {
+                            mb_arrive(&sm.empty[(t - 1) % kTiles]);
+                            mb_arrive(&sm.empty[t % kTiles]);
+                        }
+                        __syncwarp();
                         slot = ahead(slot, nk + nv);
                     }
                 }

@@ -382,3 +382,19 @@ def test_rings_shorter_than_a_tile(moe, nope, rope, v):
             again, _ = moe.latent_prompt(*a, 0.06, causal=causal)
             assert torch.equal(again[:-2], out[:-2])
     assert moe.dense_status() == 0
+
+
+@pytest.mark.parametrize("nope,rope,v", [(64, 0, 64), (128, 64, 128), (48, 16, 80)])
+def test_items_of_one_stream_between_those_of_two(moe, nope, rope, v):
+    """Requests of up to 128 queries, whose second stream has no tile, behind long keys; and requests whose first
+    128 queries see none."""
+    nq = [100, 512, 128, 256, 400, 1, 600, 128, 300, 256] * 3
+    nk = [900, 512, 700, 128, 272, 1500, 600, 128, 172, 130] * 3
+    a = setup(nq, nk, 48, nope, rope, v, torch.bfloat16, seed=nope, spare=2)
+    for causal in (True, False):
+        out, lse = moe.latent_prompt(*a, 0.08, causal=causal)
+        check(*some(a, out, lse, 17), 0.08, causal)
+        for _ in range(20):
+            again, _ = moe.latent_prompt(*a, 0.08, causal=causal)
+            assert torch.equal(again[:-2], out[:-2])
+    assert moe.dense_status() == 0

@@ -41,7 +41,7 @@ class Block:
 
     def __init__(self, seed):
         self.r, self.now, self.queue, self.n, self.pipe = random.Random(seed), 0.0, [], 0, 0.0
-        self.wrong, self.strict = 0, True
+        self.wrong, self.last = 0, {}
 
     def at(self, when, what):
         self.n += 1
@@ -83,8 +83,10 @@ class Block:
         self.pipe = max(self.pipe, self.now) + cycles
         return self.pipe
 
-    def commit(self, bar, end):  # once what was issued is done
-        self.at(max(end, self.now) + 150 + self.delay(100), lambda: self.arrive(bar))
+    def commit(self, warp, bar, end):  # once what the warp issued is done; in the order of its commits
+        when = max(max(end, self.now) + 150 + self.delay(100), self.last.get(warp, 0.0))
+        self.last[warp] = when
+        self.at(when, lambda: self.arrive(bar))
 
     def run(self, warps):
         """Whether all warps end, and every wait was for the phase it saw."""
@@ -94,21 +96,22 @@ class Block:
         while self.queue:
             self.now, _, what = heapq.heappop(self.queue)
             what()
-        return self.running == 0 and not (self.strict and self.wrong)
+        return self.running == 0 and not self.wrong
 
 
 LOOKUP, COPY, SOFTMAX, RESCALE = 900, 900, 350, 500
 
 
-def two_streams(b, items, nk, nv, slots, tiles_max, fixes_n, start="count"):
+def two_streams(b, items, nk, nv, slots, tiles_max, fixes_n, start="count", skips=False):
     """items: ((tiles of the first stream, of the second), whether the last tile is cleared).  start: what lets
     the second stream begin an item: "count" (of items whose first stream has weights), "parity" (of the
-    first stream's weights) or "nothing"."""
+    first stream's weights) or "nothing".  skips: a stream passes by the tiles that only the other one needs,
+    which gives them back for both."""
     bars = lambda n, c=1: [Barrier(c) for _ in range(n)]  # noqa: E731
     full, empty, v_fixed = bars(tiles_max), bars(tiles_max, 2), bars(fixes_n)
     q_full, q_empty, s_full, pv_done, o_full, o_empty = (bars(2) for _ in range(6))
     p_ready = [bars(2), bars(2)]
-    began, b.strict = [0], False
+    began = [0]
     turn = lambda ring, n: (ring[n % len(ring)], n // len(ring))  # noqa: E731
 
     def copies():
@@ -152,12 +155,12 @@ def two_streams(b, items, nk, nv, slots, tiles_max, fixes_n, start="count"):
 
             def first(j):
                 end = b.product(nk * 250)
-                b.commit(s_full[g], end)
-                b.commit(empty[(tile + 2 * j) % tiles_max], end)
-                if j >= other:
-                    b.commit(empty[(tile + 2 * j) % tiles_max], end)
+                b.commit(g, s_full[g], end)
+                b.commit(g, empty[(tile + 2 * j) % tiles_max], end)
+                if skips and j >= other:
+                    b.commit(g, empty[(tile + 2 * j) % tiles_max], end)
                 if j + 1 == mine:
-                    b.commit(q_empty[g], end)
+                    b.commit(g, q_empty[g], end)
             if g == 1 and mine and other:
                 if start == "parity":
                     yield "wait", p_ready[0][0], theirs
@@ -169,11 +172,15 @@ def two_streams(b, items, nk, nv, slots, tiles_max, fixes_n, start="count"):
                 yield "wait", *turn(full, tile)
                 first(0)
             else:
-                b.commit(q_empty[g], 0)
+                b.commit(g, q_empty[g], 0)
             for j in range(n):
                 fix, t, last = fixes, tile + 2 * j + 1, cleared and j == n - 1
                 fixes += last
                 if j >= mine:
+                    if not skips:
+                        for i in (t - 1, t):
+                            yield "wait", *turn(full, i)
+                            b.arrive(empty[i % tiles_max])
                     continue
                 yield "wait", *turn(full, t)
                 if last:
@@ -182,15 +189,15 @@ def two_streams(b, items, nk, nv, slots, tiles_max, fixes_n, start="count"):
                     yield "wait", o_empty[g], worked - 1
                     worked += 1
                 yield "wait", p_ready[g][0], use
-                b.commit(pv_done[g], b.product(nv * 128))
+                b.commit(g, pv_done[g], b.product(nv * 128))
                 yield "wait", p_ready[g][1], use
                 use += 1
                 end = b.product(nv * 128)
-                b.commit(empty[t % tiles_max], end)
-                if j >= other:
-                    b.commit(empty[t % tiles_max], end)
+                b.commit(g, empty[t % tiles_max], end)
+                if skips and j >= other:
+                    b.commit(g, empty[t % tiles_max], end)
                 if j + 1 == mine:
-                    b.commit(o_full[g], end)
+                    b.commit(g, o_full[g], end)
                 else:
                     yield "wait", *turn(full, t + 1)
                     first(j + 1)
@@ -275,15 +282,15 @@ def one_stream(b, items, nk, nv, slots, fixes_n, turns):
                 for c in range(nk):
                     yield "wait", *landed(k_full, keys, at)
                     end = b.product(250)
-                    b.commit(empty[at % slots], end)
+                    b.commit("s", empty[at % slots], end)
                     if c + 1 == nk:
-                        b.commit(s_full[step & 1], end)
+                        b.commit("s", s_full[step & 1], end)
                     at += 1
                     keys += 1
                 step += 1
                 if j:
                     at += nv
-            b.commit(q_empty, end)
+            b.commit("s", q_empty, end)
             at += nv
 
     def products_o():
@@ -301,11 +308,11 @@ def one_stream(b, items, nk, nv, slots, fixes_n, turns):
                 for i in range(nv):
                     yield "wait", *landed(v_full, vals, at)
                     end = b.product(128)
-                    b.commit(empty[at % slots], end)
+                    b.commit("o", empty[at % slots], end)
                     if i + 1 == nv:
-                        b.commit(pv_done[step & 1], end)
+                        b.commit("o", pv_done[step & 1], end)
                         if j + 1 == n:
-                            b.commit(o_full, end)
+                            b.commit("o", o_full, end)
                     at += 1
                     vals += 1
                 step += 1
@@ -352,7 +359,9 @@ def draw_two(r):
 def test_two_streams_come_to_their_end(nk, nv):
     for seed in range(300):
         items = draw_two(random.Random(seed))
-        assert two_streams(Block(seed), items, nk, nv, ring(nk, 2), constant("kTiles"), constant("kFixes")), (seed, items)
+        for start in ("count", "nothing"):
+            block = Block(seed)
+            assert two_streams(block, items, nk, nv, ring(nk, 2), constant("kTiles"), constant("kFixes"), start), (seed, items)
 
 
 @pytest.mark.parametrize("nk,nv", ONE)
@@ -364,17 +373,20 @@ def test_one_stream_comes_to_its_end(nk, nv):
 
 
 def test_the_model_sees_a_phase_that_is_missed():
-    """A start by the parity of the first stream's weights, two barriers of cleared rows, and a barrier for each
-    slot of a short ring are each overtaken or behind."""
+    """A start by the parity of the first stream's weights, tiles that a stream passes by, two barriers of cleared
+    rows, and a barrier for each slot of a short ring are each overtaken or behind."""
     def two(seed):
         return two_streams(Block(seed), [((2, 3), False)] * 3, 2, 2, ring(2, 2), 8, 4, "parity")
+
+    def skips(seed):
+        return two_streams(Block(seed), [((0, 4), False), ((1, 2), False)] * 4, 1, 1, ring(1, 2), 8, 4, skips=True)
 
     def fixes(seed):
         return one_stream(Block(seed), [(1, True)] * 8, 2, 1, ring(2, 1), 2, 16)
 
     def slots(seed):
         return one_stream(Block(seed), [(4, False)] * 3, 5, 4, ring(5, 1), 4, 0)
-    for order in (two, fixes, slots):
+    for order in (two, skips, fixes, slots):
         assert not all(order(s) for s in range(300)), order
 
 
@@ -386,6 +398,12 @@ def test_the_second_stream_starts_by_a_count():
 
 def test_slots_of_the_ring():
     """227 KB less the rest of a block's shared memory are 13 slots."""
-    shared = 8 * (constant("kSlots") + 2 * constant("kTurns") + constant("kFixes") + 2 * 9) + 4 * (3 + 512)  # barriers; flags and row maxima
+    barriers = constant("kSlots") + 2 * constant("kTurns") + constant("kFixes") + 2 * 9
+    shared = 8 * barriers + 4 * (3 + 512)  # and flags, and row maxima
     room = 227 * 1024 - 1024 - shared - 64
     assert room // 16384 == 13 and room - 13 * 16384 > 64
+
+
+def test_streams_see_every_tile():
+    """No stream gives a tile back for the other one."""
+    assert not re.search(r"if \(j >= other\)", source())
