@@ -765,7 +765,8 @@ typedef struct {
  * with strides in [0, 2^38) bytes.  May be captured in a CUDA graph.  The
  * queries, keys and values of a request are finite.  The rows of out are apart
  * (so are, a head at a time, those of q, k, k_rope and v); out and lse overlap no
- * input.
+ * input.  Waits inside the kernel are bounded (moe_dense_status): a request of up to
+ * 128 queries over more than some 10^8 keys, beside longer ones, can outlast them.
  * Errors: INVALID_ARG, SHAPE, CUDA.
  */
 int moe_latent_prompt(const MoePromptArgs *args, cudaStream_t stream);

@@ -2,8 +2,9 @@
 // elements (moe_quant_act_fp8):
 //   s = max(max |x| / 448, 1e-12),  code = E4M3(x / s), nearest, ties to even
 //
-// HBM bounds it: x in, a byte an element out; measured 8.2 us for 2048 x 6144 in 16 bits
-// (38 MB, 4.7 TB/s), half of the issue slots busy with the divisions.  A thread takes 16 elements (64 or
+// HBM is its floor: x in, a byte an element out.  Measured 9.3 us for 2048 x 6144 in 16 bits
+// (38 MB, 4.1 TB/s; 8.6 with x in L2): one load in flight a thread, then 16 divisions, which
+// take half of the issue slots; neither is full.  A thread takes 16 elements (64 or
 // 32 bytes in, 16 out), eight neighbouring lanes a group of 128, whose maximum
 // takes three shuffles.  The divisions are IEEE ones, so codes and scales equal
 // those of the formula bit for bit.

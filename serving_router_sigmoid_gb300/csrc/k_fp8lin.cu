@@ -12,8 +12,8 @@
 //  - Few tokens (up to 32): 128 matrix rows on the MMA's M side, the tokens (16 or
 //    32) on N.  The matrix streams once; HBM bounds it, and at the smallest the
 //    launch.  A stage is 18 or 20 KB, five or six of them let two blocks share an SM.
-//    Measured: 1 token, 6144 -> 2048 (12.6 MB) 6.1 us; 8 tokens, 2048 -> 12288 (25 MB)
-//    7.3 us.
+//    Measured: 1 token, 6144 -> 2048 (12.6 MB) 7.5 us (6.7 with the matrix in L2); 8
+//    tokens, 2048 -> 12288 (25 MB) 9.0 (7.4).
 //  - More: 128 tokens on M, 128 or 256 matrix rows on N: a thread's sums belong to
 //    one token, whose scale is one register, and the matrix scale is one number a
 //    block of 128 rows: one FMA an element.  Every accumulator is read from tensor

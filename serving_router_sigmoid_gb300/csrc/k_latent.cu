@@ -15,11 +15,12 @@
 //
 // Per tile of 64 tokens the tensor core works 36 x 32 + 16 x 48 = 1920 cycles (the
 // second product is bound by its operands' 128 bytes a cycle); HBM brings a tile in
-// 3300 cycles a SM (16-bit) or 1650 (E4M3).  Measured: a tile in 4100 (16-bit), since
+// 3300 cycles a SM (16-bit) or 1650 (E4M3) where each SM reads rows of its own, in half of
+// that where two groups of heads read them together.  Measured: a tile in 4100 (16-bit), since
 // two stages beside 72 KB of queries leave the chain load, S, softmax, O little to
 // overlap; 32-token tiles in four stages were slower (fixed costs an MMA and a
-// barrier).  64 requests of up to 16384 tokens, 128 heads: 120 us (2.3 TB/s of rows
-// read once from HBM and twice from L2); 2 of 131072 in E4M3, 64 heads: 82 us.
+// barrier).  64 requests of up to 16384 tokens, 128 heads: 121 us (2.3 TB/s of rows
+// read once from HBM and twice from L2); 2 of 131072 in E4M3, 64 heads: 83 us.
 // Prefetches to L2 two or three tiles ahead changed nothing (TMA) or cost 3 to 20%
 // (16-bit rows by prefetch instructions).
 //
@@ -35,7 +36,9 @@
 //   barriers: 139 against 136 us); four warps do the softmax and write the results.
 // - The maximum moves only when a logit passes it by 2^kLazy; then O is scaled in
 //   tensor memory.  Weights are rounded to the operand type (their sum is not), for
-//   f16 times 2^7, so that its subnormals begin at 2^-31 of the maximum.
+//   f16 times 2^7, so that its subnormals begin at 2^-31 of the maximum.  With bf16 the
+//   result is off by 0.0021 in the norm where its own rounding alone makes 0.0017; for a
+//   second term of the weights there is no room beside queries and stages.
 // - A request that several blocks share leaves its pieces (O, m, l) in the handle's
 //   workspace; a second small launch joins them in order, so results do not depend
 //   on timing.  Pieces lie as [8 heads][latent][8], so that 32 lanes write and read
@@ -78,7 +81,7 @@ struct Params {
     int runs;
     float factor;                     // scale * k_scale * log2(e)
     FastDiv by_page;
-    int box;                          // rows of a TMA box: the largest of 8 .. 64 that divides a page
+    int box;                          // rows of a TMA box: the largest power of two to 64 that divides a page; used from 32 on
     int out32;                        // rows of out start on 32 bytes
     int64_t c_page, c_tok;            // bytes
     uint32_t n_pages;
@@ -182,7 +185,7 @@ __device__ __forceinline__ bool soft_or(bool p) {
     return r != 0;
 }
 
-// How rows come: by TMA (pages of whole runs of 8 tokens; a request's last, ragged
+// How rows come: by TMA (pages of whole runs of 32 tokens; a request's last, ragged
 // tile row by row), row by row (any page size and stride), or as E4M3 codes.
 constexpr int kByRow = 0, kByTma = 1, kByCode = 2;
 

@@ -19,7 +19,10 @@
 // - A softmax thread holds a row (narrow) or half a row of logits in registers: no
 //   shuffles.  The maximum moves only when a logit passes it by 2^kLazy; then the
 //   row of O is scaled in tensor memory.  Weights are rounded to the operand type
-//   (their sum is not), for f16 times 2^7, so that its subnormals begin at 2^-31.
+//   (their sum is not), for f16 times 2^7, so that its subnormals begin at 2^-31.  The
+//   result is off by 0.0021 (bf16) in the norm where its own rounding alone makes 0.0016;
+//   a second term of the weights was measured: 0.0016, but 104 us for 91 (2048 tokens) and
+//   183 for 157 (wide).
 // - One warp brings tiles by TMA into a ring of 16 KB slots, several lanes at once: 128
 //   keys by 64 dimensions, or as many rows of V as fit; tiles are handed on in halves
 //   (narrow) or slots (wide).  What lies outside a tensor reads as
@@ -29,8 +32,8 @@
 //   in turn and back, a request's last queries first: the longest come first where
 //   the mask is causal.
 //
-// Measured: 2048 tokens, 64 heads of 128 + 64 / 128, causal: 92 us, 0.94 PFLOP/s; 1000
-// queries over 5000 keys, 32 heads of 192 + 64 / 256: 156 us, 0.94.  What bounds it is the
+// Measured: 2048 tokens, 64 heads of 128 + 64 / 128, causal: 91 us, 0.95 PFLOP/s (95 us where
+// nothing is in L2); 1000 queries over 5000 keys, 32 heads of 192 + 64 / 256: 159 us, 0.93.  What bounds it is the
 // chain of a step: some 300 to 440 cycles from a product's end to whoever waits for it, twice, and
 // the softmax between (two steps of both streams 4560 cycles, their MMAs 2560).
 #include <type_traits>
@@ -100,7 +103,7 @@ struct Cursor {
     __device__ __forceinline__ bool item(const Params &p, int it, Item &x) {
         const MoePromptArgs &a = p.a;
         constexpr int kRows = 128 * NQ;
-        const int G = gridDim.x, c = blockIdx.x, lane = threadIdx.x & 31;  // wide: pairs of blocks
+        const int G = gridDim.x, c = blockIdx.x, lane = threadIdx.x & 31;
         const long long idx = (long long)it * G + (it & 1 ? G - 1 - c : c);
         const long long unit = idx / a.n_heads;
         x.head = (int)(idx - unit * a.n_heads);
